@@ -32,6 +32,8 @@
  *         4-bit codes (8-135: byte 8+16ib+j holds weight j of sub-block ib in
  *         its low nibble and weight j+16 in its high nibble, the IQ4_NL order
  *         of that page's encode). Weight = table[q] * d*(s-32), table [16].
+ *   MXFP4 (OCP Microscaling Formats v1.0) and the 8-bit key/value cache keep
+ *         codes and power-of-two scales apart: see their calls below.
  *
  * Common conventions
  *   - Every pointer argument except `stream` is a DEVICE pointer (HIP memory
@@ -96,6 +98,7 @@ extern "C" {
 #define QWG_ERR_CAPTURE 7  /* the stream is capturing and a call would have to allocate */
 #define QWG_ERR_TIMEOUT 8  /* a wait of a layer-chain launch gave up (qwg_chain_status) */
 #define QWG_ERR_GRID 9     /* a codebook value is not exactly representable in fp16 */
+#define QWG_ERR_TYPE 10    /* unknown element type (QWG_F32, QWG_F16, QWG_BF16) */
 
 /* format ids */
 #define QWG_FMT_Q4K 0
@@ -113,6 +116,13 @@ extern "C" {
 #define QWG_MAX_N_OUT (1 << 24)
 #define QWG_MAX_BATCH 8
 #define QWG_MAX_GROUP 65536         /* GEMVs per grouped launch */
+
+/* element types of the MXFP4 and cache calls' activations and results */
+#define QWG_F32 0
+#define QWG_F16 1
+#define QWG_BF16 2
+#define QWG_MX_BLOCK 32             /* values per MXFP4 scale */
+#define QWG_MX_MAX_BATCH 16         /* rows of qwg_gemm_mxfp4 */
 
 /* Library version (major*10000 + minor*100 + patch). */
 int qwg_version(void);
@@ -529,6 +539,116 @@ int qwg_chain_status(qwg_chain *chain);
 int qwg_chain_phases(const qwg_chain *chain);
 int qwg_chain_tagged(const qwg_chain *chain);
 int qwg_chain_destroy(qwg_chain *chain);
+
+/*
+ * MXFP4 (OCP Microscaling Formats v1.0): E2M1 codes (0, 1/2, 1, 3/2, 2, 3, 4, 6
+ * and a sign bit), two to a byte, the first in the low nibble, and one E8M0 byte
+ * e per 32 consecutive values of a row, scale 2^(e-127); e = 255 is NaN. A matrix
+ * [n_rows, n_in] is two arrays, rows contiguous: codes [n_rows][n_in/2] (16-byte
+ * aligned) and scales [n_rows][n_in/32] (any alignment). n_in is a multiple of
+ * 32 in [32, QWG_MAX_N_IN]; 1 <= n_rows, n_out <= QWG_MAX_N_OUT. `type` is the
+ * element type (QWG_F32, QWG_F16, QWG_BF16) of activations and results. None of
+ * these calls allocates or keeps anything, so all may be captured into a graph.
+ *
+ * qwg_encode_mxfp4: x [n_rows][n_in], rows x_stride elements apart (x_stride >=
+ * n_in; x aligned to its type), -> codes and scales. Per block e = max(E - 2,
+ * 0) with E the biased fp32 exponent of its largest magnitude; a code is
+ * v / 2^(e-127) rounded to nearest even and saturated at 6. A block that holds a
+ * NaN or an infinity gets e = 255 and zero codes.
+ * qwg_dequant_mxfp4: n values (a multiple of 32) in block order -> dst (16-byte
+ * aligned) of `type`: code times scale, exact in fp32 and rounded once for the
+ * 16-bit types.
+ *
+ * qwg_gemm_mxfp4: Y[b, r] = sum_k W[r, k] X[b, k], 1 <= batch <=
+ * QWG_MX_MAX_BATCH; x [batch][n_in] (16-byte aligned) and y [batch][n_out] of
+ * `type`. qwg_gemv_mxfp4 is batch 1. Activations keep all their bits; sums are
+ * fp32 in an order fixed by the sizes: |y - exact| <= 2e-6 sum_k |W X| before the
+ * one rounding to `type`, for inputs whose weights lie below 2^126 (larger ones
+ * overflow to infinity). A NaN scale makes its row NaN.
+ *
+ * qwg_matmul_mxfp4: C[m, r] = sum_k A[m, k] W[r, k], A [n_rows, n_in] and W
+ * [n_out, n_in] both MXFP4, c [n_rows][n_out] of `type`; the same bound.
+ */
+int qwg_encode_mxfp4(void *codes, void *scales, const void *x, int type, int64_t n_rows,
+                     int64_t n_in, int64_t x_stride, void *stream);
+int qwg_dequant_mxfp4(const void *codes, const void *scales, void *dst, int type, int64_t n,
+                      void *stream);
+int qwg_gemv_mxfp4(void *y, const void *x, int type, const void *codes, const void *scales,
+                   int64_t n_in, int64_t n_out, void *stream);
+int qwg_gemm_mxfp4(void *y, const void *x, int type, const void *codes, const void *scales,
+                   int64_t n_in, int64_t n_out, int batch, void *stream);
+int qwg_matmul_mxfp4(void *c, int type, const void *a_codes, const void *a_scales,
+                     const void *w_codes, const void *w_scales, int64_t n_rows, int64_t n_in,
+                     int64_t n_out, void *stream);
+
+/*
+ * A key/value cache in 8 bits (what a decode step reads between its q|k|v and o
+ * products). A page holds page_tokens consecutive positions of one sequence:
+ * k_pages [n_pages][n_kv_heads][page_tokens][head_dim] and, transposed, v_pages
+ * [n_pages][n_kv_heads][head_dim][page_tokens] of e4m3 codes, with one E8M0 scale
+ * 2^(e-127) per page and head in k_scales and v_scales [n_pages][n_kv_heads].
+ * head_dim is 64, 96, 128, 192 or 256; page_tokens 16, 32, 64 or 128; the pages
+ * are 16-byte aligned. `table` [n_seqs][table_width] holds each sequence's pages
+ * in order (page p: positions p*page_tokens ..), `lens` [n_seqs] its positions;
+ * both int32 in device memory. Entries past a sequence's positions are not read.
+ * 1 <= n_seqs <= 65535.
+ *
+ * qwg_kv8_append: k and v [n_tokens][n_kv_heads][head_dim] of `type` (heads
+ * contiguous, tokens k_stride and v_stride elements apart, so slices of one
+ * fused q|k|v result may be given). Sequence s appends tokens starts[s] ..
+ * starts[s+1]-1 (int32 [n_seqs+1], device; tokens past starts[n_seqs] are left
+ * out) at positions lens[s] on, lens being the positions held BEFORE the call;
+ * starts NULL: n_tokens / n_seqs tokens each. The caller advances lens. A page's
+ * exponent is the smallest with every magnitude / 2^(e-127) <= 448 (0 at
+ * least), and never falls while the page fills: it is the larger of the stored
+ * one (where the page holds earlier positions of this sequence) and that of the
+ * new tokens; when it rises, the page's earlier codes are rounded to it. NaN and infinities
+ * become NaN codes and do not count for the exponent. Slots past the new tokens
+ * are left as they were. max_new (>= 1) is the number of tokens that a sequence
+ * appends at most, if known, or n_tokens: it sizes the launch only. A page that
+ * is written must belong to one sequence (shared pages have to be full). A token
+ * whose position lies past the table, or whose table entry is no page of the
+ * pool, is not written.
+ *
+ * qwg_kv8_attend: out[s, t, h] = sum_j softmax_j(scale q[s, t, h] . K[j]) V[j]
+ * over the positions j that token t of sequence s sees: its own is lens[s] -
+ * q_len + t (lens counting the queries' own tokens, appended before), and j runs
+ * up to it, or over the last `window` of those (0: all). q [n_seqs * q_len]
+ * [n_heads][head_dim], tokens q_stride elements apart, out contiguous, both of
+ * `type`; n_heads is a multiple of n_kv_heads, head h reading key/value head
+ * h / (n_heads / n_kv_heads); n_heads * q_len <= 65535. A row that sees nothing
+ * is zero. What masked positions and slots past lens hold (NaN codes too) has no
+ * effect. A row that sees a position whose table entry is no page of the pool,
+ * and every row of a sequence whose length is negative or past its table, is NaN.
+ * Products are exact in fp32 sums, the softmax is fp32; probabilities keep all
+ * their bits for fp32 and 16 for the 16-bit types.
+ * max_len is the largest length, if known, or 0: it shapes the split only. The
+ * positions are split over workgroups where there are few rows; the parts then
+ * meet in `workspace` (device, 16-byte aligned, qwg_kv8_attend_workspace bytes
+ * for the same arguments, which may be 0; or a negative status), which is the
+ * caller's: calls that may overlap in time need one each.
+ */
+typedef struct qwg_kv8 {
+    void *k_pages;
+    void *v_pages;
+    uint8_t *k_scales;
+    uint8_t *v_scales;
+    int64_t n_pages;
+    int n_kv_heads;
+    int head_dim;
+    int page_tokens;
+} qwg_kv8;
+
+int qwg_kv8_append(const qwg_kv8 *cache, const void *k, const void *v, int type, int64_t k_stride,
+                   int64_t v_stride, int64_t n_tokens, const int32_t *starts,
+                   const int32_t *table, int64_t table_width, const int32_t *lens, int64_t n_seqs,
+                   int64_t max_new, void *stream);
+int64_t qwg_kv8_attend_workspace(const qwg_kv8 *cache, int64_t table_width, int64_t n_seqs,
+                                 int q_len, int n_heads, int64_t max_len);
+int qwg_kv8_attend(const qwg_kv8 *cache, void *out, const void *q, int type, int64_t q_stride,
+                   const int32_t *table, int64_t table_width, const int32_t *lens, int64_t n_seqs,
+                   int q_len, int n_heads, float scale, int64_t window, int64_t max_len,
+                   void *workspace, int64_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,4 +1,5 @@
-"""qwg: fused dequantize + GEMV over block-quantized weights (Q4_K, IQ3) for MI355X.
+"""qwg: fused dequantize + GEMV over block-quantized weights (Q4_K, IQ3, MXFP4) and an 8-bit
+key/value cache for MI355X.
 
 The compute path is the HIP library ``libqwg.so`` (C ABI in ``include/qwg.h``);
 this package only marshals torch tensors into its calls. Importing the package
@@ -12,6 +13,8 @@ from ._binding import (Group, Iq3Group, Q4kChain, Iq3sGroup, Iq4xsGroup, MAX_BAT
                        pack_iq3_tiles, pack_iq3_xxs_tiles, pack_iq3s_tiles, pack_iq4xs_tiles,
                        pack_q4k_tiles, plan_splits, row_bytes, tiled_bytes, workspace_release,
                        workspace_reserve)
+from ._mx import (KV8_HEAD_DIMS, KV8_PAGE_TOKENS, MX_BLOCK, MX_MAX_BATCH, dequant_mxfp4, encode_mxfp4,
+                  gemm_mxfp4, gemv_mxfp4, kv8_append, kv8_attend, kv8_pages, matmul_mxfp4)
 
 __all__ = ["Group", "Iq3Group", "Q4kChain", "Iq3sGroup", "Iq4xsGroup", "MAX_BATCH", "Q4kBatchedGroup", "Q4kGroup", "QWG_FMT_IQ3",
            "QWG_FMT_IQ3_S", "QWG_FMT_IQ3_XXS", "QWG_FMT_IQ4_XS", "QWG_FMT_Q4K", "QwgError",
@@ -20,4 +23,6 @@ __all__ = ["Group", "Iq3Group", "Q4kChain", "Iq3sGroup", "Iq4xsGroup", "MAX_BATC
            "gemv_iq3s", "gemv_iq3s_tiled", "gemv_iq4xs", "gemv_iq4xs_tiled", "gemv_q4k", "gemv_q4k_tiled", "lib",
            "pack_iq3_tiles", "pack_iq3_xxs_tiles", "pack_iq3s_tiles", "pack_iq4xs_tiles",
            "pack_q4k_tiles", "plan_splits", "row_bytes", "tiled_bytes", "workspace_release",
-           "workspace_reserve"]
+           "workspace_reserve",
+           "KV8_HEAD_DIMS", "KV8_PAGE_TOKENS", "MX_BLOCK", "MX_MAX_BATCH", "dequant_mxfp4", "encode_mxfp4",
+           "gemm_mxfp4", "gemv_mxfp4", "kv8_append", "kv8_attend", "kv8_pages", "matmul_mxfp4"]

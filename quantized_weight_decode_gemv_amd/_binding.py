@@ -104,6 +104,19 @@ def lib() -> ctypes.CDLL:
                   "qwg_chain_create_q4k", "qwg_chain_run", "qwg_chain_status", "qwg_chain_phases",
                   "qwg_chain_destroy"):
             getattr(L, f).restype = I
+        L.qwg_encode_mxfp4.argtypes = [P, P, P, I, I64, I64, I64, P]
+        L.qwg_dequant_mxfp4.argtypes = [P, P, P, I, I64, P]
+        L.qwg_gemv_mxfp4.argtypes = [P, P, I, P, P, I64, I64, P]
+        L.qwg_gemm_mxfp4.argtypes = [P, P, I, P, P, I64, I64, I, P]
+        L.qwg_matmul_mxfp4.argtypes = [P, I, P, P, P, P, I64, I64, I64, P]
+        L.qwg_kv8_append.argtypes = [P, P, P, I, I64, I64, I64, P, P, I64, P, I64, I64, P]
+        L.qwg_kv8_attend_workspace.argtypes = [P, I64, I64, I, I, I64]
+        L.qwg_kv8_attend.argtypes = [P, P, P, I, I64, P, I64, P, I64, I, I, ctypes.c_float, I64, I64,
+                                     P, I64, P]
+        for f in ("qwg_encode_mxfp4", "qwg_dequant_mxfp4", "qwg_gemv_mxfp4", "qwg_gemm_mxfp4",
+                  "qwg_matmul_mxfp4", "qwg_kv8_append", "qwg_kv8_attend"):
+            getattr(L, f).restype = I
+        L.qwg_kv8_attend_workspace.restype = I64
         _lib = L
     return _lib
 

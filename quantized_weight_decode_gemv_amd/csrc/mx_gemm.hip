@@ -1,0 +1,202 @@
+// Y = X W^T for MXFP4 weights and 1..16 rows of fp32, fp16 or bf16 activations
+// (decoding: the weights are the traffic).
+//
+// Every weight is exact in bf16 (two significand bits and a power of two), and
+// an activation is the exact sum of one (bf16), two (fp16) or three (fp32) bf16
+// parts. The matrix cores multiply the weights by the parts, one part of one
+// activation row per column of the tile, and accumulate in fp32; a row's parts
+// are added at the end. So a batch-1 fp32 product uses 3 of the 16 columns at no
+// cost: a 16 x 512 piece of W takes 16 v_mfma_f32_16x16x32_bf16 (256 cycles)
+// and 64 conversions either way, and HBM delivers its 4.3 KB to a SIMD no
+// faster.
+//
+// A workgroup holds WR row tiles of 16 rows times WK wavefronts that share each
+// tile's sum over n_in. Lane l of a wavefront takes row l % 16 and, of each 16
+// blocks of 32 weights, blocks 4(l / 16) .. +3: 64 consecutive bytes of codes
+// and one 32-bit word of scales. The order of the products within the sum is
+// free as long as the activations follow it.
+#include "mx_device.h"
+
+namespace qwg {
+
+namespace {
+
+constexpr int kStepBlocks = 16;                       // blocks of a row per wavefront step
+constexpr int kStep = kStepBlocks * kMxBlock;         // 512 weights
+constexpr int kLdsX = 96 * 1024;                      // staged activation parts, at most
+
+struct Codes {
+    u32x4 c[4];
+    uint32_t s;  // four E8M0 bytes
+};
+
+// A lane's 4 blocks from block `b` on; blocks from `nblk` on read as zero with scale 1.
+template <bool WORDS>
+__device__ __forceinline__ void load_codes(Codes &o, const uint8_t *codes, const uint8_t *scales,
+                                           int b, int nblk) {
+    if (WORDS && b + 4 <= nblk) {
+        const u32x4 *p = (const u32x4 *)(codes + (int64_t)b * kMxCodeBytes);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o.c[q] = p[q];
+        o.s = *(const uint32_t *)(scales + b);
+        return;
+    }
+    o.s = 0x7f7f7f7fu;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        o.c[q] = u32x4{0, 0, 0, 0};
+        if (b + q < nblk) {
+            o.c[q] = *(const u32x4 *)(codes + (int64_t)(b + q) * kMxCodeBytes);
+            o.s = (o.s & ~(255u << (8 * q))) | (uint32_t)scales[b + q] << (8 * q);
+        }
+    }
+}
+
+// Eight weights (one 32-bit word of codes) as bf16, scaled.
+__device__ __forceinline__ bf16x8 decode8(uint32_t c, float s) {
+    const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0);
+    const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1);
+    const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2);
+    const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3);
+    return bf16x8{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
+}
+
+// LDS pitch in bytes of one activation part of `len` values: 16 bytes past a
+// multiple of 1024, so that 16 columns' reads at one position meet no bank twice.
+__device__ __host__ __forceinline__ int pitch_of(int len) { return len * 2 + 16; }
+
+template <int TYPE, int NT, bool WORDS>
+__global__ __launch_bounds__(1024) void mxfp4_gemm_kernel(MxGemmArgs a, int wk, int chunk) {
+    typedef typename Elem<TYPE>::T T;
+    constexpr int P = Elem<TYPE>::pieces;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int waves = blockDim.x >> 6, wr = waves / wk;
+    const int kw = wave % wk, rw = wave / wk;
+    const int n = lane & 15, g = lane >> 4;
+    const int nblk = a.n_in / kMxBlock;
+    const int64_t row0 = ((int64_t)blockIdx.x * wr + rw) * 16;
+    // rows past the last one read the last one; they are not stored
+    const int64_t row = min(row0 + n, (int64_t)a.n_out - 1);
+    const uint8_t *codes = a.codes + row * nblk * kMxCodeBytes;
+    const uint8_t *scales = a.scales + row * nblk;
+    const int cols = a.batch * P;
+    const int pitch = pitch_of(chunk);
+    f32x4 acc[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] = f32x4{0, 0, 0, 0};
+    // a column past the last part reads some part; its sums are not used
+    int col[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) col[t] = min(t * 16 + n, cols - 1) * pitch;
+
+    for (int k0 = 0; k0 < a.n_in; k0 += chunk) {
+        const int len = min(chunk, a.n_in - k0);
+        const int steps = (len + kStep - 1) / kStep;
+        int st = kw;
+        Codes cur;
+        if (st < steps) load_codes<WORDS>(cur, codes, scales, k0 / kMxBlock + st * kStepBlocks + g * 4, nblk);
+        if (k0) __syncthreads();
+        // the parts of every activation row, eight values a turn, zero past n_in
+        const int units = steps * (kStep / 8);
+        for (int i = threadIdx.x; i < units * a.batch; i += blockDim.x) {
+            const int b = i / units, u = i - b * units;
+            float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (u * 8 < len) load8<T, true>((const T *)a.x + (int64_t)b * a.n_in + k0 + u * 8, v);
+            uint32_t w[3][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t h0, m0, l0, h1, m1, l1;
+                split3(v[2 * j], h0, m0, l0);
+                split3(v[2 * j + 1], h1, m1, l1);
+                w[0][j] = h0 | h1 << 16, w[1][j] = m0 | m1 << 16, w[2][j] = l0 | l1 << 16;
+            }
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                *(u32x4 *)(lds + (b * P + p) * pitch + u * 16) = u32x4{w[p][0], w[p][1], w[p][2], w[p][3]};
+        }
+        __syncthreads();
+        for (; st < steps; st += wk) {
+            Codes next = cur;
+            if (st + wk < steps)
+                load_codes<WORDS>(next, codes, scales,
+                                  k0 / kMxBlock + (st + wk) * kStepBlocks + g * 4, nblk);
+            const int at = (st * kStepBlocks + g * 4) * kMxBlock * 2;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float s = e8m0((cur.s >> (8 * q)) & 255);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bf16x8 w = decode8(cur.c[q][j], s);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const bf16x8 x = *(const bf16x8 *)(lds + col[t] + at + q * 64 + j * 16);
+                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, acc[t], 0, 0, 0);
+                    }
+                }
+            }
+            cur = next;
+        }
+    }
+    // every wavefront's 16 x 16 NT sums meet in LDS: [wave][column][row]
+    __syncthreads();
+    float *sums = (float *)lds;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+        *(f32x4 *)(sums + ((wave * NT + t) * 16 + n) * 16 + g * 4) = acc[t];
+    __syncthreads();
+    for (int i = threadIdx.x; i < wr * 16 * a.batch; i += blockDim.x) {
+        const int r = i & 15, w = (i >> 4) % wr, b = (i >> 4) / wr;
+        const int64_t out = ((int64_t)blockIdx.x * wr + w) * 16 + r;
+        if (out >= a.n_out) continue;
+        float y = 0;
+        // the small parts first
+#pragma unroll
+        for (int p = P - 1; p >= 0; --p) {
+            float s = 0;
+            for (int k = 0; k < wk; ++k) s += sums[((w * wk + k) * NT * 16 + b * P + p) * 16 + r];
+            y += s;
+        }
+        ((T *)a.y)[(int64_t)b * a.n_out + out] = (T)y;
+    }
+}
+
+template <int TYPE, int NT>
+hipError_t launch(const MxGemmArgs &a, hipStream_t s) {
+    constexpr int P = Elem<TYPE>::pieces;
+    const int64_t tiles = ((int64_t)a.n_out + 15) / 16;
+    const int steps = (a.n_in + kStep - 1) / kStep;
+    // the wavefronts of a tile: enough for about eight per compute unit
+    int wk = 1;
+    while (wk < 16 && wk < steps && tiles * wk < 2048) wk *= 2;
+    const int wr = wk < 4 ? 4 / wk : 1;
+    int chunk = kLdsX / (a.batch * P) / 2 / kStep * kStep;
+    if (chunk > steps * kStep) chunk = steps * kStep;
+    size_t lds = (size_t)a.batch * P * pitch_of(chunk);
+    const size_t join = (size_t)wk * wr * NT * 16 * 16 * 4;
+    if (lds < join) lds = join;
+    const unsigned grid = (unsigned)((tiles + wr - 1) / wr);
+    const bool words = a.n_in % (4 * kMxBlock) == 0 && (uintptr_t)a.scales % 4 == 0;
+    if (words)
+        mxfp4_gemm_kernel<TYPE, NT, true><<<grid, wk * wr * 64, lds, s>>>(a, wk, chunk);
+    else
+        mxfp4_gemm_kernel<TYPE, NT, false><<<grid, wk * wr * 64, lds, s>>>(a, wk, chunk);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mxfp4_gemm(const MxGemmArgs &a, int type, hipStream_t s) {
+    if (type == kF32) {
+        if (a.batch * 3 <= 16) return launch<kF32, 1>(a, s);
+        if (a.batch * 3 <= 32) return launch<kF32, 2>(a, s);
+        return launch<kF32, 3>(a, s);
+    }
+    if (type == kF16) {
+        if (a.batch * 2 <= 16) return launch<kF16, 1>(a, s);
+        return launch<kF16, 2>(a, s);
+    }
+    return launch<kBF16, 1>(a, s);
+}
+
+}  // namespace qwg

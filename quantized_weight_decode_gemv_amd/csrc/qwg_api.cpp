@@ -427,9 +427,11 @@ const char *qwg_strerror(int status) {
     switch (status) {
         case QWG_OK: return "ok";
         case QWG_ERR_NULL: return "a required pointer is NULL";
-        case QWG_ERR_SHAPE: return "invalid size (n_in must be a multiple of 256 in [256, 65536]; n, n_out >= 1)";
+        case QWG_ERR_SHAPE:
+            return "invalid size (n_in must be a multiple of 256 in [256, 65536], of 32 for MXFP4; "
+                   "n, n_out >= 1; for the cache calls see qwg.h)";
         case QWG_ERR_ALIGN: return "a pointer is not aligned as the call requires";
-        case QWG_ERR_BATCH: return "batch must be in 1..8";
+        case QWG_ERR_BATCH: return "batch must be in 1..8 (1..16 for MXFP4)";
         case QWG_ERR_HIP: return "HIP runtime error";
         case QWG_ERR_FORMAT: return "unknown format id";
         case QWG_ERR_GRID:
@@ -437,6 +439,7 @@ const char *qwg_strerror(int status) {
                    "codebook in fp16)";
         case QWG_ERR_TIMEOUT:
             return "a wait of the layer-chain launch gave up (its flags have been reset)";
+        case QWG_ERR_TYPE: return "unknown element type (QWG_F32, QWG_F16 or QWG_BF16)";
         case QWG_ERR_CAPTURE:
             return "the stream is being captured and has no split-sum workspace yet "
                    "(qwg_workspace_reserve it before capture, or call qwg_gemm_q4k_noalloc)";
