@@ -42,7 +42,7 @@ __global__ __launch_bounds__(256) void mxfp4_encode_kernel(uint8_t *codes, uint8
         c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], scale, 1);
         c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], scale, 2);
         c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], scale, 3);
-        ((uint32_t *)codes)[u] = none ? 0 : c;
+        __builtin_nontemporal_store(none ? 0 : c, (uint32_t *)codes + u);
         if ((u & 3) == 0) scales[u >> 2] = (uint8_t)s;
     }
 }
@@ -69,7 +69,7 @@ __global__ __launch_bounds__(256) void mxfp4_dequant_kernel(const uint32_t *code
         t8 o;
         o[0] = (T)(p0.x * s), o[1] = (T)(p0.y * s), o[2] = (T)(p1.x * s), o[3] = (T)(p1.y * s);
         o[4] = (T)(p2.x * s), o[5] = (T)(p2.y * s), o[6] = (T)(p3.x * s), o[7] = (T)(p3.y * s);
-        ((t8 *)dst)[u] = o;
+        __builtin_nontemporal_store(o, (t8 *)dst + u);
     }
 }
 

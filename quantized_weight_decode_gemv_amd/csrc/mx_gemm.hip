@@ -10,11 +10,13 @@
 // and 64 conversions either way, and HBM delivers its 4.3 KB to a SIMD no
 // faster.
 //
-// A workgroup holds WR row tiles of 16 rows times WK wavefronts that share each
-// tile's sum over n_in. Lane l of a wavefront takes row l % 16 and, of each 16
+// A workgroup's wavefronts are wr x wk: wr groups of RT row tiles of 16 rows, wk
+// wavefronts sharing each group's sum over n_in. Lane l of a wavefront takes row l % 16 and, of each 16
 // blocks of 32 weights, blocks 4(l / 16) .. +3: 64 consecutive bytes of codes
 // and one 32-bit word of scales. The order of the products within the sum is
 // free as long as the activations follow it.
+#include <algorithm>
+
 #include "mx_device.h"
 
 namespace qwg {
@@ -23,7 +25,11 @@ namespace {
 
 constexpr int kStepBlocks = 16;                       // blocks of a row per wavefront step
 constexpr int kStep = kStepBlocks * kMxBlock;         // 512 weights
-constexpr int kLdsX = 96 * 1024;                      // staged activation parts, at most
+constexpr int kLdsX = 128 * 1024;                     // staged activation parts, at most
+
+// Wavefronts of a workgroup at most: two row tiles' codes, twice (the next
+// step's too), need more than the 128 registers that 16 wavefronts leave.
+constexpr int kMaxWaves(int rt) { return rt == 1 ? 16 : 8; }
 
 struct Codes {
     u32x4 c[4];
@@ -65,26 +71,53 @@ __device__ __forceinline__ bf16x8 decode8(uint32_t c, float s) {
 // multiple of 1024, so that 16 columns' reads at one position meet no bank twice.
 __device__ __host__ __forceinline__ int pitch_of(int len) { return len * 2 + 16; }
 
-template <int TYPE, int NT, bool WORDS>
-__global__ __launch_bounds__(1024) void mxfp4_gemm_kernel(MxGemmArgs a, int wk, int chunk) {
+template <int TYPE>
+__device__ __forceinline__ void stage_parts(uint8_t *lds, int pitch, int row, int unit,
+                                            const float (&v)[8]) {
+    constexpr int P = Elem<TYPE>::pieces;
+    uint32_t w[3][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t h0, m0, l0, h1, m1, l1;
+        split3(v[2 * j], h0, m0, l0);
+        split3(v[2 * j + 1], h1, m1, l1);
+        w[0][j] = h0 | h1 << 16, w[1][j] = m0 | m1 << 16, w[2][j] = l0 | l1 << 16;
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+        *(u32x4 *)(lds + (row * P + p) * pitch + unit * 16) =
+            u32x4{w[p][0], w[p][1], w[p][2], w[p][3]};
+}
+
+// RT: row tiles that a wavefront takes together (one read of the activations
+// for both); NT: 16-column tiles of activation parts.
+template <int TYPE, int NT, int RT, bool WORDS>
+__global__ __launch_bounds__(kMaxWaves(RT) * 64) void mxfp4_gemm_kernel(MxGemmArgs a, int wk, int chunk) {
     typedef typename Elem<TYPE>::T T;
     constexpr int P = Elem<TYPE>::pieces;
+    constexpr int kAhead = 2;  // activation units a thread loads before the first weights
     extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int waves = blockDim.x >> 6, wr = waves / wk;
     const int kw = wave % wk, rw = wave / wk;
     const int n = lane & 15, g = lane >> 4;
     const int nblk = a.n_in / kMxBlock;
-    const int64_t row0 = ((int64_t)blockIdx.x * wr + rw) * 16;
-    // rows past the last one read the last one; they are not stored
-    const int64_t row = min(row0 + n, (int64_t)a.n_out - 1);
-    const uint8_t *codes = a.codes + row * nblk * kMxCodeBytes;
-    const uint8_t *scales = a.scales + row * nblk;
+    const uint8_t *codes[RT], *scales[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        // rows past the last one read the last one; they are not stored
+        const int64_t row =
+            min((((int64_t)blockIdx.x * wr + rw) * RT + r) * 16 + n, (int64_t)a.n_out - 1);
+        codes[r] = a.codes + row * nblk * kMxCodeBytes;
+        scales[r] = a.scales + row * nblk;
+    }
     const int cols = a.batch * P;
     const int pitch = pitch_of(chunk);
-    f32x4 acc[NT];
+    f32x4 acc[RT][NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t] = f32x4{0, 0, 0, 0};
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[r][t] = f32x4{0, 0, 0, 0};
     // a column past the last part reads some part; its sums are not used
     int col[NT];
 #pragma unroll
@@ -93,95 +126,129 @@ __global__ __launch_bounds__(1024) void mxfp4_gemm_kernel(MxGemmArgs a, int wk, 
     for (int k0 = 0; k0 < a.n_in; k0 += chunk) {
         const int len = min(chunk, a.n_in - k0);
         const int steps = (len + kStep - 1) / kStep;
-        int st = kw;
-        Codes cur;
-        if (st < steps) load_codes<WORDS>(cur, codes, scales, k0 / kMxBlock + st * kStepBlocks + g * 4, nblk);
-        if (k0) __syncthreads();
-        // the parts of every activation row, eight values a turn, zero past n_in
-        const int units = steps * (kStep / 8);
-        for (int i = threadIdx.x; i < units * a.batch; i += blockDim.x) {
+        const int units = steps * (kStep / 8), all = units * a.batch;
+        // The parts of every activation row, eight values a turn, zero past n_in.
+        // The first of them are asked for before the first weights, which take
+        // longer to come.
+        float v[kAhead][8];
+        auto fetch = [&](int i, float(&o)[8]) {
             const int b = i / units, u = i - b * units;
-            float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (u * 8 < len) load8<T, true>((const T *)a.x + (int64_t)b * a.n_in + k0 + u * 8, v);
-            uint32_t w[3][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t h0, m0, l0, h1, m1, l1;
-                split3(v[2 * j], h0, m0, l0);
-                split3(v[2 * j + 1], h1, m1, l1);
-                w[0][j] = h0 | h1 << 16, w[1][j] = m0 | m1 << 16, w[2][j] = l0 | l1 << 16;
-            }
+            for (int e = 0; e < 8; ++e) o[e] = 0;
+            if (i < all && u * 8 < len)
+                load8<T, true>((const T *)a.x + (int64_t)b * a.n_in + k0 + u * 8, o);
+        };
 #pragma unroll
-            for (int p = 0; p < P; ++p)
-                *(u32x4 *)(lds + (b * P + p) * pitch + u * 16) = u32x4{w[p][0], w[p][1], w[p][2], w[p][3]};
+        for (int h = 0; h < kAhead; ++h) fetch(threadIdx.x + h * blockDim.x, v[h]);
+        int st = kw;
+        Codes cur[RT];
+        auto load = [&](Codes(&c)[RT], int s) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+                load_codes<WORDS>(c[r], codes[r], scales[r],
+                                  k0 / kMxBlock + s * kStepBlocks + g * 4, nblk);
+        };
+        if (st < steps) load(cur, st);
+        if (k0) __syncthreads();
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h) {
+            const int i = threadIdx.x + h * blockDim.x;
+            if (i < all) stage_parts<TYPE>(lds, pitch, i / units, i % units, v[h]);
+        }
+        for (int i = threadIdx.x + kAhead * blockDim.x; i < all; i += blockDim.x) {
+            fetch(i, v[0]);
+            stage_parts<TYPE>(lds, pitch, i / units, i % units, v[0]);
         }
         __syncthreads();
         for (; st < steps; st += wk) {
-            Codes next = cur;
-            if (st + wk < steps)
-                load_codes<WORDS>(next, codes, scales,
-                                  k0 / kMxBlock + (st + wk) * kStepBlocks + g * 4, nblk);
+            Codes next[RT];
+            if (st + wk < steps) load(next, st + wk);
             const int at = (st * kStepBlocks + g * 4) * kMxBlock * 2;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const float s = e8m0((cur.s >> (8 * q)) & 255);
+                float s[RT];
+#pragma unroll
+                for (int r = 0; r < RT; ++r) s[r] = e8m0((cur[r].s >> (8 * q)) & 255);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const bf16x8 w = decode8(cur.c[q][j], s);
+                    bf16x8 w[RT];
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) w[r] = decode8(cur[r].c[q][j], s[r]);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         const bf16x8 x = *(const bf16x8 *)(lds + col[t] + at + q * 64 + j * 16);
-                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, acc[t], 0, 0, 0);
+#pragma unroll
+                        for (int r = 0; r < RT; ++r)
+                            acc[r][t] =
+                                __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[r], x, acc[r][t], 0, 0, 0);
                     }
                 }
             }
-            cur = next;
+#pragma unroll
+            for (int r = 0; r < RT; ++r) cur[r] = next[r];
         }
     }
-    // every wavefront's 16 x 16 NT sums meet in LDS: [wave][column][row]
+    // every wavefront's sums meet in LDS: [wave][row tile][column][row]
     __syncthreads();
     float *sums = (float *)lds;
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-        *(f32x4 *)(sums + ((wave * NT + t) * 16 + n) * 16 + g * 4) = acc[t];
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            *(f32x4 *)(sums + (((wave * RT + r) * NT + t) * 16 + n) * 16 + g * 4) = acc[r][t];
     __syncthreads();
-    for (int i = threadIdx.x; i < wr * 16 * a.batch; i += blockDim.x) {
-        const int r = i & 15, w = (i >> 4) % wr, b = (i >> 4) / wr;
-        const int64_t out = ((int64_t)blockIdx.x * wr + w) * 16 + r;
+    for (int i = threadIdx.x; i < wr * RT * 16 * a.batch; i += blockDim.x) {
+        const int m = i & 15, w = (i >> 4) % (wr * RT), b = (i >> 4) / (wr * RT);
+        const int64_t out = ((int64_t)blockIdx.x * wr * RT + w) * 16 + m;
         if (out >= a.n_out) continue;
         float y = 0;
         // the small parts first
 #pragma unroll
         for (int p = P - 1; p >= 0; --p) {
             float s = 0;
-            for (int k = 0; k < wk; ++k) s += sums[((w * wk + k) * NT * 16 + b * P + p) * 16 + r];
+            for (int k = 0; k < wk; ++k)
+                s += sums[((((w / RT) * wk + k) * RT + w % RT) * NT * 16 + b * P + p) * 16 + m];
             y += s;
         }
         ((T *)a.y)[(int64_t)b * a.n_out + out] = (T)y;
     }
 }
 
-template <int TYPE, int NT>
-hipError_t launch(const MxGemmArgs &a, hipStream_t s) {
+// One workgroup of up to 16 wavefronts per compute unit: its activations are
+// staged once. `tp` row tiles per workgroup, and as many wavefronts as fit
+// share each tile's sum.
+constexpr int kWorkgroups = 256;
+
+template <int TYPE, int NT, int RT>
+hipError_t launch(const MxGemmArgs &a, int wr, hipStream_t s) {
     constexpr int P = Elem<TYPE>::pieces;
     const int64_t tiles = ((int64_t)a.n_out + 15) / 16;
     const int steps = (a.n_in + kStep - 1) / kStep;
-    // the wavefronts of a tile: enough for about eight per compute unit
-    int wk = 1;
-    while (wk < 16 && wk < steps && tiles * wk < 2048) wk *= 2;
-    const int wr = wk < 4 ? 4 / wk : 1;
+    int wk = kMaxWaves(RT) / wr;
+    if (wk > steps) wk = steps;
     int chunk = kLdsX / (a.batch * P) / 2 / kStep * kStep;
     if (chunk > steps * kStep) chunk = steps * kStep;
     size_t lds = (size_t)a.batch * P * pitch_of(chunk);
-    const size_t join = (size_t)wk * wr * NT * 16 * 16 * 4;
+    const size_t join = (size_t)wk * wr * RT * NT * 16 * 16 * 4;
     if (lds < join) lds = join;
-    const unsigned grid = (unsigned)((tiles + wr - 1) / wr);
+    const unsigned grid = (unsigned)((tiles + wr * RT - 1) / (wr * RT));
     const bool words = a.n_in % (4 * kMxBlock) == 0 && (uintptr_t)a.scales % 4 == 0;
     if (words)
-        mxfp4_gemm_kernel<TYPE, NT, true><<<grid, wk * wr * 64, lds, s>>>(a, wk, chunk);
+        mxfp4_gemm_kernel<TYPE, NT, RT, true><<<grid, wk * wr * 64, lds, s>>>(a, wk, chunk);
     else
-        mxfp4_gemm_kernel<TYPE, NT, false><<<grid, wk * wr * 64, lds, s>>>(a, wk, chunk);
+        mxfp4_gemm_kernel<TYPE, NT, RT, false><<<grid, wk * wr * 64, lds, s>>>(a, wk, chunk);
     return hipGetLastError();
+}
+
+template <int TYPE, int NT>
+hipError_t launch(const MxGemmArgs &a, hipStream_t s) {
+    const int64_t tiles = ((int64_t)a.n_out + 15) / 16;
+    const int64_t tp = (tiles + kWorkgroups - 1) / kWorkgroups;
+    // two row tiles per wavefront where the activations' LDS reads would bound it
+    if constexpr (NT > 1) {
+        if (tp >= 2) return launch<TYPE, NT, 2>(a, (int)std::min<int64_t>((tp + 1) / 2, kMaxWaves(2)), s);
+    }
+    return launch<TYPE, NT, 1>(a, (int)std::min<int64_t>(tp, kMaxWaves(1)), s);
 }
 
 }  // namespace
