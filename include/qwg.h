@@ -591,7 +591,7 @@ int qwg_matmul_mxfp4(void *c, int type, const void *a_codes, const void *a_scale
  * are 16-byte aligned. `table` [n_seqs][table_width] holds each sequence's pages
  * in order (page p: positions p*page_tokens ..), `lens` [n_seqs] its positions;
  * both int32 in device memory. Entries past a sequence's positions are not read.
- * 1 <= n_seqs <= 65535.
+ * 1 <= n_seqs <= 65535; table_width * page_tokens <= 2^30.
  *
  * qwg_kv8_append: k and v [n_tokens][n_kv_heads][head_dim] of `type` (heads
  * contiguous, tokens k_stride and v_stride elements apart, so slices of one

@@ -9,6 +9,7 @@
 // consecutive positions of a channel in consecutive bytes both products take
 // their operands from memory as they lie.
 #include "mx_device.h"
+#include "mx_lds.h"
 
 namespace qwg {
 
@@ -111,13 +112,46 @@ __device__ __forceinline__ bf16x8 fp8x8(uint32_t a, uint32_t b) {
     return bf16x8{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
 }
 
-constexpr int kBlk = 64;     // positions a wavefront takes at once
-constexpr int kWaves = 4;
+constexpr int kBlk = 64;          // positions a wavefront takes at once
+constexpr int kMaxChunk = 4096;   // positions of a split, at most
+constexpr int kMaxPages = (kMaxChunk + kBlk) / 16 + 1;
+constexpr int kPageBytes = (kMaxPages * 8 + 15) & ~15;
 
 // Bytes of a word that hold a NaN code, as 0x80 each.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
     return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
+
+// The largest of the four lanes' values with the same lane % 16, without LDS.
+__device__ __forceinline__ float max_groups(float v) {
+    const auto a = __builtin_amdgcn_permlane16_swap(f2u(v), f2u(v), false, false);
+    v = fmaxf(u2f(a[0]), u2f(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(f2u(v), f2u(v), false, false);
+    return fmaxf(u2f(b[0]), u2f(b[1]));
+}
+
+// Two fp32 values' upper halves in one word, the first one's low.
+__device__ __forceinline__ uint32_t upper_halves(float a, float b) {
+    return __builtin_amdgcn_perm(f2u(b), f2u(a), 0x07060302u);
+}
+
+// Floats of one split's partial result: rows of D sums, then a (maximum, total)
+// pair per row, in whole 16 bytes.
+__device__ __host__ __forceinline__ int64_t partial_floats(int64_t rows, int dim) {
+    return (rows * (dim + 2) + 3) & ~(int64_t)3;
+}
+
+// LDS of an attention workgroup: Q parts, the split's pages, then per wavefront a
+// block's K and V (V of 96 channels on 16-token pages takes padded rows).
+constexpr int q_bytes(int type, int d, int r) {
+    return r * (d / 32) * (type == kF32 ? 3 : type == kF16 ? 2 : 1) * 1024;
+}
+constexpr int k_zone(int d) { return d * kBlk; }
+constexpr int v_zone(int d) { return (d == 96 ? 128 : d) * kBlk; }
+// Wavefronts of a workgroup: four, two such workgroups to a compute unit (one's
+// start and end then overlap the other's middle); eight for two tiles of 128
+// channels, whose Q would not fit twice.
+constexpr int waves_of(int d, int r) { return d == 128 && r == 2 ? 8 : 4; }
 
 // One workgroup: one split (`chunk` positions) of one sequence, one key/value
 // head, R tiles of 16 rows; a row is a (query token, head of the group) pair.
@@ -128,18 +162,28 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 // 16(l/16) .. +15. They are the B operand of O^T = V^T P^T as they stand: the
 // A operand's lane takes the same sixteen positions of channel l%16, sixteen
 // consecutive bytes of the transposed V page. No value crosses lanes but the
-// row maxima, and nothing but Q goes through LDS.
+// row maxima.
+//
+// K and V come by LDS DMA in the order of memory (four lanes to 64 bytes where
+// the page has them: read straight into the operands' lanes every 16 bytes were
+// an access of their own, and the L1 bound the kernel at 4 TB/s), the 16-byte
+// granules of a line permuted so that the operands' reads meet no bank twice. A
+// block's K is asked for as soon as the block before has read its own, V
+// likewise.
 //
 // Queries and probabilities enter as bf16 parts (one to three) that hold all
 // their bits, or 16 of the probabilities' for the 16-bit types; e4m3 is exact in bf16.
-template <int TYPE, int D, int R>
-__global__ __launch_bounds__(kWaves * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
+template <int TYPE, int D, int R, int W>
+__global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
     typedef typename Elem<TYPE>::T T;
     constexpr int PQ = Elem<TYPE>::pieces;      // parts of a query
     constexpr int PP = TYPE == kF32 ? 3 : 2;    // parts of a probability
     constexpr int KS = D / 32;                  // steps of the first product
     constexpr int DT = D / 16;                  // channel tiles of the second
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    constexpr int C = D / 16;                   // 16-byte granules of a K row
+    constexpr int NK = D / 16;                  // DMAs (1 KB) of a block's K
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
     const Kv8 &c = a.cache;
     const int group = a.n_heads / c.n_kv;
@@ -147,22 +191,44 @@ __global__ __launch_bounds__(kWaves * 64) void kv8_attend_kernel(Kv8AttendArgs a
     const int64_t seq = blockIdx.z;
     const int tiles = (rows + 16 * R - 1) / (16 * R);
     const int head = (int)blockIdx.y / tiles, row0 = (int)blockIdx.y % tiles * 16 * R;
-    const int64_t len0 = a.lens[seq], cap = a.width * c.page;
+    const int shift = __builtin_ctz(c.page);
+    const int len0 = a.lens[seq], cap = (int)a.width << shift;
     const bool bad = len0 < 0 || len0 > cap;  // no such length: the rows become NaN
-    const int64_t len = bad ? 0 : len0;
-    const int splits = max(1, (int)((len + a.chunk - 1) / a.chunk));
+    const int len = bad ? 0 : len0;
+    const int splits = max(1, (len + a.chunk - 1) / a.chunk);
     const int split = blockIdx.x;
     if (split >= splits) return;
+    const int window = (int)min(a.window, (int64_t)1 << 30);  // 0: all
     // positions that some row sees: those below len, from the first row's window on
-    const int64_t low = a.window > 0 ? max((int64_t)0, len - a.q_len + 1 - a.window) : 0;
-    const int64_t begin = max((int64_t)split * a.chunk, low / kBlk * kBlk);
-    const int64_t end = min((int64_t)(split + 1) * a.chunk, len);
+    const int low = window > 0 ? max(0, len - a.q_len + 1 - window) : 0;
+    const int begin = max(split * a.chunk, low & -kBlk);
+    const int end = min((split + 1) * a.chunk, len);
 
     extern __shared__ __align__(16) uint8_t lds[];
+    uint8_t *const q_lds = lds;
+    // the split's pages: number (-1: no page of the pool), exponents of K and V
+    uint2 *const pages = (uint2 *)(lds + q_bytes(TYPE, D, R));
+    const uint32_t zone = q_bytes(TYPE, D, R) + kPageBytes + wave * (k_zone(D) + v_zone(D));
+    uint8_t *const k_lds = lds + zone, *const v_lds = k_lds + k_zone(D);
+    const int first_page = begin >> shift;
+    for (int i = threadIdx.x; i < kMaxPages; i += W * 64) {
+        const int pos = (first_page + i) << shift;
+        uint2 e = {0, 0x7f7f};  // past the end: any page does, its codes are masked
+        if (pos < end) {
+            const int id = a.table[seq * a.width + first_page + i];
+            if (id < 0 || id >= c.n_pages) {
+                e.x = ~0u;
+            } else {
+                const int64_t at = (int64_t)id * c.n_kv + head;
+                e.x = id, e.y = c.k_scales[at] | (uint32_t)c.v_scales[at] << 8;
+            }
+        }
+        pages[i] = e;
+    }
     // Q parts: [tile][step][part][lane] 16 bytes, as the lanes take them
     {
         const T *q = (const T *)a.q;
-        for (int i = threadIdx.x; i < R * KS * 64; i += kWaves * 64) {
+        for (int i = threadIdx.x; i < R * KS * 64; i += W * 64) {
             const int l = i & 63, ks = (i >> 6) % KS, r = (i >> 6) / KS;
             const int row = row0 + r * 16 + (l & 15), lg = l >> 4;
             // a pair of steps takes 64 channels, 16 consecutive ones per lane
@@ -184,7 +250,7 @@ __global__ __launch_bounds__(kWaves * 64) void kv8_attend_kernel(Kv8AttendArgs a
             }
 #pragma unroll
             for (int p = 0; p < PQ; ++p)
-                *(u32x4 *)(lds + (((r * KS + ks) * PQ + p) * 64 + l) * 16) =
+                *(u32x4 *)(q_lds + (((r * KS + ks) * PQ + p) * 64 + l) * 16) =
                     u32x4{w[p][0], w[p][1], w[p][2], w[p][3]};
         }
     }
@@ -193,179 +259,244 @@ __global__ __launch_bounds__(kWaves * 64) void kv8_attend_kernel(Kv8AttendArgs a
     const float to_log2 = a.scale * 1.4426950408889634f;
     float top[R], sum[R];
     f32x4 out[R][DT];
+    int last[R];  // the last position that this lane's row sees
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         top[r] = -__builtin_inff();
         sum[r] = 0;
 #pragma unroll
         for (int t = 0; t < DT; ++t) out[r][t] = f32x4{0, 0, 0, 0};
-    }
-    // the last position that each of this lane's rows sees
-    int64_t last[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
         const int row = row0 + r * 16 + n;
         last[r] = row < rows ? len - a.q_len + row / group : -1;
     }
-    const int32_t *table = a.table + seq * a.width;
     const int64_t head_bytes = (int64_t)c.page * D;
-    // page of a position: 0 for positions past the end, -1 for a number that is no page
-    auto page_of = [&](int64_t pos) -> int64_t {
-        if (pos >= len) return 0;
-        const int64_t id = table[pos / c.page];
-        return id < 0 || id >= c.n_pages ? -1 : id;
+    auto page_at = [&](int pos) { return pages[(pos >> shift) - first_page]; };
+    auto page_base = [&](const uint8_t *p, int pos) {
+        return p + ((int64_t)max((int)page_at(pos).x, 0) * c.n_kv + head) * head_bytes;
     };
 
-    for (int64_t b0 = begin + wave * kBlk; b0 < end; b0 += kWaves * kBlk) {
-        const int64_t kpos = b0 + (n >> 2) * 16, vpos = b0 + g * 16;
-        int64_t kid = page_of(kpos), vid = page_of(vpos);
-        const bool lost = vid < 0;  // this lane's sixteen positions have no page
-        kid = max(kid, (int64_t)0), vid = max(vid, (int64_t)0);
-        const uint8_t *kp = c.k + (kid * c.n_kv + head) * head_bytes + (kpos % c.page + (n & 3)) * D + g * 16;
-        const uint8_t *vp = c.v + (vid * c.n_kv + head) * head_bytes + (int64_t)n * c.page + vpos % c.page;
-        float ks = e8m0(c.k_scales[vid * c.n_kv + head]) * to_log2;
-        // where there is no page its V counts for nothing: not even its scale may
-        // (0 times a NaN scale is NaN)
-        const float vs = lost || vpos >= len ? 1.0f : e8m0(c.v_scales[vid * c.n_kv + head]);
-        if (lost) ks = __builtin_nanf("");
+    // K in LDS: granule s of row r (a position of the block) holds granule s ^
+    // key(r) of the row: eight lanes of a tile's reads (rows 16a + 4u + b, two a
+    // and four b) then meet eight different 16-byte banks.
+    auto k_key = [](int b, int a1) {
+        if constexpr (D % 128 == 0) return b | a1 << 2;
+        else if constexpr (D == 96) return a1;
+        else return b >> 1 | a1 << 1;
+    };
+    auto issue_k = [&](int b0) {
+        const uint8_t *base[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            base[q] = page_base(c.k, b0 + q * 16) + ((b0 + q * 16) & (c.page - 1)) * D;
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            const int f = i * 64 + lane, r = f / C, s = f - r * C;
+            const int q0 = i * 64 / (16 * C), q1 = (i * 64 + 63) / (16 * C);
+            const uint8_t *p = q0 == q1 || f < q1 * 16 * C ? base[q0] : base[q1];
+            dma16(p + (r & 15) * D + (s ^ k_key(r & 3, (r >> 4) & 1)) * 16, zone + i * 1024);
+        }
+    };
+    // V in LDS: [16-position pieces that lie in other pages][channel][pieces of
+    // one page row], `pg` pieces of a row side by side, permuted like K's.
+    const int pg_log = min(shift - 4, 2), pg = 1 << pg_log;
+    const int v_runs = (D * pg + 63) / 64;  // DMAs of one page row's pieces
+    const int v_piece = lane & (pg - 1);
+    auto issue_v = [&](int b0) {
+        const int d0 = lane >> pg_log;
+        const int piece = pg_log == 2 ? v_piece ^ (d0 >> 1 & 3) : pg_log == 1 ? v_piece ^ (d0 >> 2 & 1) : 0;
+        uint32_t to = zone + k_zone(D);
+        for (int o = 0; o < 4 >> pg_log; ++o) {
+            const int pos = b0 + (o * pg + piece) * 16;
+            const uint8_t *p = page_base(c.v, pos) + (pos & (c.page - 1));
+            for (int i = 0; i < v_runs; ++i, to += 1024) {
+                const int d = min(d0 + i * (64 >> pg_log), D - 1);
+                dma16(p + d * c.page, to);
+            }
+        }
+    };
+    // waits: V's DMAs are the younger ones when K is needed, the next K's when V is
+    auto wait_k = [&] {
+        if (D == 96 && pg == 1) wait_vmcnt<8>();
+        else wait_vmcnt<D / 16>();
+    };
+    const int key = k_key(n & 3, (n >> 2) & 1);
+    const uint8_t *const k_row = k_lds + ((n >> 2) * 16 + (n & 3)) * D;
+    const int v_key = pg_log == 2 ? n >> 1 & 3 : pg_log == 1 ? n >> 2 & 1 : 0;
+    const uint8_t *const v_row = v_lds + (g >> pg_log) * v_runs * 1024 +
+                                 ((n << pg_log) + ((g & (pg - 1)) ^ v_key)) * 16;
+
+    int b0 = begin + wave * kBlk;
+    if (b0 < end) {
+        issue_k(b0);
+        issue_v(b0);
+    }
+    for (; b0 < end; b0 += W * kBlk) {
+        const int vpos = b0 + g * 16, next = b0 + W * kBlk;
+        wait_k();
         u32x4 kc[4][D / 64];
         u32x2 kt[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j) kc[u][j] = *(const u32x4 *)(kp + u * 4 * D + j * 64);
+            for (int j = 0; j < D / 64; ++j)
+                kc[u][j] = *(const u32x4 *)(k_row + u * 4 * D + ((j * 4 + g) ^ key) * 16);
             if constexpr (D % 64 != 0)
-                kt[u] = *(const u32x2 *)(kp - g * 8 + u * 4 * D + (D / 64) * 64);
+                kt[u] = *(const u32x2 *)(k_row + u * 4 * D + ((D / 64 * 4 + (g >> 1)) ^ key) * 16 + (g & 1) * 8);
         }
-        u32x4 vc[DT];
-#pragma unroll
-        for (int t = 0; t < DT; ++t) vc[t] = *(const u32x4 *)(vp + (int64_t)t * 16 * c.page);
+        const uint2 page = page_at(vpos);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // K is in registers
+        if (next < end) issue_k(next);
 
         f32x4 s[R][4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int r = 0; r < R; ++r) s[r][u] = f32x4{0, 0, 0, 0};
+            for (int u = 0; u < 4; ++u) s[r][u] = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const bool odd = D % 64 != 0 && k == KS - 1;
-                const bf16x8 kv = odd ? fp8x8(kt[u][0], kt[u][1])
-                                      : fp8x8(kc[u][k >> 1][(k & 1) * 2], kc[u][k >> 1][(k & 1) * 2 + 1]);
+        for (int k = 0; k < KS; ++k) {
+            const bool odd = D % 64 != 0 && k == KS - 1;
+            bf16x8 kv[4];
 #pragma unroll
-                for (int r = 0; r < R; ++r)
+            for (int u = 0; u < 4; ++u)
+                kv[u] = odd ? fp8x8(kt[u][0], kt[u][1])
+                            : fp8x8(kc[u][k >> 1][(k & 1) * 2], kc[u][k >> 1][(k & 1) * 2 + 1]);
 #pragma unroll
-                    for (int p = PQ - 1; p >= 0; --p) {
-                        const bf16x8 q = *(const bf16x8 *)(lds + (((r * KS + k) * PQ + p) * 64 + lane) * 16);
-                        s[r][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, q, s[r][u], 0, 0, 0);
-                    }
-            }
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int p = PQ - 1; p >= 0; --p) {
+                    const bf16x8 q = *(const bf16x8 *)(q_lds + (((r * KS + k) * PQ + p) * 64 + lane) * 16);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        s[r][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv[u], q, s[r][u], 0, 0, 0);
+                }
         }
+
+        const bool lost = (int)page.x < 0;  // this lane's sixteen positions have no page
+        float ks = e8m0(page.y & 255) * to_log2;
+        // where there is no page its V counts for nothing: not even its scale may
+        // (0 times a NaN scale is NaN)
+        const float vs = lost || vpos >= len ? 1.0f : e8m0(page.y >> 8 & 255);
+        if (lost) ks = __builtin_nanf("");
         // every row sees the whole block, or the rows' masks decide
-        const bool whole = b0 + kBlk <= len - a.q_len + 1 && (a.window <= 0 || b0 >= len - a.window);
-        if (!whole) {
-            // codes past the end are whatever the pool held: none of them may
-            // reach the products
-            const int64_t left = len - vpos;
-            const int keep = left < 0 ? 0 : left > 16 ? 16 : (int)left;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const int k = keep - w * 4;
-                const uint32_t m = k >= 4 ? ~0u : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
-#pragma unroll
-                for (int t = 0; t < DT; ++t) vc[t][w] &= m;
-            }
-        }
+        const bool whole = b0 + kBlk <= len - a.q_len + 1 && (window <= 0 || b0 >= len - window);
         uint32_t seen[R];
+        if (!whole) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            seen[r] = 0xffffu;
-            if (!whole) {
-                const int64_t hi = last[r] - vpos;
-                const int64_t lo = a.window > 0 ? max((int64_t)0, last[r] - a.window + 1 - vpos) : 0;
+            for (int r = 0; r < R; ++r) {
+                const int hi = last[r] - vpos;
+                const int lo = window > 0 ? max(0, hi - window + 1) : 0;
                 uint32_t m = hi < 0 ? 0u : hi >= 15 ? 0xffffu : (2u << hi) - 1u;
                 m &= lo >= 16 ? 0u : 0xffffu << lo;
-                seen[r] = m & 0xffffu;
+                seen[r] = m;
             }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
             float m = -__builtin_inff();
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 4; ++u) s[r][u] *= ks;
+            if (!whole) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float v = s[r][u][i] * ks;
-                    if (!whole && !(seen[r] >> (u * 4 + i) & 1)) v = -__builtin_inff();
-                    s[r][u][i] = v;
-                    m = fmaxf(m, v);
-                }
-            m = fmaxf(m, __shfl_xor(m, 16));
-            m = fmaxf(m, __shfl_xor(m, 32));
-            const float now = fmaxf(top[r], m);
-            const float base = now == -__builtin_inff() ? 0.0f : now;
-            const float alpha = __builtin_amdgcn_exp2f(top[r] - base);
-            top[r] = now;
-            float part = 0;
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float p = __builtin_amdgcn_exp2f(s[r][u][i] - base);
-                    s[r][u][i] = p;
-                    part += p;
-                }
-            sum[r] = sum[r] * alpha + part;
-#pragma unroll
-            for (int t = 0; t < DT; ++t) out[r][t] *= alpha;
-        }
-        // a NaN in V that some rows see and others do not must reach the former alone
-        bool some_nan = false;
-        if (!whole) {
-            uint32_t any = 0;
-#pragma unroll
-            for (int t = 0; t < DT; ++t)
-#pragma unroll
-                for (int w = 0; w < 4; ++w) any |= nan_bytes(vc[t][w]);
-            some_nan = __any(any != 0);
-        }
-        if (some_nan) {
-#pragma unroll
-            for (int t = 0; t < DT; ++t) {
-                u32x4 flags;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const uint32_t nb = nan_bytes(vc[t][w]) >> 7;  // 1 per NaN byte
-                    flags[w] = nb * 0x38u;                          // e4m3 1.0
-                    vc[t][w] &= ~(nb * 0xffu);
-                }
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    f32x4 hit = {0, 0, 0, 0};
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        bf16x8 see;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) see[i] = (__bf16)(seen[r] >> (k * 8 + i) & 1 ? 1.0f : 0.0f);
-                        hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            fp8x8(flags[k * 2], flags[k * 2 + 1]), see, hit, 0, 0, 0);
-                    }
+                for (int u = 0; u < 4; ++u)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (hit[i] > 0) out[r][t][i] = __builtin_nanf("");
-                }
+                        if (!(seen[r] >> (u * 4 + i) & 1)) s[r][u][i] = -__builtin_inff();
             }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m = fmaxf(m, s[r][u][i]);
+            m = max_groups(m);
+            if (__any(m > top[r])) {  // a new maximum in some row: what was summed shrinks
+                const float now = fmaxf(top[r], m);
+                const float alpha = now == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(top[r] - now);
+                top[r] = now;
+                sum[r] *= alpha;
+#pragma unroll
+                for (int t = 0; t < DT; ++t) out[r][t] *= alpha;
+            }
+            const float base = top[r] == -__builtin_inff() ? 0.0f : top[r];
+            f32x4 part = {0, 0, 0, 0};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[r][u][i] = __builtin_amdgcn_exp2f(s[r][u][i] - base);
+                part += s[r][u];
+            }
+            sum[r] += (part[0] + part[1]) + (part[2] + part[3]);
         }
-        bf16x8 pp[R][2][PP];
+        // p * vs as bf16 parts by truncation: never infinite (p <= 1), and a NaN
+        // keeps its upper half
+        u32x4 pp[R][2][PP];
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float p = s[r][k * 2 + i / 4][i % 4] * vs;
-                    uint32_t h, m, l;
-                    split3(p, h, m, l);
-                    pp[r][k][0][i] = __builtin_bit_cast(__bf16, (uint16_t)h);
-                    pp[r][k][1][i] = __builtin_bit_cast(__bf16, (uint16_t)m);
-                    if constexpr (PP == 3) pp[r][k][2][i] = __builtin_bit_cast(__bf16, (uint16_t)l);
+                for (int i = 0; i < 4; ++i) {
+                    const float p0 = s[r][k * 2 + i / 2][i % 2 * 2] * vs;
+                    const float p1 = s[r][k * 2 + i / 2][i % 2 * 2 + 1] * vs;
+                    const float r0 = p0 - u2f(f2u(p0) & 0xffff0000u);
+                    const float r1 = p1 - u2f(f2u(p1) & 0xffff0000u);
+                    pp[r][k][0][i] = upper_halves(p0, p1);
+                    pp[r][k][1][i] = upper_halves(r0, r1);
+                    if constexpr (PP == 3)
+                        pp[r][k][2][i] = upper_halves(r0 - u2f(f2u(r0) & 0xffff0000u),
+                                                      r1 - u2f(f2u(r1) & 0xffff0000u));
                 }
+
+        if (next < end) wait_vmcnt<NK>();
+        else wait_vmcnt<0>();
+        u32x4 vc[DT];
+#pragma unroll
+        for (int t = 0; t < DT; ++t) vc[t] = *(const u32x4 *)(v_row + (t << pg_log) * 256);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // V is in registers
+        if (next < end) issue_v(next);
+        // a NaN in V that some rows see and others do not must reach the former alone
+        if (!whole) {
+            // codes past the end are whatever the pool held: none of them may
+            // reach the product
+            const int keep = min(max(len - vpos, 0), 16);
+            uint32_t any = 0;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const int k = keep - w * 4;
+                const uint32_t m = k >= 4 ? ~0u : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
+#pragma unroll
+                for (int t = 0; t < DT; ++t) {
+                    vc[t][w] &= m;
+                    any |= nan_bytes(vc[t][w]);
+                }
+            }
+            if (__any(any != 0)) {
+#pragma unroll
+                for (int t = 0; t < DT; ++t) {
+                    u32x4 flags;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t nb = nan_bytes(vc[t][w]) >> 7;  // 1 per NaN byte
+                        flags[w] = nb * 0x38u;                          // e4m3 1.0
+                        vc[t][w] &= ~(nb * 0xffu);
+                    }
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        f32x4 hit = {0, 0, 0, 0};
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            bf16x8 see;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                see[i] = (__bf16)(seen[r] >> (k * 8 + i) & 1 ? 1.0f : 0.0f);
+                            hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                fp8x8(flags[k * 2], flags[k * 2 + 1]), see, hit, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (hit[i] > 0) out[r][t][i] = __builtin_nanf("");
+                    }
+                }
+            }
+        }
 #pragma unroll
         for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -375,7 +506,8 @@ __global__ __launch_bounds__(kWaves * 64) void kv8_attend_kernel(Kv8AttendArgs a
                 for (int r = 0; r < R; ++r)
 #pragma unroll
                     for (int p = PP - 1; p >= 0; --p)
-                        out[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pp[r][k][p], out[r][t], 0, 0, 0);
+                        out[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            v, __builtin_bit_cast(bf16x8, pp[r][k][p]), out[r][t], 0, 0, 0);
             }
     }
 
@@ -383,7 +515,7 @@ __global__ __launch_bounds__(kWaves * 64) void kv8_attend_kernel(Kv8AttendArgs a
     __syncthreads();
     constexpr int RP = D + 4;  // row pitch: four floats past a multiple of 32 banks
     float *so = (float *)lds;
-    float *sm = so + kWaves * R * 16 * RP;
+    float *sm = so + W * R * 16 * RP;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         float t = sum[r];
@@ -396,17 +528,19 @@ __global__ __launch_bounds__(kWaves * 64) void kv8_attend_kernel(Kv8AttendArgs a
     }
     __syncthreads();
     const int64_t row_base = seq * a.q_len;
-    for (int i = threadIdx.x; i < R * 16 * (D / 4); i += kWaves * 64) {
+    const int64_t all = (int64_t)a.q_len * a.n_heads;
+    float *part = a.partial + (seq * a.max_splits + split) * partial_floats(all, D);
+    for (int i = threadIdx.x; i < R * 16 * (D / 4); i += W * 64) {
         const int d = i % (D / 4) * 4, lr = i / (D / 4), row = row0 + lr;
         if (row >= rows) continue;
         float m = -__builtin_inff();
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) m = fmaxf(m, sm[(w * R * 16 + lr) * 2]);
+        for (int w = 0; w < W; ++w) m = fmaxf(m, sm[(w * R * 16 + lr) * 2]);
         const float base = m == -__builtin_inff() ? 0.0f : m;
         float total = 0;
         f32x4 o = {0, 0, 0, 0};
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 0; w < W; ++w) {
             const float f = __builtin_amdgcn_exp2f(sm[(w * R * 16 + lr) * 2] - base);
             total += f * sm[(w * R * 16 + lr) * 2 + 1];
             o += f * *(const f32x4 *)(so + (w * R * 16 + lr) * RP + d);
@@ -414,64 +548,96 @@ __global__ __launch_bounds__(kWaves * 64) void kv8_attend_kernel(Kv8AttendArgs a
         const int t = row / group, h = head * group + row % group;
         if (splits == 1) {
             T *dst = (T *)a.out + ((row_base + t) * a.n_heads + h) * D + d;
-            const float inv = bad ? __builtin_nanf("") : total == 0 ? 0.0f : 1.0f / total;
+            const float inv = bad ? __builtin_nanf("") : 1.0f / total;
 #pragma unroll
             for (int e = 0; e < 4; ++e) dst[e] = (T)(total == 0 && !bad ? 0.0f : o[e] * inv);
         } else {
-            float *dst = a.partial + ((seq * a.max_splits + split) * a.q_len * a.n_heads + (int64_t)t * a.n_heads + h) * (D + 2);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dst[2 + d + e] = o[e];
-            if (d == 0) dst[0] = m, dst[1] = total;
+            const int64_t at = (int64_t)t * a.n_heads + h;
+            *(f32x4 *)(part + at * D + d) = o;
+            if (d == 0) part[all * D + at * 2] = m, part[all * D + at * 2 + 1] = total;
         }
     }
 }
 
-// Joins the splits of a sequence: one wavefront per (query token, head).
+// Joins the splits of a sequence: one workgroup per (query token, head), its
+// wavefronts taking the splits in turn.
 template <int TYPE, int D>
-__global__ __launch_bounds__(64) void kv8_join_kernel(Kv8AttendArgs a) {
+__global__ __launch_bounds__(256) void kv8_join_kernel(Kv8AttendArgs a) {
     typedef typename Elem<TYPE>::T T;
+    constexpr int V = D / 4;   // lanes that hold one row, four channels each
+    constexpr int S = 64 / V;  // splits that a wavefront reads at once
+    __shared__ float sums[4 * S][D + 1];
+    __shared__ float red[2][4];
     const int64_t seq = blockIdx.y;
     const int row = blockIdx.x;  // token * n_heads + head
-    const int64_t len0 = a.lens[seq];
-    const int64_t len = len0 < 0 || len0 > a.width * a.cache.page ? 0 : len0;
-    const int splits = max(1, (int)((len + a.chunk - 1) / a.chunk));
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int len0 = a.lens[seq];
+    const int len = len0 < 0 || len0 > a.width * a.cache.page ? 0 : len0;
+    const int splits = max(1, (len + a.chunk - 1) / a.chunk);
     if (splits == 1) return;
-    const int64_t rows = (int64_t)a.q_len * a.n_heads;
-    const float *p = a.partial + (seq * a.max_splits * rows + row) * (D + 2);
+    const int64_t rows = (int64_t)a.q_len * a.n_heads, each = partial_floats(rows, D);
+    const float *part = a.partial + seq * a.max_splits * each;
+    const float *ml = part + rows * D + row * 2;
     float m = -__builtin_inff();
-    for (int s = 0; s < splits; ++s) m = fmaxf(m, p[s * rows * (D + 2)]);
+    for (int s = threadIdx.x; s < splits; s += 256) m = fmaxf(m, ml[s * each]);
+#pragma unroll
+    for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if (lane == 0) red[0][wave] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
     const float base = m == -__builtin_inff() ? 0.0f : m;
     float total = 0;
-    for (int s = 0; s < splits; ++s)
-        total += __builtin_amdgcn_exp2f(p[s * rows * (D + 2)] - base) * p[s * rows * (D + 2) + 1];
-    for (int d = threadIdx.x; d < D; d += 64) {
+    for (int s = threadIdx.x; s < splits; s += 256)
+        total += __builtin_amdgcn_exp2f(ml[s * each] - base) * ml[s * each + 1];
+#pragma unroll
+    for (int o = 32; o; o >>= 1) total += __shfl_xor(total, o);
+    if (lane == 0) red[1][wave] = total;
+    f32x4 o = {0, 0, 0, 0};
+    const int sub = lane / V, d = lane % V * 4;
+    if (sub < S) {
+        for (int s = wave * S + sub; s < splits; s += 4 * S)
+            o += __builtin_amdgcn_exp2f(ml[s * each] - base) *
+                 *(const f32x4 *)(part + s * each + (int64_t)row * D + d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sums[wave * S + sub][d + e] = o[e];
+    }
+    __syncthreads();
+    total = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    for (int d = threadIdx.x; d < D; d += 256) {
         float o = 0;
-        for (int s = 0; s < splits; ++s)
-            o += __builtin_amdgcn_exp2f(p[s * rows * (D + 2)] - base) * p[s * rows * (D + 2) + 2 + d];
+#pragma unroll
+        for (int s = 0; s < 4 * S; ++s) o += sums[s][d];
         ((T *)a.out)[(seq * rows + row) * D + d] = (T)(total == 0 ? 0.0f : o / total);
     }
 }
 
 template <int TYPE, int D, int R>
 hipError_t attend(const Kv8AttendArgs &a, hipStream_t s) {
+    constexpr int W = waves_of(D, R);
     const int rows = a.q_len * (a.n_heads / a.cache.n_kv);
     const int tiles = (rows + 16 * R - 1) / (16 * R);
-    constexpr size_t q = (size_t)R * (D / 32) * Elem<TYPE>::pieces * 64 * 16;
-    constexpr size_t join = (size_t)kWaves * R * 16 * (D + 4 + 2) * 4;
+    constexpr size_t work = q_bytes(TYPE, D, R) + kPageBytes + W * (k_zone(D) + v_zone(D));
+    constexpr size_t join = (size_t)W * R * 16 * (D + 4 + 2) * 4;
+    static_assert(work <= 160 * 1024 && join <= 160 * 1024, "LDS");
     const dim3 grid(a.max_splits, a.cache.n_kv * tiles, (unsigned)a.n_seqs);
-    kv8_attend_kernel<TYPE, D, R><<<grid, kWaves * 64, q > join ? q : join, s>>>(a);
+    kv8_attend_kernel<TYPE, D, R, W><<<grid, W * 64, work > join ? work : join, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.max_splits == 1) return e;
-    kv8_join_kernel<TYPE, D><<<dim3(a.q_len * a.n_heads, (unsigned)a.n_seqs), 64, 0, s>>>(a);
+    kv8_join_kernel<TYPE, D><<<dim3(a.q_len * a.n_heads, (unsigned)a.n_seqs), 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
+// Row tiles that a workgroup takes together: two where there are more than 16
+// rows per key/value head and the registers hold two (head_dim up to 128).
+int row_tiles(int rows, int dim) { return rows > 16 && dim <= 128 ? 2 : 1; }
+
 template <int TYPE>
 hipError_t attend_dim(const Kv8AttendArgs &a, hipStream_t s) {
+    const bool two = row_tiles(a.q_len * (a.n_heads / a.cache.n_kv), a.cache.dim) == 2;
     switch (a.cache.dim) {
-        case 64: return attend<TYPE, 64, 1>(a, s);
-        case 96: return attend<TYPE, 96, 1>(a, s);
-        case 128: return attend<TYPE, 128, 1>(a, s);
+        case 64: return two ? attend<TYPE, 64, 2>(a, s) : attend<TYPE, 64, 1>(a, s);
+        case 96: return two ? attend<TYPE, 96, 2>(a, s) : attend<TYPE, 96, 1>(a, s);
+        case 128: return two ? attend<TYPE, 128, 2>(a, s) : attend<TYPE, 128, 1>(a, s);
         case 192: return attend<TYPE, 192, 1>(a, s);
         default: return attend<TYPE, 256, 1>(a, s);
     }
@@ -499,23 +665,31 @@ hipError_t launch_kv8_append(const Kv8AppendArgs &a, int type, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Splits: enough workgroups for about four per compute unit, of at least
-// 256 positions (one block for each wavefront).
+// Splits: one round of resident workgroups for a single sequence, four rounds for
+// several, whose lengths differ (32 ragged sequences of up to 8192 positions, 8
+// heads of 128: 79 us in half a round, 73 us in four, 78 in sixteen; one of
+// 131,071, 4 tokens of 64 heads: 65 us in one round, 76 in two, 104 in eight,
+// more partial sums). Up to 1024 positions stay whole: the launch that joins
+// splits costs as much as three more turns of a workgroup.
 void kv8_attend_plan(Kv8AttendArgs &a, int64_t max_len, int cus) {
     const int rows = a.q_len * (a.n_heads / a.cache.n_kv);
     const int64_t cap = a.width * a.cache.page;
     if (max_len <= 0 || max_len > cap) max_len = cap;
-    const int64_t groups = a.n_seqs * a.cache.n_kv * ((rows + 15) / 16);
-    const int64_t want = (4 * (int64_t)cus + groups - 1) / groups;
+    const int r = row_tiles(rows, a.cache.dim);
+    const int64_t groups = a.n_seqs * a.cache.n_kv * ((rows + 16 * r - 1) / (16 * r));
+    const int64_t resident = (int64_t)cus * 8 / waves_of(a.cache.dim, r);
+    const int64_t want = ((a.n_seqs > 1 ? 4 : 1) * resident + groups - 1) / groups;
     int64_t chunk = (max_len + want - 1) / want;
     chunk = (chunk + 255) / 256 * 256;
+    if (cap <= 1024) chunk = 1024;
+    if (chunk > kMaxChunk) chunk = kMaxChunk;
     a.chunk = (int)chunk;
     a.max_splits = (int)((cap + chunk - 1) / chunk);
 }
 
 int64_t kv8_attend_partial_bytes(const Kv8AttendArgs &a) {
     if (a.max_splits <= 1) return 0;
-    return a.n_seqs * a.max_splits * a.q_len * a.n_heads * (int64_t)(a.cache.dim + 2) * 4;
+    return a.n_seqs * a.max_splits * partial_floats((int64_t)a.q_len * a.n_heads, a.cache.dim) * 4;
 }
 
 hipError_t launch_kv8_attend(const Kv8AttendArgs &a, int type, hipStream_t s) {

@@ -43,7 +43,7 @@ int check_cache(const qwg_kv8 *c) {
 }
 
 bool cache_seqs(const qwg_kv8 *c, int64_t width, int64_t n_seqs) {
-    return width >= 1 && width <= INT32_MAX / c->page_tokens && n_seqs >= 1 && n_seqs <= 65535;
+    return width >= 1 && width <= (1 << 30) / c->page_tokens && n_seqs >= 1 && n_seqs <= 65535;
 }
 
 Kv8 cache_of(const qwg_kv8 *c) {
