@@ -24,20 +24,30 @@ __device__ __forceinline__ uint32_t page_exponent(uint32_t top) {
     return e > 0 ? (uint32_t)e : 0;
 }
 
-__device__ __forceinline__ uint32_t fp8_code(float v, float scale) {
+// Four codes of a value each, the first in the low byte. NaN and infinity become
+// NaN codes.
+__device__ __forceinline__ uint32_t fp8_codes(float a, float b, float c, float d, float scale) {
     typedef short s16x2 __attribute__((ext_vector_type(2)));
-    const s16x2 z = {0, 0};
-    // NaN and infinity become the NaN code
-    return __builtin_bit_cast(
-               uint32_t, __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(z, v, v, scale, false)) & 255u;
+    s16x2 v = {0, 0};
+    v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v, a, b, scale, false);
+    v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v, c, d, scale, true);
+    return __builtin_bit_cast(uint32_t, v);
 }
 
-__device__ __forceinline__ float fp8_value(uint32_t code) {
-    return __builtin_amdgcn_cvt_f32_fp8((int)code, 0);
+// The four codes of a word, times `shift`, as codes.
+__device__ __forceinline__ uint32_t fp8_shifted(uint32_t w, float shift) {
+    return fp8_codes(__builtin_amdgcn_cvt_f32_fp8((int)w, 0) * shift,
+                     __builtin_amdgcn_cvt_f32_fp8((int)w, 1) * shift,
+                     __builtin_amdgcn_cvt_f32_fp8((int)w, 2) * shift,
+                     __builtin_amdgcn_cvt_f32_fp8((int)w, 3) * shift, 1.0f);
 }
 
-// One workgroup per (page of a sequence, sequence, head of K or V).
-template <int TYPE>
+// One workgroup per (page of a sequence, sequence, head of K or V). A thread
+// takes four consecutive positions of eight channels: 8-byte stores to a K page,
+// 4-byte stores (one per channel) to a transposed V page. The page's largest new
+// magnitude comes first; a thread's first tile stays in registers meanwhile.
+// VEC: the values of a token start on 16 bytes.
+template <int TYPE, bool VEC>
 __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs a) {
     typedef typename Elem<TYPE>::T T;
     __shared__ uint32_t tops[4];
@@ -58,20 +68,46 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs a) {
     const T *x = (const T *)(is_v ? a.v : a.k) + (int64_t)head * c.dim;
     const int64_t stride = is_v ? a.v_stride : a.k_stride;
     const int64_t end = min(held + count, a.width * c.page);
+    const int octs = c.dim / 8;
     for (int64_t p = held / c.page + blockIdx.x; p * c.page < end; p += gridDim.x) {
         const int64_t id = a.table[seq * a.width + p];
         if (id < 0 || id >= c.n_pages) continue;
         const int64_t pos0 = p * c.page;
         const int old = (int)max((int64_t)0, held - pos0);               // slots filled before
         const int stop = (int)min((int64_t)c.page, end - pos0);          // slots filled after
-        const int64_t tok0 = first + pos0 - held;                        // token of slot 0
         uint8_t *codes = (is_v ? c.v : c.k) + (id * c.n_kv + head) * (int64_t)c.page * c.dim;
         uint8_t *scale = (is_v ? c.v_scales : c.k_scales) + id * c.n_kv + head;
+        const T *x0 = x + (first + pos0 - held) * stride;                // token of slot 0
+        // tiles: groups of four slots from the one that holds slot `old`, by channel octets;
+        // neighbouring threads take neighbouring octets of K, neighbouring slots of V
+        const int g0 = old >> 2, groups = ((stop + 3) >> 2) - g0, tiles = groups * octs;
+        float v[4][8];
+        auto load = [&](int i, int &slot, int &d) {
+            const int by = is_v ? groups : octs, q = i / by, r = i - q * by;
+            slot = (g0 + (is_v ? r : q)) * 4, d = (is_v ? q : r) * 8;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[t][e] = 0;
+                if (slot + t >= old && slot + t < stop)
+                    load8<T, VEC>(x0 + (slot + t) * stride + d, v[t]);
+            }
+        };
         uint32_t top = 0;
-        for (int i = threadIdx.x; i < (stop - old) * c.dim; i += blockDim.x) {
-            const int s = old + i / c.dim, d = i % c.dim;
-            const uint32_t m = f2u(to_f32(x[(tok0 + s) * stride + d])) & 0x7fffffffu;
-            if (m < 0x7f800000u) top = max(top, m);
+        // the last tile of a thread is loaded last, and kept for the second pass
+        const int last = (int)threadIdx.x < tiles
+                             ? (int)threadIdx.x + (tiles - 1 - (int)threadIdx.x) / 256 * 256
+                             : -1;
+        int slot = 0, d = 0;
+        for (int i = threadIdx.x; i < tiles; i += 256) {
+            load(i, slot, d);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t m = f2u(v[t][e]) & 0x7fffffffu;
+                    top = max(top, m < 0x7f800000u ? m : 0u);
+                }
         }
 #pragma unroll
         for (int o = 32; o; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
@@ -81,20 +117,51 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs a) {
         top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
         const uint32_t before = old ? *scale : 0;
         const uint32_t now = max(before, page_exponent(top));
-        if (old && now > before) {
-            // the page's scale rises: its codes are rounded to the new one
-            const float shift = __builtin_ldexpf(1.0f, (int)before - (int)now);
-            for (int i = threadIdx.x; i < old * c.dim; i += blockDim.x) {
-                const int64_t at = is_v ? (int64_t)(i / old) * c.page + i % old : i;
-                codes[at] = (uint8_t)fp8_code(fp8_value(codes[at]) * shift, 1.0f);
+        const float sc = e8m0(now);
+        for (int i = last; i >= 0; i -= 256) {
+            if (i != last) load(i, slot, d);
+            const int lo = max(old - slot, 0), hi = min(stop - slot, 4);
+            if (!is_v) {
+                for (int t = lo; t < hi; ++t) {
+                    u32x2 w = {0, 0};
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        if (s == t)
+                            w = u32x2{fp8_codes(v[s][0], v[s][1], v[s][2], v[s][3], sc),
+                                      fp8_codes(v[s][4], v[s][5], v[s][6], v[s][7], sc)};
+                    *(u32x2 *)(codes + (slot + t) * c.dim + d) = w;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t w = fp8_codes(v[0][e], v[1][e], v[2][e], v[3][e], sc);
+                    uint8_t *to = codes + (d + e) * c.page + slot;
+                    if (lo == 0 && hi == 4) {
+                        *(uint32_t *)to = w;
+                    } else {
+                        for (int t = lo; t < hi; ++t) to[t] = (uint8_t)(w >> (8 * t));
+                    }
+                }
             }
         }
-        const float sc = e8m0(now);
-        for (int i = threadIdx.x; i < (stop - old) * c.dim; i += blockDim.x) {
-            const int n = stop - old;
-            const int s = old + (is_v ? i % n : i / c.dim), d = is_v ? i / n : i % c.dim;
-            const float v = to_f32(x[(tok0 + s) * stride + d]);
-            codes[is_v ? d * c.page + s : s * c.dim + d] = (uint8_t)fp8_code(v, sc);
+        if (old && now > before) {
+            // the page's scale rises: its earlier codes are rounded to the new one
+            const float shift = __builtin_ldexpf(1.0f, (int)before - (int)now);
+            if (!is_v) {
+                for (int i = threadIdx.x; i < old * c.dim / 4; i += 256)
+                    ((uint32_t *)codes)[i] = fp8_shifted(((uint32_t *)codes)[i], shift);
+            } else {
+                const int words = (old + 3) >> 2;
+                for (int i = threadIdx.x; i < words * c.dim; i += 256) {
+                    const int ch = i / words, s = (i - ch * words) * 4;
+                    uint8_t *at = codes + ch * c.page + s;
+                    if (s + 4 <= old) {
+                        *(uint32_t *)at = fp8_shifted(*(uint32_t *)at, shift);
+                    } else {  // the word's other slots may be getting new codes
+                        for (int t = 0; s + t < old; ++t) at[t] = (uint8_t)fp8_shifted(at[t], shift);
+                    }
+                }
+            }
         }
         __syncthreads();  // every thread has read the scale
         if (threadIdx.x == 0) *scale = (uint8_t)now;
@@ -656,12 +723,19 @@ hipError_t launch_kv8_append(const Kv8AppendArgs &a, int type, hipStream_t s) {
     if (pages > a.width) pages = a.width;
     if (pages > 4096) pages = 4096;
     const dim3 grid((unsigned)pages, (unsigned)a.n_seqs, (unsigned)(a.cache.n_kv * 2));
+    const uintptr_t size = type == kF32 ? 4 : 2;
+    // (head_dim values are whole 16 bytes in every type)
+    const bool vec = ((uintptr_t)a.k | (uintptr_t)a.v) % 16 == 0 &&
+                     (a.n_tokens == 1 || (a.k_stride * size % 16 == 0 && a.v_stride * size % 16 == 0));
     if (type == kF32)
-        kv8_append_kernel<kF32><<<grid, 256, 0, s>>>(a);
+        vec ? kv8_append_kernel<kF32, true><<<grid, 256, 0, s>>>(a)
+            : kv8_append_kernel<kF32, false><<<grid, 256, 0, s>>>(a);
     else if (type == kF16)
-        kv8_append_kernel<kF16><<<grid, 256, 0, s>>>(a);
+        vec ? kv8_append_kernel<kF16, true><<<grid, 256, 0, s>>>(a)
+            : kv8_append_kernel<kF16, false><<<grid, 256, 0, s>>>(a);
     else
-        kv8_append_kernel<kBF16><<<grid, 256, 0, s>>>(a);
+        vec ? kv8_append_kernel<kBF16, true><<<grid, 256, 0, s>>>(a)
+            : kv8_append_kernel<kBF16, false><<<grid, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -357,3 +357,25 @@ def test_refusals():
     for call in bad:
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("shift,gap", [(1, 0), (0, 3), (8, 8)])
+def test_values_at_any_address(t, shift, gap):
+    # keys, values and queries that start on their type's alignment alone, tokens at an odd distance
+    rng = np.random.default_rng(13)
+    heads, dim, page = 2, 96, 32
+    lens, new = np.array([3, 40], np.int32), 37
+    table, n_pages = tables(rng, lens + new, page)
+    c = ref.Cache(n_pages, heads, dim, page, rng)
+    c.append(rng.standard_normal((43, heads, dim)), rng.standard_normal((43, heads, dim)), table, np.zeros(2, int), [0, 3, 43])
+    got = pages(c)
+    width = heads * dim
+    flat, d = typed(rng.standard_normal(2 * new * (width + gap) + shift), t)
+    x = flat[shift:].view(2 * new, width + gap)[:, :width].unflatten(1, (heads, dim))
+    xd = d[shift:].reshape(2 * new, width + gap)[:, :width].reshape(-1, heads, dim)
+    qwg.kv8_append(x, x, *got, dev(table), dev(lens))
+    c.append(xd, xd, table, lens, [0, new, 2 * new])
+    assert_pages(got, c)
+    q, qd = x[:4].unflatten(0, (2, 2)), xd[:4].reshape(2, 2, heads, dim)
+    assert_attend(qwg.kv8_attend(q, *got, dev(table), dev(lens + new)), *ref.attend(qd, c, table, lens + new, dim ** -0.5), t, dim)
