@@ -14,6 +14,18 @@ __device__ __forceinline__ void dma16(const void *g, uint32_t lds) {
     asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(lds), "v"(g) : "memory");
 }
 
+// The same from a wavefront-uniform base and a byte offset per lane.
+__device__ __forceinline__ void dma16(const void *base, uint32_t offset, uint32_t lds) {
+    // (readfirstlane returns int: widen through uint32_t, never by sign extension)
+    const uint64_t p = (uint64_t)(uintptr_t)base;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)p);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
+    const uint64_t u = (uint64_t)lo | (uint64_t)hi << 32;
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(lds), "v"(offset),
+                 "s"((const void *)(uintptr_t)u)
+                 : "memory");
+}
+
 // Wait until at most N vector-memory operations of this wavefront are
 // outstanding (they complete in issue order).
 template <int N>

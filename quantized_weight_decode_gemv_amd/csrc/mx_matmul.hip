@@ -1,103 +1,240 @@
 // C = A W^T for MXFP4 matrices A [n_rows, n_in] and W [n_out, n_in] (prefill:
 // the activations of many tokens encoded to MXFP4), on the matrix cores' own
 // microscaled form: v_mfma_scale_f32_16x16x128_f8f6f4 takes E2M1 operands and one
-// E8M0 byte per lane for the 32 values that the lane holds.
+// E8M0 byte per lane for the 32 values that the lane holds, and accumulates in
+// fp32 (65,536 operations in 16 cycles: 10 PFLOP/s on the chip).
+//
+// A workgroup holds BM x BN of C and walks n_in in stages of 256: 128 bytes of
+// codes and 8 of scales per row. Codes come by LDS DMA, a whole 128-byte line per
+// row, one stage ahead in the other of two buffers; the 16-byte granules of a row
+// are permuted so that a tile's operand reads meet no bank twice. Lane l takes
+// the 32-value blocks 2(l/16), 2(l/16)+1 of a stage's eight: two products.
+//
+// Rows within a group of 64 (four 16-row tiles) are dealt so that row m of tile i
+// is row 16(m/4) + 4i + m%4. The result lane's four rows in each of four tiles are
+// then 16 consecutive outputs, and four tiles' scales of a lane lie in one 8-byte
+// word, whose bytes the product instruction selects by itself.
 #include "mx_device.h"
+#include "mx_lds.h"
 
 namespace qwg {
 
 namespace {
 
-// Four wavefronts, each 64 x 64 of C, operands from memory.
-struct Frag {
-    u32x4 c[4];
-    uint32_t s;
+constexpr int kStageBlocks = 8;                                // blocks of a row per stage
+constexpr int kStageBytes = kStageBlocks * kMxCodeBytes;       // 128
+
+template <int Q, int I, int J>
+__device__ __forceinline__ f32x4 product(u32x4 w, u32x4 a, u32x2 ws, u32x2 as, f32x4 c) {
+    const i32x8 x = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+    const i32x8 y = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+        x, y, c, 4, 4, (I & 1) * 2 + Q, (int)ws[(I >> 1) & 1], (J & 1) * 2 + Q, (int)as[(J >> 1) & 1]);
+}
+
+// f(integral constant) for 0 .. N-1
+template <int I>
+struct Int {
+    static constexpr int v = I;
 };
-
-template <bool WORDS>
-__device__ __forceinline__ void load_frag(Frag &o, const uint8_t *codes, const uint8_t *scales,
-                                          int b, int nblk) {
-    if (WORDS && b + 4 <= nblk) {
-        const u32x4 *p = (const u32x4 *)(codes + (int64_t)b * kMxCodeBytes);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o.c[q] = p[q];
-        o.s = *(const uint32_t *)(scales + b);
-        return;
-    }
-    o.s = 0x7f7f7f7fu;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        o.c[q] = u32x4{0, 0, 0, 0};
-        if (b + q < nblk) {
-            o.c[q] = *(const u32x4 *)(codes + (int64_t)(b + q) * kMxCodeBytes);
-            o.s = (o.s & ~(255u << (8 * q))) | (uint32_t)scales[b + q] << (8 * q);
-        }
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(F &&f) {
+    if constexpr (I < N) {
+        f(Int<I>{});
+        each<N, I + 1>(f);
     }
 }
 
-template <int Q>
-__device__ __forceinline__ f32x4 product(const Frag &w, const Frag &a, f32x4 c) {
-    const i32x8 x = {(int)w.c[Q][0], (int)w.c[Q][1], (int)w.c[Q][2], (int)w.c[Q][3], 0, 0, 0, 0};
-    const i32x8 y = {(int)a.c[Q][0], (int)a.c[Q][1], (int)a.c[Q][2], (int)a.c[Q][3], 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, Q, (int)w.s, Q, (int)a.s);
-}
-
-template <int TYPE, bool WORDS>
-__global__ __launch_bounds__(256) void mxfp4_matmul_kernel(MxMatmulArgs a) {
+// TM, TN: 16-row tiles of A and of W that a wavefront takes; WM x WN wavefronts.
+template <int TYPE, int TM, int TN, int WM, int WN>
+__global__ __launch_bounds__(WM * WN * 64) void mxfp4_matmul_kernel(MxMatmulArgs a, int row_tiles,
+                                                                    int out_tiles) {
     typedef typename Elem<TYPE>::T T;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    constexpr int BM = WM * TM * 16, BN = WN * TN * 16, R = BM + BN, W = WM * WN;
+    static_assert(BM % 64 == 0 && BN % 64 == 0 && TN % 4 == 0 && R <= W * 64, "tiles");
+    constexpr int kBuffer = R * kStageBytes + R * 8;  // codes [row][128], then scales
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
-    const int nblk = a.n_in / kMxBlock;
-    const int64_t out0 = (int64_t)blockIdx.x * 128 + (wave & 1) * 64;
-    const int64_t row0 = (int64_t)blockIdx.y * 128 + (wave >> 1) * 64;
-    f32x4 acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-    for (int b = g * 4; b - g * 4 < nblk; b += 16) {
-        Frag w[4], x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t o = min(out0 + i * 16 + n, a.n_out - 1);
-            const int64_t r = min(row0 + i * 16 + n, a.n_rows - 1);
-            load_frag<WORDS>(w[i], a.w + o * nblk * kMxCodeBytes, a.w_scales + o * nblk, b, nblk);
-            load_frag<WORDS>(x[i], a.a + r * nblk * kMxCodeBytes, a.a_scales + r * nblk, b, nblk);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                acc[i][j] = product<0>(w[i], x[j], acc[i][j]);
-                acc[i][j] = product<1>(w[i], x[j], acc[i][j]);
-                acc[i][j] = product<2>(w[i], x[j], acc[i][j]);
-                acc[i][j] = product<3>(w[i], x[j], acc[i][j]);
-            }
+    const int wm = wave / WN, wn = wave % WN;
+    const int nblk = a.n_in / kMxBlock, stages = nblk / kStageBlocks;
+    const int64_t row_bytes = (int64_t)nblk * kMxCodeBytes;
+
+    // Workgroups go round the eight XCDs: give each a contiguous run of tiles,
+    // in bands of eight row tiles, so that its L2 holds what its workgroups share.
+    int row_tile, out_tile;
+    {
+        const int total = row_tiles * out_tiles, id = blockIdx.x;
+        const int xcd = id & 7, q = total >> 3, r = total & 7;
+        const int at = xcd * q + min(xcd, r) + (id >> 3);
+        const int band = at / (8 * out_tiles), in = at - band * 8 * out_tiles;
+        const int high = min(8, row_tiles - band * 8);
+        out_tile = in / high, row_tile = band * 8 + in % high;
     }
+    const int64_t row0 = (int64_t)row_tile * BM, out0 = (int64_t)out_tile * BN;
+    const uint8_t *a_codes = a.a + row0 * row_bytes, *w_codes = a.w + out0 * row_bytes;
+    const int a_last = (int)min<int64_t>(BM - 1, a.n_rows - 1 - row0);
+    const int w_last = (int)min<int64_t>(BN - 1, a.n_out - 1 - out0);
+
+    // LDS row r: A's rows, then W's. Rows past the last one read the last one.
+    constexpr int ND = R / 8 / W;  // DMAs (eight rows) of a wavefront per stage
+    static_assert(R % (8 * W) == 0, "whole DMAs");
+    uint32_t from[ND];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t r = row0 + j * 16 + n;
+    for (int i = 0; i < ND; ++i) {
+        const int r = (wave * ND + i) * 8 + (lane >> 3), gran = (lane & 7) ^ ((r & 3) | (r >> 4 & 1) << 2);
+        const int at = r < BM ? min(r, a_last) : min(r - BM, w_last);
+        from[i] = (uint32_t)(at * row_bytes) + gran * 16;
+    }
+    auto issue = [&](int s, int buf) {
+#pragma unroll
+        for (int i = 0; i < ND; ++i) {
+            const int r = (wave * ND + i) * 8;  // a DMA's rows are all A's or all W's
+            dma16((r < BM ? a_codes : w_codes) + (int64_t)s * kStageBytes, from[i],
+                  buf * kBuffer + r * kStageBytes);
+        }
+    };
+    // a thread's row of scales: eight bytes a stage at any alignment
+    const int sr = threadIdx.x;
+    const bool has_row = sr < R;
+    const uint8_t *scales = sr < BM ? a.a_scales + (row0 + min(sr, a_last)) * nblk
+                                    : a.w_scales + (out0 + min(sr - BM, w_last)) * nblk;
+    auto fetch_scales = [&](int s) {
+        uint64_t v = 0;
+        if (has_row) __builtin_memcpy(&v, scales + (int64_t)s * kStageBlocks, 8);
+        return v;
+    };
+    // [64-row group][lane group][lane % 16][tile] two bytes
+    auto put_scales = [&](uint64_t v, int buf) {
+        if (!has_row) return;
+        uint8_t *to = lds + buf * kBuffer + R * kStageBytes + (sr >> 6) * 512 +
+                      ((sr >> 4 & 3) * 4 + (sr & 3)) * 8 + (sr >> 2 & 3) * 2;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) *(uint16_t *)(to + h * 128) = (uint16_t)(v >> (16 * h));
+    };
+
+    f32x4 acc[TN][TM];
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    const int key = (n & 3) | (n >> 2 & 1) << 2;
+    const int lane_row = (n >> 2) * 16 + (n & 3);
+    auto compute = [&](int buf) {
+        const uint8_t *codes = lds + buf * kBuffer, *sc = codes + R * kStageBytes + g * 128 + n * 8;
+        u32x2 ws[TN / 4], as[(TM + 3) / 4];
+#pragma unroll
+        for (int i = 0; i < TN / 4; ++i) ws[i] = *(const u32x2 *)(sc + (BM / 64 + wn * (TN / 4) + i) * 512);
+#pragma unroll
+        for (int j = 0; j < (TM + 3) / 4; ++j) as[j] = *(const u32x2 *)(sc + (wm * TM / 4 + j) * 512);
+        if constexpr (TM == 2) {  // half a group: its tiles are 0, 1 or 2, 3
+            if (wm & 1) as[0][0] = as[0][1];
+        }
+        each<2>([&](auto q) {
+            u32x4 w[TN], x[TM];
+            const int gran = ((g * 2 + q.v) ^ key) * 16;
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+                w[i] = *(const u32x4 *)(codes + (BM + (wn * TN + i) / 4 * 64 + (wn * TN + i) % 4 * 4 + lane_row) * kStageBytes + gran);
+#pragma unroll
+            for (int j = 0; j < TM; ++j)
+                x[j] = *(const u32x4 *)(codes + ((wm * TM + j) / 4 * 64 + (wm * TM + j) % 4 * 4 + lane_row) * kStageBytes + gran);
+            each<TN>([&](auto i) {
+                each<TM>([&](auto j) {
+                    acc[i.v][j.v] = product<q.v, i.v, j.v>(w[i.v], x[j.v], ws[i.v / 4], as[j.v / 4], acc[i.v][j.v]);
+                });
+            });
+        });
+    };
+
+    if (stages > 0) {
+        issue(0, 0);
+        put_scales(fetch_scales(0), 0);
+        wait_vmcnt<0>();
+        __syncthreads();
+        for (int s = 0; s < stages; ++s) {
+            const int buf = s & 1;
+            uint64_t next = 0;
+            if (s + 1 < stages) {
+                next = fetch_scales(s + 1);
+                issue(s + 1, buf ^ 1);
+            }
+            compute(buf);
+            if (s + 1 < stages) {
+                wait_vmcnt<0>();
+                put_scales(next, buf ^ 1);
+            }
+            __syncthreads();
+        }
+    }
+    if (const int left = nblk - stages * kStageBlocks) {
+        // the last blocks: what lies past them is zero with scale 1
+        for (int f = threadIdx.x; f < R * kStageBlocks; f += W * 64) {
+            const int r = f >> 3, b = (f & 7) ^ ((r & 3) | (r >> 4 & 1) << 2);
+            const uint8_t *p = r < BM ? a_codes + min(r, a_last) * row_bytes
+                                      : w_codes + min(r - BM, w_last) * row_bytes;
+            u32x4 v = {0, 0, 0, 0};
+            if (b < left) v = *(const u32x4 *)(p + (int64_t)stages * kStageBytes + b * kMxCodeBytes);
+            *(u32x4 *)(lds + f * 16) = v;
+        }
+        uint64_t v = 0x7f7f7f7f7f7f7f7full;
+        if (has_row) {
+            for (int b = 0; b < left; ++b)
+                v = (v & ~(255ull << (8 * b))) | (uint64_t)scales[stages * kStageBlocks + b] << (8 * b);
+        }
+        put_scales(v, 0);
+        __syncthreads();
+        compute(0);
+    }
+
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+        const int64_t r = row0 + (wm * TM + j) / 4 * 64 + (wm * TM + j) % 4 * 4 + lane_row;
         if (r >= a.n_rows) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < TN; i += 4) {
+            // sixteen consecutive outputs
+            const int64_t o = out0 + (wn * TN + i) / 4 * 64 + g * 16;
+            T *to = (T *)a.c + r * a.n_out + o;
+            typedef T t4 __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+            if (o + 16 <= a.n_out) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int64_t o = out0 + i * 16 + g * 4 + e;
-                if (o < a.n_out) ((T *)a.c)[r * a.n_out + o] = (T)acc[i][j][e];
+                for (int h = 0; h < 4; ++h) {
+                    const f32x4 v = acc[i + h][j];
+                    *(t4 *)(to + h * 4) = t4{(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
+                }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (o + h * 4 + e < a.n_out) to[h * 4 + e] = (T)acc[i + h][j][e];
             }
+        }
     }
+}
+
+template <int TYPE, int TM, int TN, int WM, int WN>
+hipError_t launch(const MxMatmulArgs &a, hipStream_t s) {
+    constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
+    const int64_t rt = (a.n_rows + BM - 1) / BM, ot = (a.n_out + BN - 1) / BN;
+    if (rt * ot > INT32_MAX) return hipErrorInvalidValue;
+    constexpr size_t lds = 2 * (BM + BN) * (kStageBytes + 8);
+    mxfp4_matmul_kernel<TYPE, TM, TN, WM, WN>
+        <<<(unsigned)(rt * ot), WM * WN * 64, lds, s>>>(a, (int)rt, (int)ot);
+    return hipGetLastError();
 }
 
 template <int TYPE>
 hipError_t launch(const MxMatmulArgs &a, hipStream_t s) {
-    const dim3 grid((unsigned)((a.n_out + 127) / 128), (unsigned)((a.n_rows + 127) / 128));
-    const bool words = a.n_in % (4 * kMxBlock) == 0 &&
-                       ((uintptr_t)a.a_scales | (uintptr_t)a.w_scales) % 4 == 0;
-    if (words)
-        mxfp4_matmul_kernel<TYPE, true><<<grid, 256, 0, s>>>(a);
-    else
-        mxfp4_matmul_kernel<TYPE, false><<<grid, 256, 0, s>>>(a);
-    return hipGetLastError();
+    // the largest tile that still gives every compute unit one
+    auto tiles = [&](int64_t m, int64_t n) {
+        return ((a.n_rows + m - 1) / m) * ((a.n_out + n - 1) / n);
+    };
+    if (tiles(256, 256) >= 256) return launch<TYPE, 8, 4, 2, 4>(a, s);
+    if (tiles(128, 128) >= 256) return launch<TYPE, 4, 4, 2, 2>(a, s);
+    return launch<TYPE, 2, 4, 2, 2>(a, s);
 }
 
 }  // namespace
