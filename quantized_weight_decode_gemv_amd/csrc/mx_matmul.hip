@@ -97,7 +97,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mxfp4_matmul_kernel(MxMatmulArgs
     };
     // a thread's row of scales: eight bytes a stage at any alignment
     const int sr = threadIdx.x;
-    const bool has_row = sr < R;
+    const bool has_row = R == W * 64 || sr < R;
     const uint8_t *scales = sr < BM ? a.a_scales + (row0 + min(sr, a_last)) * nblk
                                     : a.w_scales + (out0 + min(sr - BM, w_last)) * nblk;
     auto fetch_scales = [&](int s) {
@@ -153,20 +153,20 @@ __global__ __launch_bounds__(WM * WN * 64) void mxfp4_matmul_kernel(MxMatmulArgs
         put_scales(fetch_scales(0), 0);
         wait_vmcnt<0>();
         __syncthreads();
-        for (int s = 0; s < stages; ++s) {
+        int s = 0;
+        for (; s + 1 < stages; ++s) {
             const int buf = s & 1;
-            uint64_t next = 0;
-            if (s + 1 < stages) {
-                next = fetch_scales(s + 1);
-                issue(s + 1, buf ^ 1);
-            }
+            const uint64_t next = fetch_scales(s + 1);
+            issue(s + 1, buf ^ 1);
             compute(buf);
-            if (s + 1 < stages) {
-                wait_vmcnt<0>();
-                put_scales(next, buf ^ 1);
-            }
+            // the products, which touch no memory, must not sink below the wait
+            __builtin_amdgcn_sched_barrier(0);
+            wait_vmcnt<0>();
+            put_scales(next, buf ^ 1);
             __syncthreads();
         }
+        compute(s & 1);
+        __syncthreads();
     }
     if (const int left = nblk - stages * kStageBlocks) {
         // the last blocks: what lies past them is zero with scale 1
