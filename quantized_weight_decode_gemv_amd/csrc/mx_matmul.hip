@@ -6,7 +6,7 @@
 //
 // A workgroup holds BM x BN of C and walks n_in in stages of 256: 128 bytes of
 // codes and 8 of scales per row. Codes come by LDS DMA, a whole 128-byte line per
-// row, one stage ahead in the other of two buffers; the 16-byte granules of a row
+// row, into the other of two buffers; the 16-byte granules of a row
 // are permuted so that a tile's operand reads meet no bank twice. Lane l takes
 // the 32-value blocks 2(l/16), 2(l/16)+1 of a stage's eight: two products.
 //
@@ -51,7 +51,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mxfp4_matmul_kernel(MxMatmulArgs
                                                                     int out_tiles) {
     typedef typename Elem<TYPE>::T T;
     constexpr int BM = WM * TM * 16, BN = WN * TN * 16, R = BM + BN, W = WM * WN;
-    static_assert(BM % 64 == 0 && BN % 64 == 0 && TN % 4 == 0 && R <= W * 64, "tiles");
+    static_assert(BM % 64 == 0 && BN % 64 == 0 && TN % 4 == 0, "tiles");
     constexpr int kBuffer = R * kStageBytes + R * 8;  // codes [row][128], then scales
     extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63;
@@ -70,7 +70,8 @@ __global__ __launch_bounds__(WM * WN * 64) void mxfp4_matmul_kernel(MxMatmulArgs
         const int at = xcd * q + min(xcd, r) + (id >> 3);
         const int band = at / (8 * out_tiles), in = at - band * 8 * out_tiles;
         const int high = min(8, row_tiles - band * 8);
-        out_tile = in / high, row_tile = band * 8 + in % high;
+        out_tile = __builtin_amdgcn_readfirstlane(in / high);
+        row_tile = __builtin_amdgcn_readfirstlane(band * 8 + in % high);
     }
     const int64_t row0 = (int64_t)row_tile * BM, out0 = (int64_t)out_tile * BN;
     const uint8_t *a_codes = a.a + row0 * row_bytes, *w_codes = a.w + out0 * row_bytes;
@@ -95,78 +96,138 @@ __global__ __launch_bounds__(WM * WN * 64) void mxfp4_matmul_kernel(MxMatmulArgs
                   buf * kBuffer + r * kStageBytes);
         }
     };
-    // a thread's row of scales: eight bytes a stage at any alignment
-    const int sr = threadIdx.x;
-    const bool has_row = R == W * 64 || sr < R;
-    const uint8_t *scales = sr < BM ? a.a_scales + (row0 + min(sr, a_last)) * nblk
-                                    : a.w_scales + (out0 + min(sr - BM, w_last)) * nblk;
+    // a thread's rows of scales: eight bytes a stage at any alignment
+    constexpr int SR = (R + W * 64 - 1) / (W * 64);
+    const uint8_t *scales[SR];
+    bool has[SR];
+#pragma unroll
+    for (int k = 0; k < SR; ++k) {
+        const int sr = threadIdx.x + k * W * 64;
+        has[k] = R % (W * 64) == 0 || sr < R;
+        scales[k] = sr < BM ? a.a_scales + (row0 + min(sr, a_last)) * nblk
+                            : a.w_scales + (out0 + min(sr - BM, w_last)) * nblk;
+    }
+    struct Scales {
+        uint64_t v[SR];
+    };
     auto fetch_scales = [&](int s) {
-        uint64_t v = 0;
-        if (has_row) __builtin_memcpy(&v, scales + (int64_t)s * kStageBlocks, 8);
+        Scales v = {};
+#pragma unroll
+        for (int k = 0; k < SR; ++k)
+            if (has[k]) __builtin_memcpy(&v.v[k], scales[k] + (int64_t)s * kStageBlocks, 8);
         return v;
     };
     // [64-row group][lane group][lane % 16][tile] two bytes
-    auto put_scales = [&](uint64_t v, int buf) {
-        if (!has_row) return;
-        uint8_t *to = lds + buf * kBuffer + R * kStageBytes + (sr >> 6) * 512 +
-                      ((sr >> 4 & 3) * 4 + (sr & 3)) * 8 + (sr >> 2 & 3) * 2;
+    auto put_scales = [&](const Scales &v, int buf) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) *(uint16_t *)(to + h * 128) = (uint16_t)(v >> (16 * h));
+        for (int k = 0; k < SR; ++k) {
+            const int sr = threadIdx.x + k * W * 64;
+            uint8_t *to = lds + buf * kBuffer + R * kStageBytes + (sr >> 6) * 512 +
+                          ((sr >> 4 & 3) * 4 + (sr & 3)) * 8 + (sr >> 2 & 3) * 2;
+            if (has[k]) {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) *(uint16_t *)(to + h * 128) = (uint16_t)(v.v[k] >> (16 * h));
+            }
+        }
     };
-
+    const int key = (n & 3) | (n >> 2 & 1) << 2;
+    const int lane_row = (n >> 2) * 16 + (n & 3);
+    struct LaneScales {
+        u32x2 w[TN / 4], x[(TM + 3) / 4];
+    };
+    auto read_scales = [&](LaneScales &v, int buf) {
+        const uint8_t *sc = lds + buf * kBuffer + R * kStageBytes + g * 128 + n * 8;
+#pragma unroll
+        for (int i = 0; i < TN / 4; ++i) v.w[i] = *(const u32x2 *)(sc + (BM / 64 + wn * (TN / 4) + i) * 512);
+#pragma unroll
+        for (int j = 0; j < (TM + 3) / 4; ++j) v.x[j] = *(const u32x2 *)(sc + (wm * TM / 4 + j) * 512);
+        if constexpr (TM == 2) {  // half a group: its tiles are 0, 1 or 2, 3
+            if (wm & 1) v.x[0][0] = v.x[0][1];
+        }
+    };
+    const uint8_t *const base_w = lds + (BM + wn * TN * 16) * kStageBytes + lane_row * kStageBytes;
+    const uint8_t *const base_x = lds + (wm * TM / 4 * 64 + wm * TM % 4 * 4) * kStageBytes + lane_row * kStageBytes;
+    auto read_w = [&](u32x4(&w)[TN], int buf, int q) {
+        const uint8_t *p = base_w + buf * kBuffer + ((g * 2 + q) ^ key) * 16;
+#pragma unroll
+        for (int i = 0; i < TN; ++i) w[i] = *(const u32x4 *)(p + (i / 4 * 64 + i % 4 * 4) * kStageBytes);
+    };
+    auto read_x = [&](u32x4 &x, int buf, int q, int j) {
+        const uint8_t *p = base_x + buf * kBuffer + ((g * 2 + q) ^ key) * 16;
+        x = *(const u32x4 *)(p + (j / 4 * 64 + j % 4 * 4) * kStageBytes);
+    };
     f32x4 acc[TN][TM];
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
         for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-    const int key = (n & 3) | (n >> 2 & 1) << 2;
-    const int lane_row = (n >> 2) * 16 + (n & 3);
-    auto compute = [&](int buf) {
-        const uint8_t *codes = lds + buf * kBuffer, *sc = codes + R * kStageBytes + g * 128 + n * 8;
-        u32x2 ws[TN / 4], as[(TM + 3) / 4];
+    // A stage is 2 TM steps, each the products of one tile of A with TN of W. A
+    // step's operand is asked for kAhead steps before; `mid` comes when the last
+    // one has been, so that under the last steps' products the wavefronts meet,
+    // the buffer takes the stage after the next, and the next stage's first
+    // operands are on their way. The products touch no memory: only the
+    // scheduling barriers keep them in their steps.
+    constexpr int kSteps = 2 * TM, kAhead = TM < 4 ? 1 : 3, kRing = kAhead + 1;
+    static_assert(kSteps % kRing == 0, "ring");
+    u32x4 w0[TN], w1[TN], x[kRing];
+    LaneScales cur, ahead;
+    auto start = [&](int buf) {
+        read_scales(ahead, buf);
+        read_w(w0, buf, 0);
 #pragma unroll
-        for (int i = 0; i < TN / 4; ++i) ws[i] = *(const u32x2 *)(sc + (BM / 64 + wn * (TN / 4) + i) * 512);
-#pragma unroll
-        for (int j = 0; j < (TM + 3) / 4; ++j) as[j] = *(const u32x2 *)(sc + (wm * TM / 4 + j) * 512);
-        if constexpr (TM == 2) {  // half a group: its tiles are 0, 1 or 2, 3
-            if (wm & 1) as[0][0] = as[0][1];
-        }
-        each<2>([&](auto q) {
-            u32x4 w[TN], x[TM];
-            const int gran = ((g * 2 + q.v) ^ key) * 16;
-#pragma unroll
-            for (int i = 0; i < TN; ++i)
-                w[i] = *(const u32x4 *)(codes + (BM + (wn * TN + i) / 4 * 64 + (wn * TN + i) % 4 * 4 + lane_row) * kStageBytes + gran);
-#pragma unroll
-            for (int j = 0; j < TM; ++j)
-                x[j] = *(const u32x4 *)(codes + ((wm * TM + j) / 4 * 64 + (wm * TM + j) % 4 * 4 + lane_row) * kStageBytes + gran);
+        for (int t = 0; t < kAhead; ++t) read_x(x[t], buf, 0, t);
+    };
+    auto stage = [&](int buf, auto &&mid, auto more) {
+        cur = ahead;
+        each<kSteps>([&](auto t) {
+            constexpr int S = t.v, J = S % TM, N = S + kAhead;
+            if constexpr (N < kSteps) {
+                read_x(x[N % kRing], buf, N / TM, N % TM);
+                if constexpr (N == TM) read_w(w1, buf, 1);
+            } else {
+                if constexpr (N == kSteps) {
+                    mid();
+                    if constexpr (more.v) read_scales(ahead, buf ^ 1), read_w(w0, buf ^ 1, 0);
+                }
+                if constexpr (more.v) read_x(x[N % kRing], buf ^ 1, 0, N - kSteps);
+            }
+            __builtin_amdgcn_sched_barrier(0);
             each<TN>([&](auto i) {
-                each<TM>([&](auto j) {
-                    acc[i.v][j.v] = product<q.v, i.v, j.v>(w[i.v], x[j.v], ws[i.v / 4], as[j.v / 4], acc[i.v][j.v]);
-                });
+                acc[i.v][J] = product<S / TM, i.v, J>(S < TM ? w0[i.v] : w1[i.v], x[S % kRing],
+                                                      cur.w[i.v / 4], cur.x[J / 4], acc[i.v][J]);
             });
+            __builtin_amdgcn_sched_barrier(0);
         });
     };
 
     if (stages > 0) {
         issue(0, 0);
-        put_scales(fetch_scales(0), 0);
+        Scales next = fetch_scales(0);
         wait_vmcnt<0>();
+        put_scales(next, 0);
         __syncthreads();
-        int s = 0;
-        for (; s + 1 < stages; ++s) {
-            const int buf = s & 1;
-            const uint64_t next = fetch_scales(s + 1);
-            issue(s + 1, buf ^ 1);
-            compute(buf);
-            // the products, which touch no memory, must not sink below the wait
-            __builtin_amdgcn_sched_barrier(0);
-            wait_vmcnt<0>();
-            put_scales(next, buf ^ 1);
-            __syncthreads();
+        if (stages > 1) {
+            next = fetch_scales(1);
+            issue(1, 1);
         }
-        compute(s & 1);
-        __syncthreads();
+        start(0);
+        int s = 0;
+        auto meet = [&] {  // stage s + 1 has come, stage s's buffer is free
+            wait_vmcnt<0>();
+            put_scales(next, (s & 1) ^ 1);
+            __syncthreads();
+        };
+        for (; s + 2 < stages; ++s)
+            stage(s & 1, [&] {
+                meet();
+                next = fetch_scales(s + 2);
+                issue(s + 2, s & 1);
+            }, Int<1>{});
+        if (s + 1 < stages) {
+            stage(s & 1, meet, Int<1>{});
+            ++s;
+        }
+        stage(s & 1, [&] { __syncthreads(); }, Int<0>{});
     }
     if (const int left = nblk - stages * kStageBlocks) {
         // the last blocks: what lies past them is zero with scale 1
@@ -178,14 +239,17 @@ __global__ __launch_bounds__(WM * WN * 64) void mxfp4_matmul_kernel(MxMatmulArgs
             if (b < left) v = *(const u32x4 *)(p + (int64_t)stages * kStageBytes + b * kMxCodeBytes);
             *(u32x4 *)(lds + f * 16) = v;
         }
-        uint64_t v = 0x7f7f7f7f7f7f7f7full;
-        if (has_row) {
-            for (int b = 0; b < left; ++b)
-                v = (v & ~(255ull << (8 * b))) | (uint64_t)scales[stages * kStageBlocks + b] << (8 * b);
+        Scales v;
+#pragma unroll
+        for (int k = 0; k < SR; ++k) {
+            v.v[k] = 0x7f7f7f7f7f7f7f7full;
+            for (int b = 0; has[k] && b < left; ++b)
+                v.v[k] = (v.v[k] & ~(255ull << (8 * b))) | (uint64_t)scales[k][stages * kStageBlocks + b] << (8 * b);
         }
         put_scales(v, 0);
         __syncthreads();
-        compute(0);
+        start(0);
+        stage(0, [] {}, Int<0>{});
     }
 
 #pragma unroll
