@@ -71,22 +71,53 @@ __device__ __forceinline__ bf16x8 decode8(uint32_t c, float s) {
 // multiple of 1024, so that 16 columns' reads at one position meet no bank twice.
 __device__ __host__ __forceinline__ int pitch_of(int len) { return len * 2 + 16; }
 
+// Eight activations as they lie in memory.
 template <int TYPE>
-__device__ __forceinline__ void stage_parts(uint8_t *lds, int pitch, int row, int unit,
-                                            const float (&v)[8]) {
-    constexpr int P = Elem<TYPE>::pieces;
-    uint32_t w[3][4];
+struct Unit {
+    u32x4 w[TYPE == kF32 ? 2 : 1];
+};
+
+// Their bf16 parts, part p's eight values at to + p * pitch. Truncation, as
+// split3, but without its test: an infinity (its remainder would be a NaN) is
+// looked for in the whole unit and takes the other path.
+template <int TYPE>
+__device__ __forceinline__ void store_parts(uint8_t *to, int pitch, const Unit<TYPE> &u) {
+    if constexpr (TYPE == kBF16) {
+        *(u32x4 *)to = u.w[0];
+    } else {
+        constexpr int P = Elem<TYPE>::pieces;
+        float v[8], top = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        uint32_t h0, m0, l0, h1, m1, l1;
-        split3(v[2 * j], h0, m0, l0);
-        split3(v[2 * j + 1], h1, m1, l1);
-        w[0][j] = h0 | h1 << 16, w[1][j] = m0 | m1 << 16, w[2][j] = l0 | l1 << 16;
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (TYPE == kF32) v[e] = u2f(u.w[e / 4][e % 4]);
+            else v[e] = (float)__builtin_bit_cast(_Float16, (uint16_t)(u.w[0][e / 2] >> (e % 2 * 16)));
+            top = fmaxf(top, __builtin_fabsf(v[e]));
+        }
+        u32x4 w[P];
+        if (top == __builtin_inff()) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t a[3], b[3];
+                split3(v[2 * j], a[0], a[1], a[2]);
+                split3(v[2 * j + 1], b[0], b[1], b[2]);
+#pragma unroll
+                for (int p = 0; p < P; ++p) w[p][j] = a[p] | b[p] << 16;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float a = v[2 * j], b = v[2 * j + 1];
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    // the upper halves of a and b, and what they leave (a NaN leaves a NaN)
+                    w[p][j] = __builtin_amdgcn_perm(f2u(b), f2u(a), 0x07060302u);
+                    a -= u2f(f2u(a) & 0xffff0000u), b -= u2f(f2u(b) & 0xffff0000u);
+                }
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) *(u32x4 *)(to + p * pitch) = w[p];
     }
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-        *(u32x4 *)(lds + (row * P + p) * pitch + unit * 16) =
-            u32x4{w[p][0], w[p][1], w[p][2], w[p][3]};
 }
 
 // RT: row tiles that a wavefront takes together (one read of the activations
@@ -95,7 +126,7 @@ template <int TYPE, int NT, int RT, bool WORDS>
 __global__ __launch_bounds__(kMaxWaves(RT) * 64) void mxfp4_gemm_kernel(MxGemmArgs a, int wk, int chunk) {
     typedef typename Elem<TYPE>::T T;
     constexpr int P = Elem<TYPE>::pieces;
-    constexpr int kAhead = 2;  // activation units a thread loads before the first weights
+    constexpr int kBatch = TYPE == kF32 ? 3 : 6;  // activation units a thread has on the way
     extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int waves = blockDim.x >> 6, wr = waves / wk;
@@ -127,21 +158,29 @@ __global__ __launch_bounds__(kMaxWaves(RT) * 64) void mxfp4_gemm_kernel(MxGemmAr
         const int len = min(chunk, a.n_in - k0);
         const int steps = (len + kStep - 1) / kStep;
         const int units = steps * (kStep / 8), all = units * a.batch;
-        // The parts of every activation row, eight values a turn, zero past n_in.
-        // The first of them are asked for before the first weights, which take
-        // longer to come.
-        float v[kAhead][8];
-        auto fetch = [&](int i, float(&o)[8]) {
-            const int b = i / units, u = i - b * units;
+        // The activation rows of the chunk, eight values a unit, zero past n_in. The
+        // first of them are asked for before the first two steps' weights, which
+        // take longer to come.
+        Unit<TYPE> v[kBatch];
+        auto fetch = [&](int i0) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = 0;
-            if (i < all && u * 8 < len)
-                load8<T, true>((const T *)a.x + (int64_t)b * a.n_in + k0 + u * 8, o);
+            for (int h = 0; h < kBatch; ++h) {
+                const int i = i0 + h * blockDim.x, b = i / units, u = i - b * units;
+                v[h] = {};
+                if (i < all && u * 8 < len)
+                    v[h] = *(const Unit<TYPE> *)((const T *)a.x + (int64_t)b * a.n_in + k0 + u * 8);
+            }
         };
+        auto put = [&](int i0) {
 #pragma unroll
-        for (int h = 0; h < kAhead; ++h) fetch(threadIdx.x + h * blockDim.x, v[h]);
+            for (int h = 0; h < kBatch; ++h) {
+                const int i = i0 + h * blockDim.x, b = i / units, u = i - b * units;
+                if (i < all) store_parts<TYPE>(lds + b * P * pitch + u * 16, pitch, v[h]);
+            }
+        };
+        fetch(threadIdx.x);
         int st = kw;
-        Codes cur[RT];
+        Codes cur[RT], next[RT];
         auto load = [&](Codes(&c)[RT], int s) {
 #pragma unroll
             for (int r = 0; r < RT; ++r)
@@ -149,20 +188,15 @@ __global__ __launch_bounds__(kMaxWaves(RT) * 64) void mxfp4_gemm_kernel(MxGemmAr
                                   k0 / kMxBlock + s * kStepBlocks + g * 4, nblk);
         };
         if (st < steps) load(cur, st);
+        if (st + wk < steps) load(next, st + wk);
         if (k0) __syncthreads();
-#pragma unroll
-        for (int h = 0; h < kAhead; ++h) {
-            const int i = threadIdx.x + h * blockDim.x;
-            if (i < all) stage_parts<TYPE>(lds, pitch, i / units, i % units, v[h]);
-        }
-        for (int i = threadIdx.x + kAhead * blockDim.x; i < all; i += blockDim.x) {
-            fetch(i, v[0]);
-            stage_parts<TYPE>(lds, pitch, i / units, i % units, v[0]);
+        put(threadIdx.x);
+        for (int i = threadIdx.x + kBatch * blockDim.x; i < all; i += kBatch * blockDim.x) {
+            fetch(i);
+            put(i);
         }
         __syncthreads();
         for (; st < steps; st += wk) {
-            Codes next[RT];
-            if (st + wk < steps) load(next, st + wk);
             const int at = (st * kStepBlocks + g * 4) * kMxBlock * 2;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -186,6 +220,7 @@ __global__ __launch_bounds__(kMaxWaves(RT) * 64) void mxfp4_gemm_kernel(MxGemmAr
             }
 #pragma unroll
             for (int r = 0; r < RT; ++r) cur[r] = next[r];
+            if (st + 2 * wk < steps) load(next, st + 2 * wk);
         }
     }
     // every wavefront's sums meet in LDS: [wave][row tile][column][row]
@@ -227,6 +262,7 @@ hipError_t launch(const MxGemmArgs &a, int wr, hipStream_t s) {
     int wk = kMaxWaves(RT) / wr;
     if (wk > steps) wk = steps;
     int chunk = kLdsX / (a.batch * P) / 2 / kStep * kStep;
+    if (chunk > wk * kStep) chunk = chunk / (wk * kStep) * (wk * kStep);  // every wavefront's turn
     if (chunk > steps * kStep) chunk = steps * kStep;
     size_t lds = (size_t)a.batch * P * pitch_of(chunk);
     const size_t join = (size_t)wk * wr * RT * NT * 16 * 16 * 4;
