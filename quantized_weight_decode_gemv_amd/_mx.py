@@ -25,19 +25,26 @@ class Kv8Desc(ctypes.Structure):
                 ("head_dim", ctypes.c_int), ("page_tokens", ctypes.c_int)]
 
 
+_Tensor = torch.Tensor
+_U8, _I32 = torch.uint8, torch.int32
+
+
 def _on_device(t, name: str, device=None) -> None:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a tensor on a HIP device")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
 def _plain(t, name: str, dtype, device=None) -> None:
+    # one expression for the usual case: a small call's time is the host's
+    if (isinstance(t, _Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (device is None or t.device == device)):
+        return
     _on_device(t, name, device)
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _type(dtype, name: str) -> int:
@@ -47,9 +54,10 @@ def _type(dtype, name: str) -> int:
     return code
 
 
-# The current stream's handle without a Stream object, which torch.cuda.current_stream builds in
-# 1.9 us: a sixth of a small call's 11 us on the host.
+# torch's own accessors of the current device and of a stream's handle; torch.cuda's build a
+# Stream object (1.9 us of a small call's 11 on the host).
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _fns: dict = {}
 
 
@@ -59,7 +67,7 @@ def _run(fn: str, device, *args) -> None:
     if f is None:
         f = _fns[fn] = getattr(lib(), fn)
     index = device.index
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         rc = f(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
@@ -70,12 +78,12 @@ def _run(fn: str, device, *args) -> None:
 
 def _matrix(codes, scales, name: str, device=None):
     """Rows and columns of an MXFP4 matrix: codes uint8 [rows, n_in/2], scales uint8 [rows, n_in/32]."""
-    _plain(codes, name, torch.uint8, device)
+    _plain(codes, name, _U8, device)
     shape = codes.shape
     if len(shape) != 2 or shape[0] < 1 or shape[1] < 16 or shape[1] % 16:
         raise ValueError(f"{name} must be [rows, n_in/2] with n_in a positive multiple of 32")
     rows, half = shape
-    _plain(scales, "scales", torch.uint8, codes.device)
+    _plain(scales, "scales", _U8, codes.device)
     if scales.shape != (rows, half // 16):
         raise ValueError(f"the scales of {name} must be [{rows}, {half // 16}], got {list(scales.shape)}")
     return rows, half * 2
@@ -183,10 +191,10 @@ def kv8_pages(n_pages: int, n_kv_heads: int, head_dim: int, page_tokens: int = 6
 
 
 def _cache(k_pages, k_scales, v_pages, v_scales, device) -> Kv8Desc:
-    _plain(k_pages, "k_pages", torch.uint8, device)
-    _plain(v_pages, "v_pages", torch.uint8, device)
-    _plain(k_scales, "k_scales", torch.uint8, device)
-    _plain(v_scales, "v_scales", torch.uint8, device)
+    _plain(k_pages, "k_pages", _U8, device)
+    _plain(v_pages, "v_pages", _U8, device)
+    _plain(k_scales, "k_scales", _U8, device)
+    _plain(v_scales, "v_scales", _U8, device)
     if k_pages.dim() != 4:
         raise ValueError("k_pages must be [n_pages, n_kv_heads, page_tokens, head_dim]")
     n_pages, heads, page, dim = k_pages.shape
@@ -201,8 +209,8 @@ def _cache(k_pages, k_scales, v_pages, v_scales, device) -> Kv8Desc:
 
 
 def _sequences(table, lens, device):
-    _plain(table, "table", torch.int32, device)
-    _plain(lens, "lens", torch.int32, device)
+    _plain(table, "table", _I32, device)
+    _plain(lens, "lens", _I32, device)
     if table.dim() != 2 or table.shape[0] < 1 or table.shape[1] < 1:
         raise ValueError("table must be [n_seqs, pages]")
     if lens.shape != (table.shape[0],):
@@ -212,18 +220,19 @@ def _sequences(table, lens, device):
 
 def _tokens(x, name: str, heads: int, dim: int):
     """Tokens and token stride of [tokens, heads, dim] or [n_seqs, tokens, heads, dim]."""
-    if x.dim() not in (3, 4) or x.shape[-2:] != (heads, dim):
+    shape, strides = x.shape, x.stride()
+    if len(shape) not in (3, 4) or shape[-2] != heads or shape[-1] != dim:
         raise ValueError(f"{name} must be [tokens, {heads}, {dim}] or [n_seqs, tokens, {heads}, {dim}]")
-    if x.stride(-1) != 1 or (heads > 1 and x.stride(-2) != dim):
+    if strides[-1] != 1 or (heads > 1 and strides[-2] != dim):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    stride = x.stride(-3)
-    n = x.shape[0]
-    if x.dim() == 4:
-        n *= x.shape[1]
-        if x.shape[1] == 1:
-            stride = x.stride(0)
-        elif x.shape[0] > 1 and x.stride(0) != x.shape[1] * stride:
+    n, stride = shape[0], strides[-3]
+    if len(shape) == 4:
+        each = shape[1]
+        if each == 1:
+            stride = strides[0]
+        elif n > 1 and strides[0] != each * stride:
             raise ValueError(f"the tokens of {name} must lie at one distance")
+        n *= each
     if n > 1 and stride < heads * dim:
         raise ValueError(f"the tokens of {name} must not overlap")
     return n, stride
@@ -257,7 +266,7 @@ def kv8_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, k_scales
             raise ValueError(f"{n} tokens are not as many for each of {n_seqs} sequences")
         most = n // n_seqs
     else:
-        _plain(starts, "starts", torch.int32, k.device)
+        _plain(starts, "starts", _I32, k.device)
         if starts.shape != (n_seqs + 1,):
             raise ValueError(f"starts must be [{n_seqs + 1}]")
         most = n if max_new is None else max_new
