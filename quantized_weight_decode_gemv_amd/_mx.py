@@ -106,14 +106,17 @@ def encode_mxfp4(x: torch.Tensor, codes: torch.Tensor | None = None,
     columns) -> MXFP4 (codes uint8 [rows, n_in/2], scales uint8 [rows, n_in/32])."""
     _on_device(x, "x")
     kind = _type(x.dtype, "x")
-    if x.dim() != 2 or x.shape[0] < 1 or x.shape[1] < MX_BLOCK or x.shape[1] % MX_BLOCK:
+    shape = x.shape
+    if len(shape) != 2 or shape[0] < 1 or shape[1] < MX_BLOCK or shape[1] % MX_BLOCK:
         raise ValueError("x must be [rows, n_in] with n_in a positive multiple of 32")
-    rows, n_in = x.shape
-    stride = x.stride(0) if rows > 1 else n_in
-    if x.stride(1) != 1 or stride < n_in:
+    rows, n_in = shape
+    stride, each = x.stride()
+    if rows == 1:
+        stride = n_in
+    if each != 1 or stride < n_in:
         raise ValueError("the values of a row of x must be contiguous, and rows must not overlap")
-    codes = _out(codes, (rows, n_in // 2), x, "codes", torch.uint8)
-    scales = _out(scales, (rows, n_in // MX_BLOCK), x, "scales", torch.uint8)
+    codes = _out(codes, (rows, n_in // 2), x, "codes", _U8)
+    scales = _out(scales, (rows, n_in // MX_BLOCK), x, "scales", _U8)
     _run("qwg_encode_mxfp4", x.device, codes.data_ptr(), scales.data_ptr(), x.data_ptr(), kind,
          rows, n_in, stride)
     return codes, scales
@@ -137,13 +140,15 @@ def gemm_mxfp4(w: torch.Tensor, scales: torch.Tensor, x: torch.Tensor,
     n_out, n_in = _matrix(w, scales, "w")
     _on_device(x, "x", w.device)
     kind = _type(x.dtype, "x")
-    if x.dim() != 2 or not 1 <= x.shape[0] <= MX_MAX_BATCH or x.shape[1] != n_in:
+    shape = x.shape
+    if len(shape) != 2 or not 1 <= shape[0] <= MX_MAX_BATCH or shape[1] != n_in:
         raise ValueError(f"x must be [batch, {n_in}] with 1 <= batch <= {MX_MAX_BATCH}")
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
-    out = _out(out, (x.shape[0], n_out), x)
+    batch = shape[0]
+    out = _out(out, (batch, n_out), x)
     _run("qwg_gemm_mxfp4", x.device, out.data_ptr(), x.data_ptr(), kind, w.data_ptr(),
-         scales.data_ptr(), n_in, n_out, x.shape[0])
+         scales.data_ptr(), n_in, n_out, batch)
     return out
 
 
@@ -195,14 +200,15 @@ def _cache(k_pages, k_scales, v_pages, v_scales, device) -> Kv8Desc:
     _plain(v_pages, "v_pages", _U8, device)
     _plain(k_scales, "k_scales", _U8, device)
     _plain(v_scales, "v_scales", _U8, device)
-    if k_pages.dim() != 4:
+    shape = k_pages.shape
+    if len(shape) != 4:
         raise ValueError("k_pages must be [n_pages, n_kv_heads, page_tokens, head_dim]")
-    n_pages, heads, page, dim = k_pages.shape
+    n_pages, heads, page, dim = shape
     if dim not in KV8_HEAD_DIMS or page not in KV8_PAGE_TOKENS:
         raise ValueError(f"head_dim must be one of {KV8_HEAD_DIMS} and page_tokens of {KV8_PAGE_TOKENS}")
     if v_pages.shape != (n_pages, heads, dim, page):
         raise ValueError(f"v_pages must be [{n_pages}, {heads}, {dim}, {page}]")
-    if k_scales.shape != (n_pages, heads) or v_scales.shape != (n_pages, heads):
+    if k_scales.shape != shape[:2] or v_scales.shape != shape[:2]:
         raise ValueError(f"k_scales and v_scales must be [{n_pages}, {heads}]")
     return Kv8Desc(k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
                    n_pages, heads, dim, page)
@@ -211,11 +217,12 @@ def _cache(k_pages, k_scales, v_pages, v_scales, device) -> Kv8Desc:
 def _sequences(table, lens, device):
     _plain(table, "table", _I32, device)
     _plain(lens, "lens", _I32, device)
-    if table.dim() != 2 or table.shape[0] < 1 or table.shape[1] < 1:
+    shape = table.shape
+    if len(shape) != 2 or shape[0] < 1 or shape[1] < 1:
         raise ValueError("table must be [n_seqs, pages]")
-    if lens.shape != (table.shape[0],):
-        raise ValueError(f"lens must be [{table.shape[0]}]")
-    return table.shape
+    if lens.shape != shape[:1]:
+        raise ValueError(f"lens must be [{shape[0]}]")
+    return shape
 
 
 def _tokens(x, name: str, heads: int, dim: int):

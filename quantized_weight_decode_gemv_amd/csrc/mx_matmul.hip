@@ -51,7 +51,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mxfp4_matmul_kernel(MxMatmulArgs
                                                                     int out_tiles) {
     typedef typename Elem<TYPE>::T T;
     constexpr int BM = WM * TM * 16, BN = WN * TN * 16, R = BM + BN, W = WM * WN;
-    static_assert(BM % 64 == 0 && BN % 64 == 0 && TN % 4 == 0, "tiles");
+    static_assert(BM % 64 == 0 && BN % 64 == 0 && TN % 4 == 0 && R <= W * 64, "tiles");
     constexpr int kBuffer = R * kStageBytes + R * 8;  // codes [row][128], then scales
     extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63;
@@ -96,38 +96,23 @@ __global__ __launch_bounds__(WM * WN * 64) void mxfp4_matmul_kernel(MxMatmulArgs
                   buf * kBuffer + r * kStageBytes);
         }
     };
-    // a thread's rows of scales: eight bytes a stage at any alignment
-    constexpr int SR = (R + W * 64 - 1) / (W * 64);
-    const uint8_t *scales[SR];
-    bool has[SR];
-#pragma unroll
-    for (int k = 0; k < SR; ++k) {
-        const int sr = threadIdx.x + k * W * 64;
-        has[k] = R % (W * 64) == 0 || sr < R;
-        scales[k] = sr < BM ? a.a_scales + (row0 + min(sr, a_last)) * nblk
-                            : a.w_scales + (out0 + min(sr - BM, w_last)) * nblk;
-    }
-    struct Scales {
-        uint64_t v[SR];
-    };
+    // a thread's row of scales: eight bytes a stage at any alignment
+    const int sr = threadIdx.x;
+    const bool has_row = R == W * 64 || sr < R;
+    const uint8_t *scales = sr < BM ? a.a_scales + (row0 + min(sr, a_last)) * nblk
+                                    : a.w_scales + (out0 + min(sr - BM, w_last)) * nblk;
     auto fetch_scales = [&](int s) {
-        Scales v = {};
-#pragma unroll
-        for (int k = 0; k < SR; ++k)
-            if (has[k]) __builtin_memcpy(&v.v[k], scales[k] + (int64_t)s * kStageBlocks, 8);
+        uint64_t v = 0;
+        if (has_row) __builtin_memcpy(&v, scales + (int64_t)s * kStageBlocks, 8);
         return v;
     };
     // [64-row group][lane group][lane % 16][tile] two bytes
-    auto put_scales = [&](const Scales &v, int buf) {
+    auto put_scales = [&](uint64_t v, int buf) {
+        uint8_t *to = lds + buf * kBuffer + R * kStageBytes + (sr >> 6) * 512 +
+                      ((sr >> 4 & 3) * 4 + (sr & 3)) * 8 + (sr >> 2 & 3) * 2;
+        if (has_row) {
 #pragma unroll
-        for (int k = 0; k < SR; ++k) {
-            const int sr = threadIdx.x + k * W * 64;
-            uint8_t *to = lds + buf * kBuffer + R * kStageBytes + (sr >> 6) * 512 +
-                          ((sr >> 4 & 3) * 4 + (sr & 3)) * 8 + (sr >> 2 & 3) * 2;
-            if (has[k]) {
-#pragma unroll
-                for (int h = 0; h < 4; ++h) *(uint16_t *)(to + h * 128) = (uint16_t)(v.v[k] >> (16 * h));
-            }
+            for (int h = 0; h < 4; ++h) *(uint16_t *)(to + h * 128) = (uint16_t)(v >> (16 * h));
         }
     };
     const int key = (n & 3) | (n >> 2 & 1) << 2;
@@ -202,7 +187,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mxfp4_matmul_kernel(MxMatmulArgs
 
     if (stages > 0) {
         issue(0, 0);
-        Scales next = fetch_scales(0);
+        uint64_t next = fetch_scales(0);
         wait_vmcnt<0>();
         put_scales(next, 0);
         __syncthreads();
@@ -239,13 +224,9 @@ __global__ __launch_bounds__(WM * WN * 64) void mxfp4_matmul_kernel(MxMatmulArgs
             if (b < left) v = *(const u32x4 *)(p + (int64_t)stages * kStageBytes + b * kMxCodeBytes);
             *(u32x4 *)(lds + f * 16) = v;
         }
-        Scales v;
-#pragma unroll
-        for (int k = 0; k < SR; ++k) {
-            v.v[k] = 0x7f7f7f7f7f7f7f7full;
-            for (int b = 0; has[k] && b < left; ++b)
-                v.v[k] = (v.v[k] & ~(255ull << (8 * b))) | (uint64_t)scales[k][stages * kStageBlocks + b] << (8 * b);
-        }
+        uint64_t v = 0x7f7f7f7f7f7f7f7full;
+        for (int b = 0; has_row && b < left; ++b)
+            v = (v & ~(255ull << (8 * b))) | (uint64_t)scales[stages * kStageBlocks + b] << (8 * b);
         put_scales(v, 0);
         __syncthreads();
         start(0);
