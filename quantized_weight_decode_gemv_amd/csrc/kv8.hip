@@ -240,7 +240,11 @@ constexpr int waves_of(int d, int r) { return d == 128 && r == 2 ? 8 : 4; }
 //
 // Queries and probabilities enter as bf16 parts (one to three) that hold all
 // their bits, or 16 of the probabilities' for the 16-bit types; e4m3 is exact in bf16.
-template <int TYPE, int D, int R, int W>
+//
+// ONCE: this workgroup takes all rows of its key/value head, whose lines are then
+// read once (with the hint 32 ragged sequences of up to 8192 positions took 60 us,
+// without it 68; three row tiles, which share the lines, 61 and 56).
+template <int TYPE, int D, int R, int W, bool ONCE>
 __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
     typedef typename Elem<TYPE>::T T;
     constexpr int PQ = Elem<TYPE>::pieces;      // parts of a query
@@ -350,6 +354,7 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
         else if constexpr (D == 96) return a1;
         else return b >> 1 | a1 << 1;
     };
+    auto dma = [](const uint8_t *p, uint32_t to) { ONCE ? dma16_once(p, to) : dma16(p, to); };
     auto issue_k = [&](int b0) {
         const uint8_t *base[4];
 #pragma unroll
@@ -360,7 +365,7 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
             const int f = i * 64 + lane, r = f / C, s = f - r * C;
             const int q0 = i * 64 / (16 * C), q1 = (i * 64 + 63) / (16 * C);
             const uint8_t *p = q0 == q1 || f < q1 * 16 * C ? base[q0] : base[q1];
-            dma16(p + (r & 15) * D + (s ^ k_key(r & 3, (r >> 4) & 1)) * 16, zone + i * 1024);
+            dma(p + (r & 15) * D + (s ^ k_key(r & 3, (r >> 4) & 1)) * 16, zone + i * 1024);
         }
     };
     // V in LDS: [16-position pieces that lie in other pages][channel][pieces of
@@ -377,7 +382,7 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
             const uint8_t *p = page_base(c.v, pos) + (pos & (c.page - 1));
             for (int i = 0; i < v_runs; ++i, to += 1024) {
                 const int d = min(d0 + i * (64 >> pg_log), D - 1);
-                dma16(p + d * c.page, to);
+                dma(p + d * c.page, to);
             }
         }
     };
@@ -687,7 +692,15 @@ hipError_t attend(const Kv8AttendArgs &a, hipStream_t s) {
     constexpr size_t join = (size_t)W * R * 16 * (D + 4 + 2) * 4;
     static_assert(work <= 160 * 1024 && join <= 160 * 1024, "LDS");
     const dim3 grid(a.max_splits, a.cache.n_kv * tiles, (unsigned)a.n_seqs);
-    kv8_attend_kernel<TYPE, D, R, W><<<grid, W * 64, work > join ? work : join, s>>>(a);
+    const size_t lds = work > join ? work : join;
+    if constexpr (R == 1 && D <= 128) {  // (16 rows at most)
+        kv8_attend_kernel<TYPE, D, R, W, true><<<grid, W * 64, lds, s>>>(a);
+    } else {
+        if (tiles == 1)
+            kv8_attend_kernel<TYPE, D, R, W, true><<<grid, W * 64, lds, s>>>(a);
+        else
+            kv8_attend_kernel<TYPE, D, R, W, false><<<grid, W * 64, lds, s>>>(a);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.max_splits == 1) return e;
     kv8_join_kernel<TYPE, D><<<dim3(a.q_len * a.n_heads, (unsigned)a.n_seqs), 256, 0, s>>>(a);

@@ -16,7 +16,13 @@ __device__ __forceinline__ void dma16(const void *g, uint32_t lds) {
     asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(lds), "v"(g) : "memory");
 }
 
-// The same from a wavefront-uniform base and a byte offset per lane.
+// The same for lines that no other workgroup reads: the non-temporal hint keeps
+// them out of the way of what is read again.
+__device__ __forceinline__ void dma16_once(const void *g, uint32_t lds) {
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %1, off nt" ::"{m0}"(lds), "v"(g) : "memory");
+}
+
+// The same as dma16 from a wavefront-uniform base and a byte offset per lane.
 __device__ __forceinline__ void dma16(const void *base, uint32_t offset, uint32_t lds) {
     // (readfirstlane returns int: widen through uint32_t, never by sign extension)
     const uint64_t p = (uint64_t)(uintptr_t)base;
