@@ -217,7 +217,9 @@ constexpr int k_zone(int d) { return d * kBlk; }
 constexpr int v_zone(int d) { return (d == 96 ? 128 : d) * kBlk; }
 // Wavefronts of a workgroup: four, two such workgroups to a compute unit (one's
 // start and end then overlap the other's middle); eight for two tiles of 128
-// channels, whose Q would not fit twice.
+// channels, whose Q would not fit twice, and where every workgroup has a compute
+// unit to itself and takes a whole sequence (one of 517 positions, 4 heads of 64:
+// 10.0 us with four, 8.3 with eight, 8.7 with sixteen).
 constexpr int waves_of(int d, int r) { return d == 128 && r == 2 ? 8 : 4; }
 
 // One workgroup: one split (`chunk` positions) of one sequence, one key/value
@@ -683,9 +685,11 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8AttendArgs a) {
     }
 }
 
-template <int TYPE, int D, int R>
+template <int TYPE, int D, int R, int W = waves_of(D, R)>
 hipError_t attend(const Kv8AttendArgs &a, hipStream_t s) {
-    constexpr int W = waves_of(D, R);
+    if constexpr (D <= 128 && W == 4) {
+        if (a.few) return attend<TYPE, D, R, 8>(a, s);
+    }
     const int rows = a.q_len * (a.n_heads / a.cache.n_kv);
     const int tiles = (rows + 16 * R - 1) / (16 * R);
     constexpr size_t work = q_bytes(TYPE, D, R) + kPageBytes + W * (k_zone(D) + v_zone(D));
@@ -757,7 +761,10 @@ hipError_t launch_kv8_append(const Kv8AppendArgs &a, int type, hipStream_t s) {
 // heads of 128: 79 us in half a round, 73 us in four, 78 in sixteen; one of
 // 131,071, 4 tokens of 64 heads: 65 us in one round, 76 in two, 104 in eight,
 // more partial sums). Up to 1024 positions stay whole: the launch that joins
-// splits costs as much as three more turns of a workgroup.
+// splits costs as much as two more turns of a workgroup (64 ragged sequences of up
+// to 900, 8 heads of 128: 22 us whole, 35 in splits of 256), unless a workgroup of
+// four wavefronts would take more than two turns with three quarters of the compute
+// units idle (900 positions, 4 heads of 256: 19.4 us whole, 12.3 in splits of 256).
 void kv8_attend_plan(Kv8AttendArgs &a, int64_t max_len, int cus) {
     const int rows = a.q_len * (a.n_heads / a.cache.n_kv);
     const int64_t cap = a.width * a.cache.page;
@@ -768,10 +775,12 @@ void kv8_attend_plan(Kv8AttendArgs &a, int64_t max_len, int cus) {
     const int64_t want = ((a.n_seqs > 1 ? 4 : 1) * resident + groups - 1) / groups;
     int64_t chunk = (max_len + want - 1) / want;
     chunk = (chunk + 255) / 256 * 256;
-    if (cap <= 1024) chunk = 1024;
+    const bool idle = a.cache.dim > 128 && groups * 4 <= cus;
+    if (cap <= (idle ? 512 : 1024)) chunk = 1024;
     if (chunk > kMaxChunk) chunk = kMaxChunk;
     a.chunk = (int)chunk;
     a.max_splits = (int)((cap + chunk - 1) / chunk);
+    a.few = a.max_splits == 1 && groups <= cus;
 }
 
 int64_t kv8_attend_partial_bytes(const Kv8AttendArgs &a) {

@@ -201,6 +201,44 @@ def test_attend_long_and_split(t, dim, page, length):
 
 
 @pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("dim,page,kv,group,q_len", [(64, 16, 1, 4, 1), (64, 32, 1, 17, 1), (96, 64, 1, 2, 9), (128, 16, 2, 4, 1)])
+def test_attend_many_short_sequences(t, dim, page, kv, group, q_len):
+    rng = np.random.default_rng(dim * group)
+    lens = rng.integers(0, 300, 300).astype(np.int32)
+    c, table = filled(rng, lens, kv, dim, page)
+    q, qd = typed(rng.standard_normal((300, q_len, kv * group, dim)), t)
+    out = qwg.kv8_attend(q, *pages(c), dev(table), dev(lens))
+    assert_attend(out, *ref.attend(qd, c, table, lens, dim ** -0.5, 0), t, dim)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("length", [512, 513, 1008, 1024, 1025])
+def test_attend_one_sequence_around_the_first_split(dim, length):
+    rng = np.random.default_rng(dim + length)
+    lens = np.array([length], np.int32)
+    c, table = filled(rng, lens, 2, dim, 16)
+    table = table[:, :-(-length // 16)]
+    q, qd = typed(rng.standard_normal((1, 1, 6, dim)), torch.bfloat16)
+    out = qwg.kv8_attend(q, *pages(c), dev(table), dev(lens))
+    assert_attend(out, *ref.attend(qd, c, table, lens, dim ** -0.5, 0), torch.bfloat16, dim)
+
+
+@pytest.mark.parametrize("t", TYPES)
+def test_attend_nan_in_a_query_stays_in_its_row(t):
+    rng = np.random.default_rng(12)
+    lens = np.array([90, 5], np.int32)
+    c, table = filled(rng, lens, 2, 64, 16)
+    q, qd = typed(rng.standard_normal((2, 3, 8, 64)), t)
+    want, weight, size = ref.attend(qd, c, table, lens, 0.125, 0)
+    q[0, 1, 2, 7], q[1, 2, 5, 0] = float("nan"), float("inf")
+    out = qwg.kv8_attend(q, *pages(c), dev(table), dev(lens))
+    for at in ((0, 1, 2), (1, 2, 5)):
+        assert torch.isnan(out[at]).all()
+        out[at] = torch.from_numpy(want[at]).to(out)  # the others are as they were
+    assert_attend(out, want, weight, size, t, 64)
+
+
+@pytest.mark.parametrize("t", TYPES)
 @pytest.mark.parametrize("size", [30.0, 3000.0])
 def test_attend_sharp_softmax_and_slices(t, size):
     # scores far apart: one position takes all, and the row maximum changes from block to block
