@@ -644,7 +644,7 @@ int qwg_kv8_append(const qwg_kv8 *cache, const void *k, const void *v, int type,
                    const int32_t *table, int64_t table_width, const int32_t *lens, int64_t n_seqs,
                    int64_t max_new, void *stream);
 int64_t qwg_kv8_attend_workspace(const qwg_kv8 *cache, int64_t table_width, int64_t n_seqs,
-                                 int q_len, int n_heads, int64_t max_len);
+                                 int q_len, int n_heads, int64_t window, int64_t max_len);
 int qwg_kv8_attend(const qwg_kv8 *cache, void *out, const void *q, int type, int64_t q_stride,
                    const int32_t *table, int64_t table_width, const int32_t *lens, int64_t n_seqs,
                    int q_len, int n_heads, float scale, int64_t window, int64_t max_len,

@@ -110,7 +110,7 @@ def lib() -> ctypes.CDLL:
         L.qwg_gemm_mxfp4.argtypes = [P, P, I, P, P, I64, I64, I, P]
         L.qwg_matmul_mxfp4.argtypes = [P, I, P, P, P, P, I64, I64, I64, P]
         L.qwg_kv8_append.argtypes = [P, P, P, I, I64, I64, I64, P, P, I64, P, I64, I64, P]
-        L.qwg_kv8_attend_workspace.argtypes = [P, I64, I64, I, I, I64]
+        L.qwg_kv8_attend_workspace.argtypes = [P, I64, I64, I, I, I64, I64]
         L.qwg_kv8_attend.argtypes = [P, P, P, I, I64, P, I64, P, I64, I, I, ctypes.c_float, I64, I64,
                                      P, I64, P]
         for f in ("qwg_encode_mxfp4", "qwg_dequant_mxfp4", "qwg_gemv_mxfp4", "qwg_gemm_mxfp4",

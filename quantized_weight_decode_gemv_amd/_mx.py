@@ -312,7 +312,7 @@ def kv8_attend(q: torch.Tensor, k_pages: torch.Tensor, k_scales: torch.Tensor,
     out = _out(out, q.shape, q)
     most = max_len or 0
     ref = ctypes.byref(cache)
-    size = lib().qwg_kv8_attend_workspace(ref, width, n_seqs, q_len, heads, most)
+    size = lib().qwg_kv8_attend_workspace(ref, width, n_seqs, q_len, heads, window, most)
     if size < 0:
         _check(-size, "qwg_kv8_attend_workspace")
     # of this call's stream (or of the graph that captures it): no two calls share one

@@ -8,6 +8,8 @@
 // [n_kv][dim][page]: attention's second product sums over positions, and with
 // consecutive positions of a channel in consecutive bytes both products take
 // their operands from memory as they lie.
+#include <algorithm>
+
 #include "mx_device.h"
 #include "mx_lds.h"
 
@@ -202,6 +204,12 @@ __device__ __forceinline__ uint32_t upper_halves(float a, float b) {
     return __builtin_amdgcn_perm(f2u(b), f2u(a), 0x07060302u);
 }
 
+// The block of positions that the first row's window starts in: what some row
+// sees is from there to the end, and the splits begin there.
+__device__ __forceinline__ int first_seen(int len, int q_len, int window) {
+    return window > 0 ? max(0, len - q_len + 1 - window) & -kBlk : 0;
+}
+
 // Floats of one split's partial result: rows of D sums, then a (maximum, total)
 // pair per row, in whole 16 bytes.
 __device__ __host__ __forceinline__ int64_t partial_floats(int64_t rows, int dim) {
@@ -268,14 +276,12 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
     const int len0 = a.lens[seq], cap = (int)a.width << shift;
     const bool bad = len0 < 0 || len0 > cap;  // no such length: the rows become NaN
     const int len = bad ? 0 : len0;
-    const int splits = max(1, (len + a.chunk - 1) / a.chunk);
+    const int window = (int)min(a.window, (int64_t)1 << 30);  // 0: all
+    const int low = first_seen(len, a.q_len, window);
+    const int splits = max(1, (len - low + a.chunk - 1) / a.chunk);
     const int split = blockIdx.x;
     if (split >= splits) return;
-    const int window = (int)min(a.window, (int64_t)1 << 30);  // 0: all
-    // positions that some row sees: those below len, from the first row's window on
-    const int low = window > 0 ? max(0, len - a.q_len + 1 - window) : 0;
-    const int begin = max(split * a.chunk, low & -kBlk);
-    const int end = min((split + 1) * a.chunk, len);
+    const int begin = low + split * a.chunk, end = min(begin + a.chunk, len);
 
     extern __shared__ __align__(16) uint8_t lds[];
     uint8_t *const q_lds = lds;
@@ -647,7 +653,8 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8AttendArgs a) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int len0 = a.lens[seq];
     const int len = len0 < 0 || len0 > a.width * a.cache.page ? 0 : len0;
-    const int splits = max(1, (len + a.chunk - 1) / a.chunk);
+    const int low = first_seen(len, a.q_len, (int)min(a.window, (int64_t)1 << 30));
+    const int splits = max(1, (len - low + a.chunk - 1) / a.chunk);
     if (splits == 1) return;
     const int64_t rows = (int64_t)a.q_len * a.n_heads, each = partial_floats(rows, D);
     const float *part = a.partial + seq * a.max_splits * each;
@@ -767,7 +774,9 @@ hipError_t launch_kv8_append(const Kv8AppendArgs &a, int type, hipStream_t s) {
 // units idle (900 positions, 4 heads of 256: 19.4 us whole, 12.3 in splits of 256).
 void kv8_attend_plan(Kv8AttendArgs &a, int64_t max_len, int cus) {
     const int rows = a.q_len * (a.n_heads / a.cache.n_kv);
-    const int64_t cap = a.width * a.cache.page;
+    // positions that a sequence's rows see together, at most and as far as known
+    int64_t cap = a.width * a.cache.page;
+    if (a.window > 0 && a.window < cap) cap = std::min(cap, a.window + a.q_len + kBlk - 2);
     if (max_len <= 0 || max_len > cap) max_len = cap;
     const int r = row_tiles(rows, a.cache.dim);
     const int64_t groups = a.n_seqs * a.cache.n_kv * ((rows + 16 * r - 1) / (16 * r));
@@ -776,11 +785,11 @@ void kv8_attend_plan(Kv8AttendArgs &a, int64_t max_len, int cus) {
     int64_t chunk = (max_len + want - 1) / want;
     chunk = (chunk + 255) / 256 * 256;
     const bool idle = a.cache.dim > 128 && groups * 4 <= cus;
-    if (cap <= (idle ? 512 : 1024)) chunk = 1024;
+    if (max_len <= (idle ? 512 : 1024)) chunk = 1024;
     if (chunk > kMaxChunk) chunk = kMaxChunk;
     a.chunk = (int)chunk;
     a.max_splits = (int)((cap + chunk - 1) / chunk);
-    a.few = a.max_splits == 1 && groups <= cus;
+    a.few = max_len <= chunk && groups <= cus;
 }
 
 int64_t kv8_attend_partial_bytes(const Kv8AttendArgs &a) {

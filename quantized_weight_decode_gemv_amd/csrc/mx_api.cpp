@@ -136,13 +136,15 @@ int qwg_kv8_append(const qwg_kv8 *cache, const void *k, const void *v, int type,
 }
 
 int64_t qwg_kv8_attend_workspace(const qwg_kv8 *cache, int64_t table_width, int64_t n_seqs,
-                                 int q_len, int n_heads, int64_t max_len) {
+                                 int q_len, int n_heads, int64_t window, int64_t max_len) {
     int rc = check_cache(cache);
     if (!rc) rc = attend_shape(cache, table_width, n_seqs, q_len, n_heads, max_len);
+    if (!rc && window < 0) rc = QWG_ERR_SHAPE;
     if (rc) return -rc;
     Kv8AttendArgs a = {};
     a.cache = cache_of(cache);
     a.width = table_width, a.n_seqs = n_seqs, a.q_len = q_len, a.n_heads = n_heads;
+    a.window = window;
     kv8_attend_plan(a, max_len, kCus);
     return kv8_attend_partial_bytes(a);
 }

@@ -61,8 +61,8 @@ struct Kv8AttendArgs {
     int q_len, n_heads;
     float scale;
     int chunk;       // positions per split (a multiple of 64)
-    int max_splits;  // splits of a sequence that fills its table
-    bool few;        // one split each, and no more workgroups than compute units
+    int max_splits;  // splits of a sequence that fills its table or window
+    bool few;        // as far as known one split each, and no more of them than compute units
     float *partial;  // [n_seqs][max_splits][q_len * n_heads][dim + 2], or null for one split
 };
 

@@ -211,6 +211,19 @@ def test_attend_many_short_sequences(t, dim, page, kv, group, q_len):
     assert_attend(out, *ref.attend(qd, c, table, lens, dim ** -0.5, 0), t, dim)
 
 
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("dim,page,window", [(64, 16, 512), (128, 64, 1000), (128, 128, 4097), (256, 32, 961), (96, 16, 2500)])
+def test_attend_window_of_a_long_sequence(t, dim, page, window):
+    rng = np.random.default_rng(window)
+    lens = np.array([9001, 3, window, window + 62, 0, 4 * window - 1], np.int32)
+    c, table = filled(rng, lens, 1, dim, page, spread=0.3)
+    q, qd = typed(rng.standard_normal((len(lens), 3, 4, dim)), t)
+    want = ref.attend(qd, c, table, lens, dim ** -0.5, window)
+    for most in (None, 16):
+        out = qwg.kv8_attend(q, *pages(c), dev(table), dev(lens), window=window, max_len=most)
+        assert_attend(out, want[0], want[1] * (1 + window / 64 / 64), want[2], t, dim)
+
+
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("length", [512, 513, 1008, 1024, 1025])
 def test_attend_one_sequence_around_the_first_split(dim, length):

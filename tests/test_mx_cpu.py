@@ -86,10 +86,12 @@ def test_attend_refusals(L, cache, change, status):  # noqa: F811
 
 def test_attend_workspace(L):  # noqa: F811
     size = L.qwg_kv8_attend_workspace
-    assert size(desc(), 2, 2, 1, 4, 0) == 0                 # 32 positions: one workgroup a head
-    assert size(desc(), 65536, 1, 1, 8, 0) > 0
-    assert size(desc(head_dim=80), 2, 2, 1, 4, 0) == -2 and size(None, 2, 2, 1, 4, 0) == -1
-    assert size(desc(), 2, 2, 1, 3, 0) == -2
+    assert size(desc(), 2, 2, 1, 4, 0, 0) == 0              # 32 positions: one workgroup a head
+    assert size(desc(), 65536, 1, 1, 8, 0, 0) > 0
+    assert size(desc(), 65536, 1, 1, 8, 512, 0) == 0        # a window of 512: the same
+    assert 0 < size(desc(), 65536, 1, 1, 8, 8192, 0) < size(desc(), 65536, 1, 1, 8, 0, 0)
+    assert size(desc(head_dim=80), 2, 2, 1, 4, 0, 0) == -2 and size(None, 2, 2, 1, 4, 0, 0) == -1
+    assert size(desc(), 2, 2, 1, 3, 0, 0) == -2 and size(desc(), 2, 2, 1, 4, -1, 0) == -2
 
 
 def test_binding_refuses_cpu_tensors():
