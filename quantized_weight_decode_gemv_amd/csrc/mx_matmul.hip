@@ -14,6 +14,8 @@
 // is row 16(m/4) + 4i + m%4. The result lane's four rows in each of four tiles are
 // then 16 consecutive outputs, and four tiles' scales of a lane lie in one 8-byte
 // word, whose bytes the product instruction selects by itself.
+#include <algorithm>
+
 #include "mx_device.h"
 #include "mx_lds.h"
 
@@ -260,6 +262,95 @@ __global__ __launch_bounds__(WM * WN * 64) void mxfp4_matmul_kernel(MxMatmulArgs
     }
 }
 
+// Few tiles: 32 x 32 of C per workgroup, whose wavefronts share n_in. A wavefront
+// takes 512 columns of the 64 rows at a time, straight from memory into the
+// operands, lane l of a row's sixteen blocks 4(l/16) .. +3 (64 consecutive bytes;
+// with 16 bytes of 64-byte pieces per lane group instead, 128 outputs of 32 rows of
+// 8192 took 16.4 us). A compute unit alone draws 30-40 GB/s, so the smallest tile
+// that the operands' form allows, on as many units as there are, is what counts.
+// us here and in 64 x 128 tiles: 4096 outputs of 64 rows of 14336 18.6 and 38.3, 1024
+// of 32 of 2048 5.5 and 6.3, of 512 (one wavefront's columns) 5.2 and 3.7; 4096 of 128
+// of 2048 (512 tiles) 7.9 and 6.6.
+constexpr int kFewWaves = 16;
+constexpr int kFewMinIn = 2048;
+
+template <int TYPE, bool WORDS>
+__global__ __launch_bounds__(kFewWaves * 64) void mxfp4_matmul_few_kernel(MxMatmulArgs a) {
+    typedef typename Elem<TYPE>::T T;
+    __shared__ __align__(16) float sums[kFewWaves][32][32 + 4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int n = lane & 15, g = lane >> 4;
+    const int nblk = a.n_in / kMxBlock, steps = (nblk + 15) / 16;
+    const int64_t row0 = (int64_t)blockIdx.y * 32, out0 = (int64_t)blockIdx.x * 32;
+    // rows past the last one read the last one
+    const uint8_t *codes[4], *scales[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t r = i < 2 ? min(out0 + i * 16 + n, a.n_out - 1) : min(row0 + (i - 2) * 16 + n, a.n_rows - 1);
+        codes[i] = (i < 2 ? a.w : a.a) + r * nblk * kMxCodeBytes;
+        scales[i] = (i < 2 ? a.w_scales : a.a_scales) + r * nblk;
+    }
+    f32x4 acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    for (int s = wave; s < steps; s += waves) {
+        const int b = s * 16 + g * 4;
+        u32x4 c[4][4];
+        uint32_t e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (WORDS && b + 4 <= nblk) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) c[i][q] = *(const u32x4 *)(codes[i] + (int64_t)(b + q) * kMxCodeBytes);
+                e[i] = *(const uint32_t *)(scales[i] + b);
+            } else {
+                e[i] = 0x7f7f7f7fu;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    c[i][q] = u32x4{0, 0, 0, 0};
+                    if (b + q < nblk) {
+                        c[i][q] = *(const u32x4 *)(codes[i] + (int64_t)(b + q) * kMxCodeBytes);
+                        e[i] = (e[i] & ~(255u << (8 * q))) | (uint32_t)scales[i][b + q] << (8 * q);
+                    }
+                }
+            }
+        }
+        each<4>([&](auto q) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[i][j] = product<q.v & 1, q.v / 2, q.v / 2>(c[i][q.v], c[2 + j][q.v], u32x2{e[i], 0}, u32x2{e[2 + j], 0}, acc[i][j]);
+        });
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) *(f32x4 *)&sums[wave][j * 16 + n][i * 16 + g * 4] = acc[i][j];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * 32; i += blockDim.x) {
+        const int r = i >> 5, o = i & 31;
+        if (row0 + r >= a.n_rows || out0 + o >= a.n_out) continue;
+        float v = 0;
+        for (int w = 0; w < waves; ++w) v += sums[w][r][o];
+        ((T *)a.c)[(row0 + r) * a.n_out + out0 + o] = (T)v;
+    }
+}
+
+template <int TYPE>
+hipError_t launch_few(const MxMatmulArgs &a, hipStream_t s) {
+    const int steps = (a.n_in / kMxBlock + 15) / 16;
+    const dim3 grid((unsigned)((a.n_out + 31) / 32), (unsigned)((a.n_rows + 31) / 32));
+    const bool words = a.n_in % (4 * kMxBlock) == 0 && ((uintptr_t)a.a_scales | (uintptr_t)a.w_scales) % 4 == 0;
+    if (words)
+        mxfp4_matmul_few_kernel<TYPE, true><<<grid, std::min(steps, kFewWaves) * 64, 0, s>>>(a);
+    else
+        mxfp4_matmul_few_kernel<TYPE, false><<<grid, std::min(steps, kFewWaves) * 64, 0, s>>>(a);
+    return hipGetLastError();
+}
+
 template <int TYPE, int TM, int TN, int WM, int WN>
 hipError_t launch(const MxMatmulArgs &a, hipStream_t s) {
     constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
@@ -277,6 +368,7 @@ hipError_t launch(const MxMatmulArgs &a, hipStream_t s) {
     auto tiles = [&](int64_t m, int64_t n) {
         return ((a.n_rows + m - 1) / m) * ((a.n_out + n - 1) / n);
     };
+    if (a.n_in >= kFewMinIn && tiles(32, 32) <= 256) return launch_few<TYPE>(a, s);
     if (tiles(256, 256) >= 256) return launch<TYPE, 8, 4, 2, 4>(a, s);
     if (tiles(128, 128) >= 256) return launch<TYPE, 4, 4, 2, 2>(a, s);
     return launch<TYPE, 2, 4, 2, 2>(a, s);

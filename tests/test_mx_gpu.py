@@ -225,6 +225,24 @@ def test_matmul_larger(t, rows, n_out, n_in):
     assert_product(qwg.matmul_mxfp4(dev(ac), dev(asc), dev(c), dev(s), dtype=t), w, a, t)
 
 
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("rows,n_out,n_in", [(1, 5, 2080), (33, 31, 2304), (32, 256, 2048), (250, 1000, 2176), (257, 1000, 2176),
+                                             (70, 90, 16416)])
+def test_matmul_of_few_tiles_and_long_rows(t, rows, n_out, n_in):
+    rng = gen(rows + n_in)
+    c, s, w = weights(rng, n_out, n_in)
+    ac, asc, a = weights(rng, rows, n_in)
+    assert_product(qwg.matmul_mxfp4(dev(ac), dev(asc), dev(c), dev(s), dtype=t), w, a, t)
+    # scales at an odd address, and a NaN block of each: its row and its column alone
+    s[0, 63], asc[0, 1] = 255, 255
+    odd = torch.zeros(s.size + 1, dtype=torch.uint8, device=DEV)[1:].view(s.shape)
+    odd.copy_(dev(s))
+    y = qwg.matmul_mxfp4(dev(ac), dev(asc), dev(c), odd, dtype=t)
+    assert torch.isnan(y[0]).all() and torch.isnan(y[:, 0]).all()
+    if rows > 1:
+        assert_product(y[1:, 1:], w[1:], a[1:], t)
+
+
 def test_matmul_nan_blocks_and_odd_scales():
     rng = gen(8)
     c, s, w = weights(rng, 70, 256)
