@@ -131,6 +131,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mxfp4_matmul_kernel(MxMatmulArgs
         if constexpr (TM == 2) {  // half a group: its tiles are 0, 1 or 2, 3
             if (wm & 1) v.x[0][0] = v.x[0][1];
         }
+        if constexpr (TM == 1) v.x[0][0] = (wm & 2 ? v.x[0][1] : v.x[0][0]) >> (wm & 1) * 16;
     };
     const uint8_t *const base_w = lds + (BM + wn * TN * 16) * kStageBytes + lane_row * kStageBytes;
     const uint8_t *const base_x = lds + (wm * TM / 4 * 64 + wm * TM % 4 * 4) * kStageBytes + lane_row * kStageBytes;
@@ -339,6 +340,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void mxfp4_matmul_few_kernel(MxMatm
     }
 }
 
+constexpr int64_t kUnits = 256;  // compute units
+
 template <int TYPE>
 hipError_t launch_few(const MxMatmulArgs &a, hipStream_t s) {
     const int steps = (a.n_in / kMxBlock + 15) / 16;
@@ -364,13 +367,20 @@ hipError_t launch(const MxMatmulArgs &a, hipStream_t s) {
 
 template <int TYPE>
 hipError_t launch(const MxMatmulArgs &a, hipStream_t s) {
-    // the largest tile that still gives every compute unit one
+    // The largest tile that keeps five eighths of the compute units busy in every round
+    // (us in 256 x 256, 128 x 128, 64 x 128 and 64 x 64 tiles: 3606 x 2016 -> 3162, 195
+    // large tiles, 27.0, 30.6, 34.3, 39.3; 2048 x 4096 -> 4096, 128 of them, 34.9, 27.0,
+    // 34.3, 39.6; 509 x 2048 -> 5632, 176 of 128 x 128, 19.3, 10.1, 11.2, 10.8), and the
+    // smallest where there is at most one to a unit (140 x 5568 -> 2875: 43.4, 21.6,
+    // 21.2, 13.5; 200 x 14336 -> 4096: 88.4, 43.3, 39.0, 32.2).
     auto tiles = [&](int64_t m, int64_t n) {
         return ((a.n_rows + m - 1) / m) * ((a.n_out + n - 1) / n);
     };
-    if (a.n_in >= kFewMinIn && tiles(32, 32) <= 256) return launch_few<TYPE>(a, s);
-    if (tiles(256, 256) >= 256) return launch<TYPE, 8, 4, 2, 4>(a, s);
-    if (tiles(128, 128) >= 256) return launch<TYPE, 4, 4, 2, 2>(a, s);
+    if (a.n_in >= kFewMinIn && tiles(32, 32) <= kUnits) return launch_few<TYPE>(a, s);
+    if (tiles(64, 64) <= kUnits) return launch<TYPE, 1, 4, 4, 1>(a, s);
+    const int64_t large = tiles(256, 256), rounds = (large + kUnits - 1) / kUnits;
+    if (large * 8 >= rounds * kUnits * 5) return launch<TYPE, 8, 4, 2, 4>(a, s);
+    if (tiles(128, 128) * 8 >= kUnits * 5) return launch<TYPE, 4, 4, 2, 2>(a, s);
     return launch<TYPE, 2, 4, 2, 2>(a, s);
 }
 

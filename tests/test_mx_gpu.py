@@ -216,7 +216,7 @@ def test_matmul_matches(t, rows, n_out, n_in):
 
 
 @pytest.mark.parametrize("t", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("rows,n_out,n_in", [(509, 2048, 5632), (1025, 1030, 1024), (2048, 3000, 256), (16, 20000, 320),
+@pytest.mark.parametrize("rows,n_out,n_in", [(509, 2048, 5632), (1025, 1030, 1024), (2048, 3000, 256), (16, 20000, 320), (3600, 3170, 96),
                                              (3, 64, 65536)])
 def test_matmul_larger(t, rows, n_out, n_in):
     rng = gen(rows + n_out)
