@@ -50,9 +50,10 @@ __device__ __forceinline__ uint32_t fp8_shifted(uint32_t w, float shift) {
 // magnitude comes first; a thread's first tile stays in registers meanwhile.
 // VEC: the values of a token start on 16 bytes.
 template <int TYPE, bool VEC>
-__global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs a) {
+__global__ __launch_bounds__(1024) void kv8_append_kernel(Kv8AppendArgs a) {
     typedef typename Elem<TYPE>::T T;
-    __shared__ uint32_t tops[4];
+    __shared__ uint32_t tops[16];
+    const int threads = blockDim.x;
     const Kv8 &c = a.cache;
     const int64_t seq = blockIdx.y;
     const int head = (int)blockIdx.z >> 1;
@@ -98,10 +99,10 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs a) {
         uint32_t top = 0;
         // the last tile of a thread is loaded last, and kept for the second pass
         const int last = (int)threadIdx.x < tiles
-                             ? (int)threadIdx.x + (tiles - 1 - (int)threadIdx.x) / 256 * 256
+                             ? (int)threadIdx.x + (tiles - 1 - (int)threadIdx.x) / threads * threads
                              : -1;
         int slot = 0, d = 0;
-        for (int i = threadIdx.x; i < tiles; i += 256) {
+        for (int i = threadIdx.x; i < tiles; i += threads) {
             load(i, slot, d);
 #pragma unroll
             for (int t = 0; t < 4; ++t)
@@ -116,11 +117,11 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs a) {
         __syncthreads();
         if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
         __syncthreads();
-        top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+        for (int w = 0; w < threads / 64; ++w) top = max(top, tops[w]);
         const uint32_t before = old ? *scale : 0;
         const uint32_t now = max(before, page_exponent(top));
         const float sc = e8m0(now);
-        for (int i = last; i >= 0; i -= 256) {
+        for (int i = last; i >= 0; i -= threads) {
             if (i != last) load(i, slot, d);
             const int lo = max(old - slot, 0), hi = min(stop - slot, 4);
             if (!is_v) {
@@ -150,11 +151,11 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs a) {
             // the page's scale rises: its earlier codes are rounded to the new one
             const float shift = __builtin_ldexpf(1.0f, (int)before - (int)now);
             if (!is_v) {
-                for (int i = threadIdx.x; i < old * c.dim / 4; i += 256)
+                for (int i = threadIdx.x; i < old * c.dim / 4; i += threads)
                     ((uint32_t *)codes)[i] = fp8_shifted(((uint32_t *)codes)[i], shift);
             } else {
                 const int words = (old + 3) >> 2;
-                for (int i = threadIdx.x; i < words * c.dim; i += 256) {
+                for (int i = threadIdx.x; i < words * c.dim; i += threads) {
                     const int ch = i / words, s = (i - ch * words) * 4;
                     uint8_t *at = codes + ch * c.page + s;
                     if (s + 4 <= old) {
@@ -307,6 +308,7 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
     // Q parts: [tile][step][part][lane] 16 bytes, as the lanes take them
     {
         const T *q = (const T *)a.q;
+        const bool vec = ((uintptr_t)q | (uintptr_t)a.q_stride * sizeof(T)) % 16 == 0;
         for (int i = threadIdx.x; i < R * KS * 64; i += W * 64) {
             const int l = i & 63, ks = (i >> 6) % KS, r = (i >> 6) / KS;
             const int row = row0 + r * 16 + (l & 15), lg = l >> 4;
@@ -317,7 +319,8 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
             float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             if (row < rows) {
                 const int t = row / group, h = head * group + row % group;
-                load8<T, false>(q + (seq * a.q_len + t) * a.q_stride + (int64_t)h * D + d, v);
+                const T *p = q + (seq * a.q_len + t) * a.q_stride + (int64_t)h * D + d;
+                vec ? load8<T, true>(p, v) : load8<T, false>(p, v);
             }
             uint32_t w[3][4];
 #pragma unroll
@@ -747,31 +750,36 @@ hipError_t launch_kv8_append(const Kv8AppendArgs &a, int type, hipStream_t s) {
     if (pages > a.width) pages = a.width;
     if (pages > 4096) pages = 4096;
     const dim3 grid((unsigned)pages, (unsigned)a.n_seqs, (unsigned)(a.cache.n_kv * 2));
+    // a thread per tile of a full page
+    const int threads = std::min(std::max(a.cache.page * a.cache.dim / 32, 256), 1024);
     const uintptr_t size = type == kF32 ? 4 : 2;
     // (head_dim values are whole 16 bytes in every type)
     const bool vec = ((uintptr_t)a.k | (uintptr_t)a.v) % 16 == 0 &&
                      (a.n_tokens == 1 || (a.k_stride * size % 16 == 0 && a.v_stride * size % 16 == 0));
     if (type == kF32)
-        vec ? kv8_append_kernel<kF32, true><<<grid, 256, 0, s>>>(a)
-            : kv8_append_kernel<kF32, false><<<grid, 256, 0, s>>>(a);
+        vec ? kv8_append_kernel<kF32, true><<<grid, threads, 0, s>>>(a)
+            : kv8_append_kernel<kF32, false><<<grid, threads, 0, s>>>(a);
     else if (type == kF16)
-        vec ? kv8_append_kernel<kF16, true><<<grid, 256, 0, s>>>(a)
-            : kv8_append_kernel<kF16, false><<<grid, 256, 0, s>>>(a);
+        vec ? kv8_append_kernel<kF16, true><<<grid, threads, 0, s>>>(a)
+            : kv8_append_kernel<kF16, false><<<grid, threads, 0, s>>>(a);
     else
-        vec ? kv8_append_kernel<kBF16, true><<<grid, 256, 0, s>>>(a)
-            : kv8_append_kernel<kBF16, false><<<grid, 256, 0, s>>>(a);
+        vec ? kv8_append_kernel<kBF16, true><<<grid, threads, 0, s>>>(a)
+            : kv8_append_kernel<kBF16, false><<<grid, threads, 0, s>>>(a);
     return hipGetLastError();
 }
 
-// Splits: one round of resident workgroups for a single sequence, four rounds for
-// several, whose lengths differ (32 ragged sequences of up to 8192 positions, 8
-// heads of 128: 79 us in half a round, 73 us in four, 78 in sixteen; one of
-// 131,071, 4 tokens of 64 heads: 65 us in one round, 76 in two, 104 in eight,
-// more partial sums). Up to 1024 positions stay whole: the launch that joins
-// splits costs as much as two more turns of a workgroup (64 ragged sequences of up
-// to 900, 8 heads of 128: 22 us whole, 35 in splits of 256), unless a workgroup of
-// four wavefronts would take more than two turns with three quarters of the compute
-// units idle (900 positions, 4 heads of 256: 19.4 us whole, 12.3 in splits of 256).
+// Splits. A workgroup's start and end cost as much as three or four of its turns,
+// and the launch that joins splits two more, so splits are as long as the chip
+// stays busy: what a round of resident workgroups shares evenly; twice that, or
+// 1024 positions, where two workgroups share a compute unit and the sequences are
+// few or uneven (us: 2 x 32,000, 8 heads of 128, splits of 256 / 512 / 1024 / 2048:
+// 37.6, 31.5, 27.9, 26.3; 32 x 8192: 97, 72, 65, 68; one of 4000: 9.9, 11.6, 15.8,
+// 24.1, there 256 is twice the share). Whole sequences where they fill the chip by
+// themselves (256 x 1500, 8 heads of 128: 93, in splits of 1024 137; 30 x 3000, 4
+// heads of 256: 32.0 and 41.5) and, up to 1024 positions, everywhere (64 x 900, 8
+// heads of 128: 22, in splits of 256 35) but where a workgroup of four wavefronts
+// would take more than two turns with three quarters of the compute units idle (900
+// positions, 4 heads of 256: 19.4 whole, 12.3 in splits of 256).
 void kv8_attend_plan(Kv8AttendArgs &a, int64_t max_len, int cus) {
     const int rows = a.q_len * (a.n_heads / a.cache.n_kv);
     // positions that a sequence's rows see together, at most and as far as known
@@ -780,9 +788,12 @@ void kv8_attend_plan(Kv8AttendArgs &a, int64_t max_len, int cus) {
     if (max_len <= 0 || max_len > cap) max_len = cap;
     const int r = row_tiles(rows, a.cache.dim);
     const int64_t groups = a.n_seqs * a.cache.n_kv * ((rows + 16 * r - 1) / (16 * r));
-    const int64_t resident = (int64_t)cus * 8 / waves_of(a.cache.dim, r);
-    const int64_t want = ((a.n_seqs > 1 ? 4 : 1) * resident + groups - 1) / groups;
-    int64_t chunk = (max_len + want - 1) / want;
+    const bool two = a.cache.dim <= 128 && waves_of(a.cache.dim, r) == 4;  // to a compute unit
+    const int64_t slots = two ? 2 * cus : cus;
+    int64_t chunk = (max_len * groups + slots - 1) / slots;
+    const bool full = two ? groups >= slots : 2 * groups > slots;
+    if (max_len <= kMaxChunk && full) chunk = max_len;
+    else if (two && (chunk <= 1024 || a.n_seqs > 1)) chunk = std::min<int64_t>(2 * chunk, 1024);
     chunk = (chunk + 255) / 256 * 256;
     const bool idle = a.cache.dim > 128 && groups * 4 <= cus;
     if (max_len <= (idle ? 512 : 1024)) chunk = 1024;
