@@ -229,7 +229,9 @@ constexpr int v_zone(int d) { return (d == 96 ? 128 : d) * kBlk; }
 // channels, whose Q would not fit twice, and where every workgroup has a compute
 // unit to itself and takes a whole sequence (one of 517 positions, 4 heads of 64:
 // 10.0 us with four, 8.3 with eight, 8.7 with sixteen).
-constexpr int waves_of(int d, int r) { return d == 128 && r == 2 ? 8 : 4; }
+constexpr int waves_of(int d, int r, int type) {
+    return d == 128 && r == 2 ? 8 : d == 256 && r == 2 && type != kBF16 ? 3 : 4;
+}
 
 // One workgroup: one split (`chunk` positions) of one sequence, one key/value
 // head, R tiles of 16 rows; a row is a (query token, head of the group) pair.
@@ -695,7 +697,7 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8AttendArgs a) {
     }
 }
 
-template <int TYPE, int D, int R, int W = waves_of(D, R)>
+template <int TYPE, int D, int R, int W = waves_of(D, R, TYPE)>
 hipError_t attend(const Kv8AttendArgs &a, hipStream_t s) {
     if constexpr (D <= 128 && W == 4) {
         if (a.few) return attend<TYPE, D, R, 8>(a, s);
@@ -721,19 +723,15 @@ hipError_t attend(const Kv8AttendArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Row tiles that a workgroup takes together: two where there are more than 16
-// rows per key/value head and the registers hold two (head_dim up to 128).
-int row_tiles(int rows, int dim) { return rows > 16 && dim <= 128 ? 2 : 1; }
-
 template <int TYPE>
 hipError_t attend_dim(const Kv8AttendArgs &a, hipStream_t s) {
-    const bool two = row_tiles(a.q_len * (a.n_heads / a.cache.n_kv), a.cache.dim) == 2;
+    const bool two = a.row_tiles == 2;
     switch (a.cache.dim) {
         case 64: return two ? attend<TYPE, 64, 2>(a, s) : attend<TYPE, 64, 1>(a, s);
         case 96: return two ? attend<TYPE, 96, 2>(a, s) : attend<TYPE, 96, 1>(a, s);
         case 128: return two ? attend<TYPE, 128, 2>(a, s) : attend<TYPE, 128, 1>(a, s);
-        case 192: return attend<TYPE, 192, 1>(a, s);
-        default: return attend<TYPE, 256, 1>(a, s);
+        case 192: return two ? attend<TYPE, 192, 2>(a, s) : attend<TYPE, 192, 1>(a, s);
+        default: return two ? attend<TYPE, 256, 2>(a, s) : attend<TYPE, 256, 1>(a, s);
     }
 }
 
@@ -786,9 +784,16 @@ void kv8_attend_plan(Kv8AttendArgs &a, int64_t max_len, int cus) {
     int64_t cap = a.width * a.cache.page;
     if (a.window > 0 && a.window < cap) cap = std::min(cap, a.window + a.q_len + kBlk - 2);
     if (max_len <= 0 || max_len > cap) max_len = cap;
-    const int r = row_tiles(rows, a.cache.dim);
+    // Row tiles that a workgroup takes together: two where there are more than 16 rows
+    // per key/value head; of more than 128 channels (one wavefront to a SIMD) where it
+    // saves a third of the passes over the cache and that is what counts (us: 8 x 6018,
+    // 40 rows, 8 heads of 256: 74, one by one 120; 32 rows of 16 x 3000, 8 heads of 192:
+    // 39 and 42; 32 rows of 2 x 500, 4 heads of 256: 26 and 14).
+    const int64_t alone = a.n_seqs * a.cache.n_kv * ((rows + 15) / 16);
+    const int r = rows > 16 && (a.cache.dim <= 128 || (rows > 32 && alone * max_len >= cus * 1024)) ? 2 : 1;
+    a.row_tiles = r;
     const int64_t groups = a.n_seqs * a.cache.n_kv * ((rows + 16 * r - 1) / (16 * r));
-    const bool two = a.cache.dim <= 128 && waves_of(a.cache.dim, r) == 4;  // to a compute unit
+    const bool two = a.cache.dim <= 128 && !(a.cache.dim == 128 && r == 2);  // to a compute unit
     const int64_t slots = two ? 2 * cus : cus;
     int64_t chunk = (max_len * groups + slots - 1) / slots;
     const bool full = two ? groups >= slots : 2 * groups > slots;

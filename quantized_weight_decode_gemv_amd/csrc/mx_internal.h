@@ -60,6 +60,7 @@ struct Kv8AttendArgs {
     int64_t width, n_seqs, window;
     int q_len, n_heads;
     float scale;
+    int row_tiles;   // tiles of 16 rows per workgroup
     int chunk;       // positions per split (a multiple of 64)
     int max_splits;  // splits of a sequence that fills its table or window
     bool few;        // as far as known one split each, and no more of them than compute units

@@ -224,6 +224,18 @@ def test_attend_window_of_a_long_sequence(t, dim, page, window):
         assert_attend(out, want[0], want[1] * (1 + window / 64 / 64), want[2], t, dim)
 
 
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("dim,kv,group,q_len", [(192, 1, 13, 3), (256, 2, 5, 8), (256, 1, 16, 5)])
+def test_attend_many_rows_of_wide_heads(t, dim, kv, group, q_len):
+    rng = np.random.default_rng(dim + group)
+    lens = np.array([2600, 70, 1, 40000 // kv], np.int32)  # enough to take two tiles of rows at once
+    c, table = filled(rng, lens, kv, dim, 32, spread=0.3)
+    q, qd = typed(rng.standard_normal((len(lens), q_len, kv * group, dim)), t)
+    want = ref.attend(qd, c, table, lens, dim ** -0.5, 0)
+    out = qwg.kv8_attend(q, *pages(c), dev(table), dev(lens))
+    assert_attend(out, want[0], want[1] * (1 + lens.max() / 64 / 64), want[2], t, dim)
+
+
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("length", [512, 513, 1008, 1024, 1025])
 def test_attend_one_sequence_around_the_first_split(dim, length):
