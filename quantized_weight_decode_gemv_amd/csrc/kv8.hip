@@ -226,9 +226,12 @@ constexpr int k_zone(int d) { return d * kBlk; }
 constexpr int v_zone(int d) { return (d == 96 ? 128 : d) * kBlk; }
 // Wavefronts of a workgroup: four, two such workgroups to a compute unit (one's
 // start and end then overlap the other's middle); eight for two tiles of 128
-// channels, whose Q would not fit twice, and where every workgroup has a compute
-// unit to itself and takes a whole sequence (one of 517 positions, 4 heads of 64:
-// 10.0 us with four, 8.3 with eight, 8.7 with sixteen).
+// channels, whose Q would not fit twice; three or four for two of 256, as LDS
+// holds. Eight where every workgroup has a compute unit to itself and takes a
+// whole sequence (one of 517 positions, 4 heads of 64: 10.0 us with four, 8.3 with
+// eight, 8.7 with sixteen); two, and so more workgroups at once, where short
+// sequences are many (100 of up to 200 positions, 8 heads of 256: 33.0 us with four,
+// 25.6 with two; of up to 86, 8 of 128: 13.3 and 9.1).
 constexpr int waves_of(int d, int r, int type) {
     return d == 128 && r == 2 ? 8 : d == 256 && r == 2 && type != kBF16 ? 3 : 4;
 }
@@ -699,6 +702,9 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8AttendArgs a) {
 
 template <int TYPE, int D, int R, int W = waves_of(D, R, TYPE)>
 hipError_t attend(const Kv8AttendArgs &a, hipStream_t s) {
+    if constexpr (W == waves_of(D, R, TYPE)) {
+        if (a.brief) return attend<TYPE, D, R, 2>(a, s);
+    }
     if constexpr (D <= 128 && W == 4) {
         if (a.few) return attend<TYPE, D, R, 8>(a, s);
     }
@@ -806,6 +812,7 @@ void kv8_attend_plan(Kv8AttendArgs &a, int64_t max_len, int cus) {
     a.chunk = (int)chunk;
     a.max_splits = (int)((cap + chunk - 1) / chunk);
     a.few = max_len <= chunk && groups <= cus;
+    a.brief = max_len <= 512 && groups > slots;
 }
 
 int64_t kv8_attend_partial_bytes(const Kv8AttendArgs &a) {

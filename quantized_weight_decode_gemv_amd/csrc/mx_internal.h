@@ -63,6 +63,7 @@ struct Kv8AttendArgs {
     int row_tiles;   // tiles of 16 rows per workgroup
     int chunk;       // positions per split (a multiple of 64)
     int max_splits;  // splits of a sequence that fills its table or window
+    bool brief;      // more workgroups than fit at once, as far as known of 512 positions at most
     bool few;        // as far as known one split each, and no more of them than compute units
     float *partial;  // [n_seqs][max_splits][q_len * n_heads][dim + 2], or null for one split
 };

@@ -201,7 +201,9 @@ def test_attend_long_and_split(t, dim, page, length):
 
 
 @pytest.mark.parametrize("t", TYPES)
-@pytest.mark.parametrize("dim,page,kv,group,q_len", [(64, 16, 1, 4, 1), (64, 32, 1, 17, 1), (96, 64, 1, 2, 9), (128, 16, 2, 4, 1)])
+@pytest.mark.parametrize("dim,page,kv,group,q_len", [(64, 16, 1, 4, 1), (64, 32, 1, 17, 1), (96, 64, 1, 2, 9), (128, 16, 2, 4, 1),
+                                                     (64, 32, 2, 17, 1), (96, 16, 2, 3, 1), (128, 128, 1, 5, 4), (192, 64, 1, 2, 1),
+                                                     (192, 32, 1, 1, 17), (256, 16, 1, 3, 1)])
 def test_attend_many_short_sequences(t, dim, page, kv, group, q_len):
     rng = np.random.default_rng(dim * group)
     lens = rng.integers(0, 300, 300).astype(np.int32)
