@@ -9,6 +9,7 @@
 // consecutive positions of a channel in consecutive bytes both products take
 // their operands from memory as they lie.
 #include <algorithm>
+#include <type_traits>
 
 #include "mx_device.h"
 #include "mx_lds.h"
@@ -47,13 +48,17 @@ __device__ __forceinline__ uint32_t fp8_shifted(uint32_t w, float shift) {
 // One workgroup per (page of a sequence, sequence, head of K or V). A thread
 // takes four consecutive positions of eight channels: 8-byte stores to a K page,
 // 4-byte stores (one per channel) to a transposed V page. The page's largest new
-// magnitude comes first; a thread's first tile stays in registers meanwhile.
+// magnitude comes first (one pass over the values, a cross-lane and an LDS step);
+// a thread's last tile stays in registers meanwhile, so that a page of up to 256
+// tiles is read once. Memory bounds it where there is much: 9 prompts of up to 2000
+// tokens, 8 heads of 128, bf16 (62 MB read and written): 17.4 us, 3.5 TB/s. One token
+// each of 33 sequences takes 5.4 us: the launch and four round trips in a row (length,
+// page number, values, exponent).
 // VEC: the values of a token start on 16 bytes.
-template <int TYPE, bool VEC>
-__global__ __launch_bounds__(1024) void kv8_append_kernel(Kv8AppendArgs a) {
+template <int TYPE, bool VEC, int threads>
+__global__ __launch_bounds__(threads) void kv8_append_kernel(Kv8AppendArgs a) {
     typedef typename Elem<TYPE>::T T;
-    __shared__ uint32_t tops[16];
-    const int threads = blockDim.x;
+    __shared__ uint32_t tops[threads / 64];
     const Kv8 &c = a.cache;
     const int64_t seq = blockIdx.y;
     const int head = (int)blockIdx.z >> 1;
@@ -117,6 +122,7 @@ __global__ __launch_bounds__(1024) void kv8_append_kernel(Kv8AppendArgs a) {
         __syncthreads();
         if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
         __syncthreads();
+#pragma unroll
         for (int w = 0; w < threads / 64; ++w) top = max(top, tops[w]);
         const uint32_t before = old ? *scale : 0;
         const uint32_t now = max(before, page_exponent(top));
@@ -253,6 +259,14 @@ constexpr int waves_of(int d, int r, int type) {
 // granules of a line permuted so that the operands' reads meet no bank twice. A
 // block's K is asked for as soon as the block before has read its own, V
 // likewise.
+//
+// It is bound by memory where the cache is long: 32 ragged sequences of up to 8192
+// positions, 8 heads of 128, four queries' heads each (324 MB): 58.9 us and 4.6 to
+// join the splits, 5.1 TB/s (a large copy reaches 4.7); one of 131,071, 4 tokens of 64
+// heads: 52-54 us and 4.6. A short call is bound by its chain of round trips (length,
+// page numbers, exponents, K and V, the sums' meeting): 8.2 us for 517 positions.
+// Asking for the first K and V before the exponents took a barrier more and 0.3-0.9
+// us more.
 //
 // Queries and probabilities enter as bf16 parts (one to three) that hold all
 // their bits, or 16 of the probabilities' for the 16-bit types; e4m3 is exact in bf16.
@@ -648,7 +662,10 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
 }
 
 // Joins the splits of a sequence: one workgroup per (query token, head), its
-// wavefronts taking the splits in turn.
+// wavefronts taking the splits in turn. 4.6 us for 32 x 32 rows of 128 channels in
+// up to nine splits (40 MB at most, from the last-level cache), most of it the launch
+// and two round trips; in this launch and not in the last workgroup to end, so that
+// no counter has to be cleared and the order of the sums is fixed.
 template <int TYPE, int D>
 __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8AttendArgs a) {
     typedef typename Elem<TYPE>::T T;
@@ -717,6 +734,8 @@ hipError_t attend(const Kv8AttendArgs &a, hipStream_t s) {
     const size_t lds = work > join ? work : join;
     if constexpr (R == 1 && D <= 128) {  // (16 rows at most)
         kv8_attend_kernel<TYPE, D, R, W, true><<<grid, W * 64, lds, s>>>(a);
+    } else if constexpr (R == 2 && D > 128) {  // (more than 32)
+        kv8_attend_kernel<TYPE, D, R, W, false><<<grid, W * 64, lds, s>>>(a);
     } else {
         if (tiles == 1)
             kv8_attend_kernel<TYPE, D, R, W, true><<<grid, W * 64, lds, s>>>(a);
@@ -741,6 +760,33 @@ hipError_t attend_dim(const Kv8AttendArgs &a, hipStream_t s) {
     }
 }
 
+template <int TYPE>
+hipError_t append(const Kv8AppendArgs &a, hipStream_t s) {
+    // pages that max_new tokens touch at most; a sequence with more of them takes more trips
+    int64_t pages = a.max_new / a.cache.page + 2;
+    if (a.max_new <= 1) pages = 1;
+    if (pages > a.width) pages = a.width;
+    if (pages > 4096) pages = 4096;
+    const dim3 grid((unsigned)pages, (unsigned)a.n_seqs, (unsigned)(a.cache.n_kv * 2));
+    const uintptr_t size = sizeof(typename Elem<TYPE>::T);
+    // (head_dim values are whole 16 bytes in every type)
+    const bool vec = ((uintptr_t)a.k | (uintptr_t)a.v) % 16 == 0 &&
+                     (a.n_tokens == 1 || (a.k_stride * size % 16 == 0 && a.v_stride * size % 16 == 0));
+    // a thread per tile of a full page, or per two (44 prompts of up to 491 tokens on
+    // pages of 16, 4 heads of 96, fp16: 32.8 us with 256 threads for the 48 tiles, 14.6
+    // with 64; 34 of 44 on pages of 64, 8 heads of 192: 20.9 with 1024 for the 384, 11.5
+    // with 512)
+    const int tiles = a.cache.page * a.cache.dim / 32;
+    auto run = [&](auto threads) {
+        if (vec) kv8_append_kernel<TYPE, true, threads.value><<<grid, threads.value, 0, s>>>(a);
+        else kv8_append_kernel<TYPE, false, threads.value><<<grid, threads.value, 0, s>>>(a);
+    };
+    if (tiles <= 64) run(std::integral_constant<int, 64>{});
+    else if (tiles <= 256) run(std::integral_constant<int, 256>{});
+    else run(std::integral_constant<int, 512>{});
+    return hipGetLastError();
+}
+
 }  // namespace
 
 bool kv8_dim_supported(int dim) {
@@ -748,28 +794,9 @@ bool kv8_dim_supported(int dim) {
 }
 
 hipError_t launch_kv8_append(const Kv8AppendArgs &a, int type, hipStream_t s) {
-    // pages that max_new tokens touch at most; a sequence with more of them takes more trips
-    int64_t pages = a.max_new / a.cache.page + 2;
-    if (a.max_new <= 1) pages = 1;
-    if (pages > a.width) pages = a.width;
-    if (pages > 4096) pages = 4096;
-    const dim3 grid((unsigned)pages, (unsigned)a.n_seqs, (unsigned)(a.cache.n_kv * 2));
-    // a thread per tile of a full page
-    const int threads = std::min(std::max(a.cache.page * a.cache.dim / 32, 256), 1024);
-    const uintptr_t size = type == kF32 ? 4 : 2;
-    // (head_dim values are whole 16 bytes in every type)
-    const bool vec = ((uintptr_t)a.k | (uintptr_t)a.v) % 16 == 0 &&
-                     (a.n_tokens == 1 || (a.k_stride * size % 16 == 0 && a.v_stride * size % 16 == 0));
-    if (type == kF32)
-        vec ? kv8_append_kernel<kF32, true><<<grid, threads, 0, s>>>(a)
-            : kv8_append_kernel<kF32, false><<<grid, threads, 0, s>>>(a);
-    else if (type == kF16)
-        vec ? kv8_append_kernel<kF16, true><<<grid, threads, 0, s>>>(a)
-            : kv8_append_kernel<kF16, false><<<grid, threads, 0, s>>>(a);
-    else
-        vec ? kv8_append_kernel<kBF16, true><<<grid, threads, 0, s>>>(a)
-            : kv8_append_kernel<kBF16, false><<<grid, threads, 0, s>>>(a);
-    return hipGetLastError();
+    if (type == kF32) return append<kF32>(a, s);
+    if (type == kF16) return append<kF16>(a, s);
+    return append<kBF16>(a, s);
 }
 
 // Splits. A workgroup's start and end cost as much as three or four of its turns,

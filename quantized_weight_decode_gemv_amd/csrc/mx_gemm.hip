@@ -11,10 +11,16 @@
 // faster.
 //
 // A workgroup's wavefronts are wr x wk: wr groups of RT row tiles of 16 rows, wk
-// wavefronts sharing each group's sum over n_in. Lane l of a wavefront takes row l % 16 and, of each 16
-// blocks of 32 weights, blocks 4(l / 16) .. +3: 64 consecutive bytes of codes
-// and one 32-bit word of scales. The order of the products within the sum is
-// free as long as the activations follow it.
+// wavefronts sharing each group's sum over n_in. Lane l of a wavefront takes row
+// l % 16 and, of each 16 blocks of 32 weights, blocks 4(l / 16) .. +3: 64
+// consecutive bytes of codes and one 32-bit word of scales. The order of the products
+// within the sum is free as long as the activations follow it.
+//
+// Measured: 2048 -> 32000, one bf16 row (34.8 MB) 9.3-10.3 us, 3.5 TB/s, where a
+// loop that only loads the same bytes takes 6.5-7.0: the start of 16 wavefronts per
+// compute unit, the staged activations and the sums' meeting are the rest. 2048 ->
+// 2048 fp32 4.9 us (launch, one trip to memory, the meeting). 4096 -> 14336, 11 rows
+// of fp16 15.6 us: staging the 22 parts in every compute unit is 5 of them.
 #include <algorithm>
 
 #include "mx_device.h"
@@ -253,7 +259,8 @@ __global__ __launch_bounds__(kMaxWaves(RT) * 64) void mxfp4_gemm_kernel(MxGemmAr
 
 // One workgroup of up to 16 wavefronts per compute unit: its activations are
 // staged once. `tp` row tiles per workgroup, and as many wavefronts as fit
-// share each tile's sum.
+// share each tile's sum. (Two workgroups of eight per unit: 2048 -> 32000 9.5 us,
+// 4096 -> 14336 10.0 against 9.6, 2048 -> 5632 fp32 5.2 against 4.9.)
 constexpr int kWorkgroups = 256;
 
 template <int TYPE, int NT, int RT>

@@ -4,6 +4,12 @@
 // E8M0 byte per lane for the 32 values that the lane holds, and accumulates in
 // fp32 (65,536 operations in 16 cycles: 10 PFLOP/s on the chip).
 //
+// 8192 x 4096 -> 28672 (bf16 C) takes 545-565 us, 3.4-3.5 PFLOP/s. Without its stores
+// (470 MB, 100 us at copy rate, which one workgroup per compute unit overlaps little)
+// it takes 451, without stores and loads 371: the products alone, at the 7 PFLOP/s
+// that the chip's power leaves them on random data (9.5 on zeros), would take 275.
+// 509 x 2048 -> 5632: 10.2 us, launch and eight stages' latency.
+//
 // A workgroup holds BM x BN of C and walks n_in in stages of 256: 128 bytes of
 // codes and 8 of scales per row. Codes come by LDS DMA, a whole 128-byte line per
 // row, into the other of two buffers; the 16-byte granules of a row
