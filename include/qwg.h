@@ -625,7 +625,8 @@ int qwg_matmul_mxfp4(void *c, int type, const void *a_codes, const void *a_scale
  * max_len is the largest length, if known, or 0: it shapes the split only. The
  * positions are split over workgroups where there are few rows; the parts then
  * meet in `workspace` (device, 16-byte aligned, qwg_kv8_attend_workspace bytes
- * for the same arguments, which may be 0; or a negative status), which is the
+ * for the same arguments, which may be 0, and is where the table holds at most 1024
+ * positions, 512 for a head_dim above 128; or a negative status), which is the
  * caller's: calls that may overlap in time need one each.
  */
 typedef struct qwg_kv8 {

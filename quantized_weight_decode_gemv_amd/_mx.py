@@ -312,9 +312,11 @@ def kv8_attend(q: torch.Tensor, k_pages: torch.Tensor, k_scales: torch.Tensor,
     out = _out(out, q.shape, q)
     most = max_len or 0
     ref = ctypes.byref(cache)
-    size = lib().qwg_kv8_attend_workspace(ref, width, n_seqs, q_len, heads, window, most)
-    if size < 0:
-        _check(-size, "qwg_kv8_attend_workspace")
+    size = 0  # (short tables never need a workspace, and a small call's time is the host's)
+    if width * cache.page_tokens > (1024 if dim <= 128 else 512):
+        size = lib().qwg_kv8_attend_workspace(ref, width, n_seqs, q_len, heads, window, most)
+        if size < 0:
+            _check(-size, "qwg_kv8_attend_workspace")
     # of this call's stream (or of the graph that captures it): no two calls share one
     space = table.new_empty(size // 4) if size else None
     _run("qwg_kv8_attend", q.device, ref, out.data_ptr(), q.data_ptr(), kind, stride,

@@ -663,7 +663,7 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
 
 // Joins the splits of a sequence: one workgroup per (query token, head), its
 // wavefronts taking the splits in turn. 4.6 us for 32 x 32 rows of 128 channels in
-// up to nine splits (40 MB at most, from the last-level cache), most of it the launch
+// up to nine splits (5 MB at most, from the last-level cache), most of it the launch
 // and two round trips; in this launch and not in the last workgroup to end, so that
 // no counter has to be cleared and the order of the sums is fixed.
 template <int TYPE, int D>

@@ -38,7 +38,7 @@ __device__ __forceinline__ Packed<TYPE> load_unit(const typename Elem<TYPE>::T *
 // Memory bounds both directions: 32000 x 2048 fp32 takes 48-50 us to encode (297 MB,
 // 6.0 TB/s) and 43-49 us to decode (6.0-7.0 TB/s); with a whole block per lane, whose
 // loads touch 64 lines at a time, decoding took 56. Non-temporal stores, ordinary
-// loads (with the hint on loads too, encoding was 5% slower).
+// loads (the hint on loads too gained nothing).
 //
 // The block's lanes find its largest magnitude in two or three cross-lane steps;
 // the hardware conversion does the division by the scale, the rounding and the

@@ -89,6 +89,9 @@ def test_attend_workspace(L):  # noqa: F811
     assert size(desc(), 2, 2, 1, 4, 0, 0) == 0              # 32 positions: one workgroup a head
     assert size(desc(), 65536, 1, 1, 8, 0, 0) > 0
     assert size(desc(), 65536, 1, 1, 8, 512, 0) == 0        # a window of 512: the same
+    for dim, width in ((64, 64), (128, 64), (192, 32), (256, 32)):  # 1024 and 512 positions on pages of 16
+        for seqs, most in ((1, 0), (1, 1), (300, 0)):
+            assert size(desc(head_dim=dim), width, seqs, 4, 32, 0, most) == 0
     assert 0 < size(desc(), 65536, 1, 1, 8, 8192, 0) < size(desc(), 65536, 1, 1, 8, 0, 0)
     assert size(desc(head_dim=80), 2, 2, 1, 4, 0, 0) == -2 and size(None, 2, 2, 1, 4, 0, 0) == -1
     assert size(desc(), 2, 2, 1, 3, 0, 0) == -2 and size(desc(), 2, 2, 1, 4, -1, 0) == -2
