@@ -602,9 +602,9 @@ int qwg_matmul_mxfp4(void *c, int type, const void *a_codes, const void *a_scale
  * exponent is the smallest with every magnitude / 2^(e-127) <= 448 (0 at
  * least), and never falls while the page fills: it is the larger of the stored
  * one (where the page holds earlier positions of this sequence) and that of the
- * new tokens; when it rises, the page's earlier codes are rounded to it. NaN and infinities
- * become NaN codes and do not count for the exponent. Slots past the new tokens
- * are left as they were. max_new (>= 1) is the number of tokens that a sequence
+ * new tokens; when it rises, the page's earlier codes are rounded to it. NaN and
+ * infinities become NaN codes and do not count for the exponent. Slots past the new
+ * tokens are left as they were. max_new (>= 1) is the number of tokens that a sequence
  * appends at most, if known, or n_tokens: it sizes the launch only. A page that
  * is written must belong to one sequence (shared pages have to be full). A token
  * whose position lies past the table, or whose table entry is no page of the
@@ -625,9 +625,9 @@ int qwg_matmul_mxfp4(void *c, int type, const void *a_codes, const void *a_scale
  * max_len is the largest length, if known, or 0: it shapes the split only. The
  * positions are split over workgroups where there are few rows; the parts then
  * meet in `workspace` (device, 16-byte aligned, qwg_kv8_attend_workspace bytes
- * for the same arguments, which may be 0, and is where the table holds at most 1024
- * positions, 512 for a head_dim above 128; or a negative status), which is the
- * caller's: calls that may overlap in time need one each.
+ * for the same arguments: 0 where the table holds at most 1024 positions, 512 for
+ * a head_dim above 128, and may be 0 elsewhere; a negative status for a refusal),
+ * which is the caller's: calls that may overlap in time need one each.
  */
 typedef struct qwg_kv8 {
     void *k_pages;
