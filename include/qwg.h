@@ -621,7 +621,8 @@ int qwg_matmul_mxfp4(void *c, int type, const void *a_codes, const void *a_scale
  * effect. A row that sees a position whose table entry is no page of the pool,
  * and every row of a sequence whose length is negative or past its table, is NaN.
  * Products are exact in fp32 sums, the softmax is fp32; probabilities keep all
- * their bits for fp32 and 16 for the 16-bit types.
+ * their bits for fp32 and are rounded for the 16-bit types, to within 2^-17 of
+ * themselves and as often up as down.
  * max_len is the largest length, if known, or 0: it shapes the split only. The
  * positions are split over workgroups where there are few rows; the parts then
  * meet in `workspace` (device, 16-byte aligned, qwg_kv8_attend_workspace bytes

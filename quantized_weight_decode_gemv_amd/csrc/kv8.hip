@@ -211,6 +211,11 @@ __device__ __forceinline__ uint32_t upper_halves(float a, float b) {
     return __builtin_amdgcn_perm(f2u(b), f2u(a), 0x07060302u);
 }
 
+// Two fp32 values rounded to bf16 (nearest, ties to even) in one word, the first one low.
+__device__ __forceinline__ uint32_t nearest_halves(float a, float b) {
+    return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+}
+
 // The block of positions that the first row's window starts in: what some row
 // sees is from there to the end, and the splits begin there.
 __device__ __forceinline__ int first_seen(int len, int q_len, int window) {
@@ -269,7 +274,8 @@ constexpr int waves_of(int d, int r, int type) {
 // us more.
 //
 // Queries and probabilities enter as bf16 parts (one to three) that hold all
-// their bits, or 16 of the probabilities' for the 16-bit types; e4m3 is exact in bf16.
+// their bits, or the nearest value of two parts for the 16-bit types' probabilities (off by
+// 2^-17 of it at most); e4m3 is exact in bf16.
 //
 // ONCE: this workgroup takes all rows of its key/value head, whose lines are then
 // read once (with the hint 32 ragged sequences of up to 8192 positions took 60 us,
@@ -527,8 +533,12 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
             }
             sum[r] += (part[0] + part[1]) + (part[2] + part[3]);
         }
-        // p * vs as bf16 parts by truncation: never infinite (p <= 1), and a NaN
-        // keeps its upper half
+        // p * vs as bf16 parts: never infinite (p <= 1, vs a power of two), and a NaN stays
+        // one. Two parts are each rounded to nearest, which leaves 2^-17 of p, as often up
+        // as down; cut off they left up to 2^-15, and outputs too small by 2^-17 of
+        // themselves, the sum of the probabilities being whole. Three hold every bit (for
+        // the 16-bit types 32 x 8192 would take 64.6 us for 63.4, 131,071 x 4 tokens 65.0 for
+        // 60.3: more than outputs of 8 or 11 bits show).
         u32x4 pp[R][2][PP];
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -538,13 +548,16 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
                 for (int i = 0; i < 4; ++i) {
                     const float p0 = s[r][k * 2 + i / 2][i % 2 * 2] * vs;
                     const float p1 = s[r][k * 2 + i / 2][i % 2 * 2 + 1] * vs;
-                    const float r0 = p0 - u2f(f2u(p0) & 0xffff0000u);
-                    const float r1 = p1 - u2f(f2u(p1) & 0xffff0000u);
-                    pp[r][k][0][i] = upper_halves(p0, p1);
-                    pp[r][k][1][i] = upper_halves(r0, r1);
-                    if constexpr (PP == 3)
+                    const uint32_t w = PP == 2 ? nearest_halves(p0, p1) : upper_halves(p0, p1);
+                    const float r0 = p0 - u2f(w << 16), r1 = p1 - u2f(w & 0xffff0000u);
+                    pp[r][k][0][i] = w;
+                    if constexpr (PP == 2) {
+                        pp[r][k][1][i] = nearest_halves(r0, r1);
+                    } else {
+                        pp[r][k][1][i] = upper_halves(r0, r1);
                         pp[r][k][2][i] = upper_halves(r0 - u2f(f2u(r0) & 0xffff0000u),
                                                       r1 - u2f(f2u(r1) & 0xffff0000u));
+                    }
                 }
 
         if (next < end) wait_vmcnt<NK>();

@@ -1,0 +1,60 @@
+"""How exact attention over the 8-bit cache is, on inputs that leave no other error to hide behind.
+
+Keys and values are powers of two or small whole numbers, exact as codes, and scores are exact in fp32
+sums, so that each test's tolerance holds the roundings that it names and nothing else."""
+import numpy as np
+import pytest
+import torch
+
+import mx_ref as ref
+import quantized_weight_decode_gemv_amd as qwg
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+TYPES = [torch.float32, torch.float16, torch.bfloat16]
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+def cache_of(k, v, page):
+    """One sequence's k and v [positions, dim], exact as codes of scale 1, in pages in reversed order."""
+    n, dim = k.shape
+    need = -(-n // page)
+    c = ref.Cache(need, 1, dim, page, np.random.default_rng(n))
+    c.ks[...], c.vs[...] = 127, 127
+    table = np.arange(need, dtype=np.int32)[::-1][None].copy()
+    for pos in range(n):
+        c.k[table[0, pos // page], 0, pos % page] = ref.encode_e4m3(k[pos])
+        c.v[table[0, pos // page], 0, :, pos % page] = ref.encode_e4m3(v[pos])
+    got_k, got_v = c.rows(table, 0, n)
+    assert np.array_equal(got_k[0], k) and np.array_equal(got_v[0], v)
+    return (dev(c.k), dev(c.ks), dev(c.v), dev(c.vs)), dev(table), dev(np.array([n], np.int32))
+
+
+def first_against_the_rest(q0, dim, page, n, key, first, rest, scale):
+    """out of queries that are q0 in channel 0 over a position of `key` there and n of zero: the first
+    has weight 1 and value `first`, the others weight exp(-scale q0 key) and value `rest`."""
+    k, v = np.zeros((n + 1, dim)), np.full((n + 1, dim), float(rest))
+    k[0, 0], v[0] = key, first
+    q = torch.zeros(1, len(q0), dim, dtype=q0.dtype, device=DEV)
+    q[0, :, 0] = q0
+    pages, table, lens = cache_of(k, v, page)
+    out = qwg.kv8_attend(q, *pages, table, lens, scale=scale)
+    p = np.exp(-scale * key * q0.cpu().double().numpy())
+    return out[0].cpu().double().numpy(), ((first + n * rest * p) / (1 + n * p))[:, None]
+
+
+@pytest.mark.parametrize("t", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dim,page,heads", [(64, 16, 16), (64, 64, 48), (96, 32, 16), (128, 64, 16), (128, 16, 48), (192, 16, 16),
+                                            (256, 128, 16), (256, 32, 40)])
+def test_probabilities_of_the_16_bit_types_are_rounded_to_nearest(t, dim, page, heads):
+    # 64 positions of weight p a little below 1 against one of weight 1 and the opposite value: the
+    # output, 64 (p - 1) / (1 + 64 p), shows p's own error. p lies in [1/2, 1), where two roundings to 8 bits
+    # leave 2^-18; exp2 leaves 2^-24, and 16 additions of up to 64 in fp32, over 65, 2^-20.
+    # (Cut off to 16 bits p is off by up to 2^-16, by 2^-17 on average.)
+    q0 = (1 + 3 * torch.rand(heads, generator=torch.Generator().manual_seed(dim + heads))).to(t).to(DEV)
+    got, want = first_against_the_rest(q0, dim, page, 64, 64.0, -64.0, 1.0, 2.0 ** -18)
+    tol = 2.0 ** -18 + 2.0 ** -24 + 2.0 ** -20 + torch.finfo(t).eps / 2 * np.abs(want)
+    assert (np.abs(got - want) <= tol).all(), np.abs((got - want) / tol).max()
