@@ -481,13 +481,13 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
 
         const bool lost = (int)page.x < 0;  // this lane's sixteen positions have no page
         float ks = e8m0(page.y & 255) * to_log2;
-        // where there is no page its V counts for nothing: not even its scale may
-        // (0 times a NaN scale is NaN)
-        const float vs = lost || vpos >= len ? 1.0f : e8m0(page.y >> 8 & 255);
+        const float vs = e8m0(page.y >> 8 & 255);
         if (lost) ks = __builtin_nanf("");
         // every row sees the whole block, or the rows' masks decide
         const bool whole = b0 + kBlk <= len - a.q_len + 1 && (window <= 0 || b0 >= len - window);
-        uint32_t seen[R];
+        uint32_t seen[R];  // of this lane's sixteen positions, which lie in one page
+#pragma unroll
+        for (int r = 0; r < R; ++r) seen[r] = 0xffffu;
         if (!whole) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -536,9 +536,10 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
         // p * vs as bf16 parts: never infinite (p <= 1, vs a power of two), and a NaN stays
         // one. Two parts are each rounded to nearest, which leaves 2^-17 of p, as often up
         // as down; cut off they left up to 2^-15, and outputs too small by 2^-17 of
-        // themselves, the sum of the probabilities being whole. Three hold every bit (for
-        // the 16-bit types 32 x 8192 would take 64.6 us for 63.4, 131,071 x 4 tokens 65.0 for
-        // 60.3: more than outputs of 8 or 11 bits show).
+        // themselves, the sum of the probabilities being whole. Three hold every bit; for
+        // the 16-bit types they cost more than outputs of 8 or 11 bits show (32 x 8192, bf16:
+        // 64.6 us for 63.4, and 0.6e-5 off the rounded exact result for 5.1e-5, a plain fp32
+        // softmax being 4.5e-5 off; 131,071 x 4 tokens: 65.0 us for 60.3).
         u32x4 pp[R][2][PP];
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -546,8 +547,11 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float p0 = s[r][k * 2 + i / 2][i % 2 * 2] * vs;
-                    const float p1 = s[r][k * 2 + i / 2][i % 2 * 2 + 1] * vs;
+                    // a page that the row does not see counts for nothing: not even its
+                    // scale may (0 times a NaN scale is NaN)
+                    const float f = seen[r] ? vs : 1.0f;
+                    const float p0 = s[r][k * 2 + i / 2][i % 2 * 2] * f;
+                    const float p1 = s[r][k * 2 + i / 2][i % 2 * 2 + 1] * f;
                     const uint32_t w = PP == 2 ? nearest_halves(p0, p1) : upper_halves(p0, p1);
                     const float r0 = p0 - u2f(w << 16), r1 = p1 - u2f(w & 0xffff0000u);
                     pp[r][k][0][i] = w;

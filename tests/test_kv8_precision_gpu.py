@@ -58,3 +58,37 @@ def test_probabilities_of_the_16_bit_types_are_rounded_to_nearest(t, dim, page, 
     got, want = first_against_the_rest(q0, dim, page, 64, 64.0, -64.0, 1.0, 2.0 ** -18)
     tol = 2.0 ** -18 + 2.0 ** -24 + 2.0 ** -20 + torch.finfo(t).eps / 2 * np.abs(want)
     assert (np.abs(got - want) <= tol).all(), np.abs((got - want) / tol).max()
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("dim,page,heads,n,window,bad", [
+    (64, 16, 2, 70, 8, [0, 1, 2]),       # before the window, in the block where it begins
+    (128, 32, 20, 60, 3, [0]),
+    (256, 16, 3, 70, 8, [1]),
+    (64, 16, 2, 65, 0, [4]),             # a last page that the newest query alone sees
+    (128, 64, 40, 129, 0, [2]),
+    (96, 128, 1, 129, 100, [1]),
+    (192, 16, 17, 33, 0, [2]),
+    (64, 16, 4, 33, 16, [0, 2]),         # both
+    (64, 16, 4, 32, 16, [0]),            # a page whose last position the older query alone sees
+])
+def test_a_nan_scale_reaches_the_rows_that_see_its_page(t, dim, page, heads, n, window, bad):
+    rng = np.random.default_rng(n + dim)
+    k, v = rng.integers(-4, 5, (2, n, dim)).astype(np.float64)
+    pages, table, lens = cache_of(k, v, page)
+    q = torch.from_numpy(rng.standard_normal((1, 2, heads, dim))).to(t).to(DEV)
+    want = qwg.kv8_attend(q, *pages, table, lens, window=window)
+    sees = []
+    for r in range(2):
+        last = n - 2 + r
+        first = max(0, last - window + 1) if window else 0
+        sees.append(any(p * page <= last and first < (p + 1) * page for p in bad))
+    assert not all(sees)
+    ids = table[0, torch.tensor(bad, device=DEV)].long()
+    for which in (1, 3):  # K's scale, then V's
+        spoiled = list(pages)
+        spoiled[which] = pages[which].clone()
+        spoiled[which][ids] = 255
+        got = qwg.kv8_attend(q, *spoiled, table, lens, window=window)
+        for r in range(2):
+            assert bool(torch.isnan(got[0, r]).all()) if sees[r] else torch.equal(got[0, r], want[0, r]), (which, r)
