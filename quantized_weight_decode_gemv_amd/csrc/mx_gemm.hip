@@ -22,6 +22,7 @@
 // 2048 fp32 4.9 us (launch, one trip to memory, the meeting). 4096 -> 14336, 11 rows
 // of fp16 15.6 us: staging the 22 parts in every compute unit is 5 of them.
 #include <algorithm>
+#include <type_traits>
 
 #include "mx_device.h"
 
@@ -34,6 +35,16 @@ constexpr int kStep = kStepBlocks * kMxBlock;         // 512 weights
 // Staged activation parts, at most (16 rows of fp32, 4096 x 14336: 37 us with 128 KB,
 // 31 with 156).
 constexpr int kLdsX = 156 * 1024;
+
+// Where a wavefront takes more than kFold steps (of 16 products, each of 32 terms), its sums
+// are added to a second set after every kFold of them and begin anew. One fp32 chain over
+// all of a long row was off by 5.5e-5 of sum |w x| where the terms have one sign and repeat
+// (65536 -> 32000; 14336 -> 70016 1.2e-5); chains of 64 products, and of up to 32 of
+// those, by 1.5e-6 (2.1e-6 with 16 rows), for 0 to 1% of the time. One row tile and several
+// column tiles keep one chain, of a step per chunk (16 x 14336 -> 4096 fp32 4.2e-6): there
+// the second set leaves too few registers for the activations' reads, 34.2 us for 30.5.
+constexpr int kFold = 4;
+constexpr bool folds(int nt, int rt) { return nt == 1 || rt == 2; }
 
 // Wavefronts of a workgroup at most: two row tiles' codes, twice (the next
 // step's too), need more than the 128 registers that 16 wavefronts leave.
@@ -130,7 +141,7 @@ __device__ __forceinline__ void store_parts(uint8_t *to, int pitch, const Unit<T
 
 // RT: row tiles that a wavefront takes together (one read of the activations
 // for both); NT: 16-column tiles of activation parts.
-template <int TYPE, int NT, int RT, bool WORDS>
+template <int TYPE, int NT, int RT, bool WORDS, bool FOLD>
 __global__ __launch_bounds__(kMaxWaves(RT) * 64) void mxfp4_gemm_kernel(MxGemmArgs a, int wk, int chunk) {
     typedef typename Elem<TYPE>::T T;
     constexpr int P = Elem<TYPE>::pieces;
@@ -152,11 +163,18 @@ __global__ __launch_bounds__(kMaxWaves(RT) * 64) void mxfp4_gemm_kernel(MxGemmAr
     }
     const int cols = a.batch * P;
     const int pitch = pitch_of(chunk);
-    f32x4 acc[RT][NT];
+    f32x4 acc[RT][NT], sum[RT][NT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[r][t] = f32x4{0, 0, 0, 0};
+        for (int t = 0; t < NT; ++t) acc[r][t] = sum[r][t] = f32x4{0, 0, 0, 0};
+    int turns = 0;
+    auto fold = [&] {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sum[r][t] += acc[r][t], acc[r][t] = f32x4{0, 0, 0, 0};
+    };
     // a column past the last part reads some part; its sums are not used
     int col[NT];
 #pragma unroll
@@ -229,8 +247,10 @@ __global__ __launch_bounds__(kMaxWaves(RT) * 64) void mxfp4_gemm_kernel(MxGemmAr
 #pragma unroll
             for (int r = 0; r < RT; ++r) cur[r] = next[r];
             if (st + 2 * wk < steps) load(next, st + 2 * wk);
+            if (FOLD && ++turns % kFold == 0) fold();
         }
     }
+    if constexpr (FOLD) fold();
     // every wavefront's sums meet in LDS: [wave][row tile][column][row]
     __syncthreads();
     float *sums = (float *)lds;
@@ -238,7 +258,7 @@ __global__ __launch_bounds__(kMaxWaves(RT) * 64) void mxfp4_gemm_kernel(MxGemmAr
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-            *(f32x4 *)(sums + (((wave * RT + r) * NT + t) * 16 + n) * 16 + g * 4) = acc[r][t];
+            *(f32x4 *)(sums + (((wave * RT + r) * NT + t) * 16 + n) * 16 + g * 4) = (FOLD ? sum : acc)[r][t];
     __syncthreads();
     for (int i = threadIdx.x; i < wr * RT * 16 * a.batch; i += blockDim.x) {
         const int m = i & 15, w = (i >> 4) % (wr * RT), b = (i >> 4) / (wr * RT);
@@ -282,11 +302,17 @@ hipError_t launch(const MxGemmArgs &a, int wr, hipStream_t s) {
     if (lds < join) lds = join;
     const unsigned grid = (unsigned)((tiles + wr * RT - 1) / (wr * RT));
     const bool words = a.n_in % (4 * kMxBlock) == 0 && (uintptr_t)a.scales % 4 == 0;
-    if (words)
-        mxfp4_gemm_kernel<TYPE, NT, RT, true><<<grid, wk * wr * 64, lds, s>>>(a, wk, chunk);
-    else
-        mxfp4_gemm_kernel<TYPE, NT, RT, false><<<grid, wk * wr * 64, lds, s>>>(a, wk, chunk);
-    return hipGetLastError();
+    auto run = [&](auto fold) {
+        if (words) mxfp4_gemm_kernel<TYPE, NT, RT, true, fold.value><<<grid, wk * wr * 64, lds, s>>>(a, wk, chunk);
+        else mxfp4_gemm_kernel<TYPE, NT, RT, false, fold.value><<<grid, wk * wr * 64, lds, s>>>(a, wk, chunk);
+        return hipGetLastError();
+    };
+    if constexpr (folds(NT, RT)) {
+        // the steps of one wavefront at most: every wk-th of each chunk
+        const int turns = (steps + fit - 1) / fit * ((fit + wk - 1) / wk);
+        if (turns > kFold) return run(std::true_type{});
+    }
+    return run(std::false_type{});
 }
 
 template <int TYPE, int NT>

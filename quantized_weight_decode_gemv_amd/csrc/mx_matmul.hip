@@ -10,6 +10,10 @@
 // that the chip's power leaves them on random data (9.5 on zeros), would take 275.
 // 509 x 2048 -> 5632: 10.2 us, launch and eight stages' latency.
 //
+// An output is one chain of n_in / 128 fp32 sums (the accumulators of a large tile leave no
+// registers for a second set): where terms of one sign repeat it is off by 1.8e-6 of their
+// sum at an n_in of 4096, 6.2e-6 at 14336, 3.3e-5 at 65536.
+//
 // A workgroup holds BM x BN of C and walks n_in in stages of 256: 128 bytes of
 // codes and 8 of scales per row. Codes come by LDS DMA, a whole 128-byte line per
 // row, into the other of two buffers; the 16-byte granules of a row
