@@ -569,9 +569,9 @@ int qwg_chain_destroy(qwg_chain *chain);
  * infinity). A NaN scale makes its row NaN.
  *
  * qwg_matmul_mxfp4: C[m, r] = sum_k A[m, k] W[r, k], A [n_rows, n_in] and W
- * [n_out, n_in] both MXFP4, c [n_rows][n_out] of `type`; the same bound with
- * c = 16 + n_in / 64 (where terms of one sign repeat 1.8e-6 of their sum at an n_in of
- * 4096, 6.2e-6 at 14336, 3.3e-5 at 65536).
+ * [n_out, n_in] both MXFP4, c [n_rows][n_out] of `type`, n_rows n_out <= 2^38; the
+ * same bound with c = 16 + n_in / 64 (where terms of one sign repeat 1.8e-6 of their
+ * sum at an n_in of 4096, 6.2e-6 at 14336, 3.3e-5 at 65536).
  */
 int qwg_encode_mxfp4(void *codes, void *scales, const void *x, int type, int64_t n_rows,
                      int64_t n_in, int64_t x_stride, void *stream);

@@ -169,7 +169,8 @@ def gemv_mxfp4(w: torch.Tensor, scales: torch.Tensor, x: torch.Tensor,
 def matmul_mxfp4(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
                  dtype=torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
     """C = A W^T for two MXFP4 matrices (codes and scales of each, as encode_mxfp4 gives them),
-    A [n_rows, n_in] and W [n_out, n_in] -> [n_rows, n_out] of `dtype`."""
+    A [n_rows, n_in] and W [n_out, n_in] (at most 2^24 rows each and 2^38 outputs) -> [n_rows, n_out]
+    of `dtype`."""
     n_rows, n_in = _matrix(a, a_scales, "a")
     n_out, w_in = _matrix(w, w_scales, "w", a.device)
     if w_in != n_in:

@@ -27,6 +27,10 @@ bool mx_width(int64_t n_in) {
 
 bool mx_count(int64_t n) { return n >= 1 && n <= QWG_MAX_N_OUT; }
 
+// Outputs of qwg_matmul_mxfp4: a grid of large tiles (2^22 and the edges' at most) then
+// stays below the 2^32 threads of a launch. In 16 bits they are 512 GB, more than the memory.
+constexpr int64_t kMaxOutputs = (int64_t)1 << 38;
+
 // Compute units of a current MI355X; the plan of a split needs no exact figure.
 constexpr int kCus = 256;
 
@@ -105,7 +109,8 @@ int qwg_matmul_mxfp4(void *c, int type, const void *a_codes, const void *a_scale
                      int64_t n_out, void *stream) {
     if (!c || !a_codes || !a_scales || !w_codes || !w_scales) return QWG_ERR_NULL;
     if (!known_type(type)) return QWG_ERR_TYPE;
-    if (!mx_width(n_in) || !mx_count(n_out) || !mx_count(n_rows)) return QWG_ERR_SHAPE;
+    if (!mx_width(n_in) || !mx_count(n_out) || !mx_count(n_rows) || n_rows * n_out > kMaxOutputs)
+        return QWG_ERR_SHAPE;
     if (!aligned(a_codes, 16) || !aligned(w_codes, 16) || !aligned(c, size_of(type)))
         return QWG_ERR_ALIGN;
     const MxMatmulArgs a = {(const uint8_t *)a_codes, (const uint8_t *)a_scales,

@@ -368,7 +368,6 @@ template <int TYPE, int TM, int TN, int WM, int WN>
 hipError_t launch(const MxMatmulArgs &a, hipStream_t s) {
     constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
     const int64_t rt = (a.n_rows + BM - 1) / BM, ot = (a.n_out + BN - 1) / BN;
-    if (rt * ot > INT32_MAX) return hipErrorInvalidValue;
     constexpr size_t lds = 2 * (BM + BN) * (kStageBytes + 8);
     mxfp4_matmul_kernel<TYPE, TM, TN, WM, WN>
         <<<(unsigned)(rt * ot), WM * WN * 64, lds, s>>>(a, (int)rt, (int)ot);

@@ -129,3 +129,9 @@ def test_e4m3_by_hand():
     assert np.array_equal(ref.encode_e4m3(ref.E4M3[:127]), np.arange(127))
     assert ref.encode_e4m3(np.array([1.0625, 1.1875, 2.0 ** -10, 1.5 * 2.0 ** -9, np.inf])).tolist() == [0x38, 0x3A, 0, 2, 127]
     assert [ref.page_exponent(np.array([v])) for v in (448.0, 449.0, 0.0, 1.75, 1.0)] == [127, 128, 0, 119, 119]
+
+
+@pytest.mark.parametrize("n_rows,n_out", [(1 << 24, 1 << 24), (1 << 24, (1 << 14) + 1), ((1 << 19) + 1, 1 << 19)])
+def test_matmul_refuses_more_outputs_than_a_launch_takes(L, n_rows, n_out):  # noqa: F811
+    # the size is refused as such, before any HIP call
+    assert L.qwg_matmul_mxfp4(FAKE, 2, FAKE, FAKE, FAKE, FAKE, n_rows, 64, n_out, None) == 2
