@@ -92,3 +92,39 @@ def test_a_nan_scale_reaches_the_rows_that_see_its_page(t, dim, page, heads, n, 
         got = qwg.kv8_attend(q, *spoiled, table, lens, window=window)
         for r in range(2):
             assert bool(torch.isnan(got[0, r]).all()) if sees[r] else torch.equal(got[0, r], want[0, r]), (which, r)
+
+
+def fp32_queries(low, high, heads, seed):
+    """Queries whose significand ends in eight ones, spread over [low, high] when multiplied by 64 * 2^-6."""
+    x = torch.linspace(low, high, heads, dtype=torch.float32) * (1 + 0.01 * torch.rand(heads, generator=torch.Generator().manual_seed(seed)))
+    return (x.view(torch.int32) | 0xFF).view(torch.float32)
+
+
+def fp32_tolerance(x):
+    """Relative, of the output n p / (1 + n p) with p = exp(-x), in fp32: the score is exact, its product with
+    the scale and log2 e is off by 1.5 u x (u = 2^-24), exp2 by 2 u, so numerator and denominator by
+    3 u x + 4 u together; at most 12 u in the numerator's sums (6 instructions and the join), 8 u in the
+    denominator's and 4 u in the division. In all (3 x + 28) u."""
+    return (3 * x + 32) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dim,page,heads", [(64, 16, 16), (64, 64, 48), (96, 32, 16), (96, 16, 40), (128, 64, 16), (128, 16, 48),
+                                            (192, 16, 16), (192, 64, 48), (256, 128, 16), (256, 32, 40)])
+@pytest.mark.parametrize("low,high", [(0.02, 1.0), (4.0, 9.0)])
+def test_fp32_queries_and_probabilities_keep_all_their_bits(dim, page, heads, low, high):
+    # near scores show a probability's own error, far ones (where n p is 1 or less) a query's: sixteen bits
+    # of a probability are up to 2^-16 of it too small, sixteen of these queries 255 2^-24, x times that in p
+    q0 = fp32_queries(low, high, heads, dim + heads)
+    got, want = first_against_the_rest(q0.to(DEV), dim, page, 64, 64.0, 0.0, 1.0, 2.0 ** -6)
+    tol = fp32_tolerance(q0.double().numpy())[:, None] * want
+    assert (np.abs(got - want) <= tol).all(), np.abs((got - want) / tol).max()
+
+
+@pytest.mark.parametrize("dim,page,heads", [(64, 16, 16), (128, 64, 48), (256, 32, 40)])
+def test_fp16_queries_keep_all_their_bits(dim, page, heads):
+    # eleven bits, the last three of them ones: eight would be 7 2^-10 off, x times that in p. The tolerance of
+    # fp32, 2^-17 for a probability's own rounding (p may lie anywhere) and half a step of the output
+    q0 = (torch.linspace(4.0, 9.0, heads).half().view(torch.int16) | 7).view(torch.float16)
+    got, want = first_against_the_rest(q0.to(DEV), dim, page, 64, 64.0, 0.0, 1.0, 2.0 ** -6)
+    tol = (fp32_tolerance(q0.double().numpy())[:, None] + 2.0 ** -17 + 2.0 ** -11) * want
+    assert (np.abs(got - want) <= tol).all(), np.abs((got - want) / tol).max()
