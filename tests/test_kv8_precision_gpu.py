@@ -128,3 +128,25 @@ def test_fp16_queries_keep_all_their_bits(dim, page, heads):
     got, want = first_against_the_rest(q0.to(DEV), dim, page, 64, 64.0, 0.0, 1.0, 2.0 ** -6)
     tol = (fp32_tolerance(q0.double().numpy())[:, None] + 2.0 ** -17 + 2.0 ** -11) * want
     assert (np.abs(got - want) <= tol).all(), np.abs((got - want) / tol).max()
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("dim,page,n", [(64, 16, 700), (96, 32, 3000), (128, 64, 3000), (192, 16, 1100), (256, 128, 3000)])
+@pytest.mark.parametrize("steep", [7, 15])
+def test_one_position_takes_all(t, dim, page, n, steep):
+    # scores are whole multiples of 2^(steep - 3), the largest at least seven of them above every other: e^-112 and
+    # less is 0 in fp32, so a row is the value of its position, exactly; of two with one score, their mean
+    rng = np.random.default_rng(n + dim)
+    k = rng.integers(-8, 9, (n, dim)).astype(np.float64)
+    v = ref.E4M3[rng.integers(0, 127, (n, dim)) + 128 * rng.integers(0, 2, (n, dim))]
+    # in the first and last positions of blocks of 64 and of splits; the last two heads have two winners
+    at = [[0], [63], [64], [255], [256], [n // 2], [n - 1], [1, n - 2], [200, n // 2 + 1]]
+    q = torch.zeros(1, len(at), dim, dtype=t, device=DEV)
+    for h, where in enumerate(at):
+        q[0, h, 7 * h] = 2.0 ** steep if h % 2 else -2.0 ** steep
+        k[where, 7 * h] = 15 if h % 2 else -15
+    pages, table, lens = cache_of(k, v, page)
+    want = torch.from_numpy(np.stack([v[where].sum(0) / len(where) for where in at])).to(t)
+    for most in (None, n):  # splits by the table and by the length
+        got = qwg.kv8_attend(q, *pages, table, lens, scale=0.125, max_len=most)
+        assert torch.equal(got[0].cpu(), want)
