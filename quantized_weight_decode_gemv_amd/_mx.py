@@ -15,6 +15,9 @@ MX_MAX_BATCH = 16
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 KV8_HEAD_DIMS = (64, 96, 128, 192, 256)
 KV8_PAGE_TOKENS = (16, 32, 64, 128)
+# Positions in a table up to which qwg_kv8_attend_workspace is 0 for every call, by head_dim (qwg.h):
+# such calls, whose time is the host's, do not ask.
+_ALONE = {64: 1024, 96: 1024, 128: 1024, 192: 512, 256: 512}
 
 
 class Kv8Desc(ctypes.Structure):
@@ -55,7 +58,7 @@ def _type(dtype, name: str) -> int:
 
 
 # torch's own accessors of the current device and of a stream's handle; torch.cuda's build a
-# Stream object (1.9 us of a small call's 11 on the host).
+# Stream object (1.9 us on the host, where a small call takes 8 to 12 in all).
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 _fns: dict = {}
@@ -313,8 +316,8 @@ def kv8_attend(q: torch.Tensor, k_pages: torch.Tensor, k_scales: torch.Tensor,
     out = _out(out, q.shape, q)
     most = max_len or 0
     ref = ctypes.byref(cache)
-    size = 0  # (short tables never need a workspace, and a small call's time is the host's)
-    if width * cache.page_tokens > (1024 if dim <= 128 else 512):
+    size = 0
+    if width * cache.page_tokens > _ALONE[dim]:
         size = lib().qwg_kv8_attend_workspace(ref, width, n_seqs, q_len, heads, window, most)
         if size < 0:
             _check(-size, "qwg_kv8_attend_workspace")

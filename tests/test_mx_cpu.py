@@ -135,3 +135,22 @@ def test_e4m3_by_hand():
 def test_matmul_refuses_more_outputs_than_a_launch_takes(L, n_rows, n_out):  # noqa: F811
     # the size is refused as such, before any HIP call
     assert L.qwg_matmul_mxfp4(FAKE, 2, FAKE, FAKE, FAKE, FAKE, n_rows, 64, n_out, None) == 2
+
+
+def test_the_binding_asks_for_a_workspace_wherever_one_is_needed(L):  # noqa: F811
+    """Up to the positions that the binding takes for short, and the header names, the workspace is 0
+    whatever the sequences, heads, query tokens, window and known length are."""
+    assert tuple(_mx._ALONE) == _mx.KV8_HEAD_DIMS
+    for dim, most in _mx._ALONE.items():
+        assert most == (1024 if dim <= 128 else 512)
+        for page in _mx.KV8_PAGE_TOKENS:
+            for kv, group, q_len in ((1, 1, 1), (1, 16, 1), (8, 4, 1), (2, 17, 3), (8, 1, 128), (1024, 1, 1)):
+                c = desc(head_dim=dim, page_tokens=page, n_kv_heads=kv)
+                for seqs in (1, 2, 9, 33, 64, 300, 65535):
+                    for window in (0, 1, 100, most, 1 << 40):
+                        for known in (0, 1, most // 2, most, 1 << 40):
+                            for width in (1, most // page):
+                                assert L.qwg_kv8_attend_workspace(c, width, seqs, q_len, kv * group, window, known) == 0
+        # and one twice as long needs one, for one sequence at least
+        c = desc(head_dim=dim, page_tokens=128, n_kv_heads=1)
+        assert L.qwg_kv8_attend_workspace(c, 2 * most // 128, 1, 1, 1, 0, 0) > 0
