@@ -1,7 +1,9 @@
 """Binding of libqwg's MXFP4 and 8-bit cache calls (include/qwg.h). Argument
 marshalling only, as in _binding: every step of the computation runs in the library's
 HIP kernels, calls enqueue on torch's current stream of the tensors' device, and no
-call waits, allocates inside the library or keeps anything."""
+call waits, allocates inside the library or keeps anything. Codes, pages, the activations of
+gemm_mxfp4 and gemv_mxfp4 and dequant_mxfp4's result start on 16 bytes, as whole tensors do; a view
+that does not is refused with a QwgError."""
 from __future__ import annotations
 
 import ctypes
@@ -139,7 +141,8 @@ def dequant_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.float32
 def gemm_mxfp4(w: torch.Tensor, scales: torch.Tensor, x: torch.Tensor,
                out: torch.Tensor | None = None) -> torch.Tensor:
     """Y = X W^T for MXFP4 weights (w uint8 [n_out, n_in/2], scales uint8 [n_out, n_in/32]) and
-    X [batch, n_in] (1 <= batch <= 16; fp32, fp16 or bf16) -> [batch, n_out] of X's type."""
+    X [batch, n_in] (1 <= batch <= 16; fp32, fp16 or bf16; starting on 16 bytes) -> [batch, n_out] of
+    X's type."""
     n_out, n_in = _matrix(w, scales, "w")
     _on_device(x, "x", w.device)
     kind = _type(x.dtype, "x")
@@ -157,7 +160,8 @@ def gemm_mxfp4(w: torch.Tensor, scales: torch.Tensor, x: torch.Tensor,
 
 def gemv_mxfp4(w: torch.Tensor, scales: torch.Tensor, x: torch.Tensor,
                out: torch.Tensor | None = None) -> torch.Tensor:
-    """y = W x for MXFP4 weights (as gemm_mxfp4) and x [n_in] -> [n_out] of x's type."""
+    """y = W x for MXFP4 weights (as gemm_mxfp4) and x [n_in], starting on 16 bytes -> [n_out] of x's
+    type."""
     n_out, n_in = _matrix(w, scales, "w")
     _plain(x, "x", x.dtype if isinstance(x, torch.Tensor) else None, w.device)
     kind = _type(x.dtype, "x")

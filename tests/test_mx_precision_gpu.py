@@ -57,3 +57,22 @@ def test_matmul_terms_of_one_sign(rows, n_out, n_in):
         for i, j in ((0, 0), (rows - ROWS, n_out - ROWS)):
             off = ((y[i:i + ROWS, j:j + ROWS].double() - want).abs() / want).max()
             assert float(off) <= (16 + n_in / 64) * U + U, (spread, period, float(off))
+
+
+@pytest.mark.parametrize("t", [torch.float32, torch.float16, torch.bfloat16])
+def test_views_that_start_between_16_bytes_are_refused(t):
+    c, s = qwg.encode_mxfp4(torch.randn(4, 64, device=DEV))
+    x = torch.zeros(72, device=DEV, dtype=t)
+    odd = torch.zeros(4 * 32 + 1, device=DEV, dtype=torch.uint8)[1:].view(4, 32)
+    cache = qwg.kv8_pages(2, 1, 64, 16, device=DEV)
+    pages = torch.zeros(2 * 16 * 64 + 1, device=DEV, dtype=torch.uint8)[1:].view(2, 1, 16, 64)
+    table, lens = torch.zeros(1, 2, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    k = torch.zeros(1, 1, 64, device=DEV, dtype=t)
+    for call in (lambda: qwg.gemm_mxfp4(c, s, x[1:65].view(1, 64)), lambda: qwg.gemv_mxfp4(c, s, x[1:65]),
+                 lambda: qwg.gemm_mxfp4(odd, s, x[:64].view(1, 64)), lambda: qwg.matmul_mxfp4(odd, s, c, s, dtype=t),
+                 lambda: qwg.matmul_mxfp4(c, s, odd, s, dtype=t), lambda: qwg.dequant_mxfp4(odd, s, dtype=t),
+                 lambda: qwg.dequant_mxfp4(c[:1], s[:1], dtype=t, out=x[1:65].view(1, 64)),
+                 lambda: qwg.kv8_append(k, k, pages, *cache[1:], table, lens),
+                 lambda: qwg.kv8_attend(k, pages, *cache[1:], table, lens)):
+        with pytest.raises(qwg.QwgError):
+            call()
