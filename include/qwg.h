@@ -561,12 +561,12 @@ int qwg_chain_destroy(qwg_chain *chain);
  *
  * qwg_gemm_mxfp4: Y[b, r] = sum_k W[r, k] X[b, k], 1 <= batch <=
  * QWG_MX_MAX_BATCH; x [batch][n_in] (16-byte aligned) and y [batch][n_out] of
- * `type`. qwg_gemv_mxfp4 is batch 1. Activations keep all their bits; sums are
- * fp32 in an order fixed by the sizes: |y - exact| <= c 2^-24 sum_k |W X| before the
- * one rounding to `type`, c = 16 + n_in / 32, and 112 at most for one row (whose
- * error stays below 2e-6 sum_k |W X| also where terms of one sign repeat, the worst
- * found), for inputs whose weights lie below 2^126 (larger ones overflow to
- * infinity). A NaN scale makes its row NaN.
+ * `type`. qwg_gemv_mxfp4 is batch 1. Activations keep all their bits (fp32 ones
+ * below 2^-110 those above 2^-133); sums are fp32 in an order fixed by the sizes:
+ * |y - exact| <= c 2^-24 sum_k |W X| before the one rounding to `type`, c = 16 +
+ * n_in / 32, and 112 at most for one row (whose error stays below 2e-6 sum_k |W X|
+ * also where terms of one sign repeat, the worst found), for inputs whose weights
+ * lie below 2^126 (larger ones overflow to infinity). A NaN scale makes its row NaN.
  *
  * qwg_matmul_mxfp4: C[m, r] = sum_k A[m, k] W[r, k], A [n_rows, n_in] and W
  * [n_out, n_in] both MXFP4, c [n_rows][n_out] of `type`, n_rows n_out <= 2^38; the
@@ -626,7 +626,9 @@ int qwg_matmul_mxfp4(void *c, int type, const void *a_codes, const void *a_scale
  * and every row of a sequence whose length is negative or past its table, is NaN.
  * Products are exact in fp32 sums, the softmax is fp32; probabilities keep all
  * their bits for fp32 and are rounded for the 16-bit types, to within 2^-17 of
- * themselves and as often up as down.
+ * themselves and as often up as down. What lies below 2^-133 of a query, or of a
+ * probability times its page's V scale, is lost; the sums of q times K's codes, which
+ * are scaled afterwards, have to lie within fp32.
  * max_len is the largest length, if known, or 0: it shapes the split only. The
  * positions are split over workgroups where there are few rows; the parts then
  * meet in `workspace` (device, 16-byte aligned, qwg_kv8_attend_workspace bytes

@@ -150,3 +150,28 @@ def test_one_position_takes_all(t, dim, page, n, steep):
     for most in (None, n):  # splits by the table and by the length
         got = qwg.kv8_attend(q, *pages, table, lens, scale=0.125, max_len=most)
         assert torch.equal(got[0].cpu(), want)
+
+
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("scale", [0, 5, 12, 20])
+def test_the_smallest_values(t, dim, page, scale):
+    # a probability times its page's V scale loses what lies below 2^-133, in each of n positions: 2^-133 times
+    # the sum of the codes' values at most, the largest probability being 1 before the division
+    rng = np.random.default_rng(scale + dim)
+    n = 3 * page + 5
+    k, v = rng.integers(-4, 5, (n, dim)).astype(np.float64), rng.integers(1, 9, (n, dim)).astype(np.float64)
+    pages, table, lens = cache_of(k, v, page)
+    pages[3].fill_(scale)
+    q = torch.from_numpy(rng.standard_normal((1, 8, dim))).to(t).to(DEV)
+    got = qwg.kv8_attend(q, *pages, table, lens)[0].cpu().double().numpy()
+    x = q[0].cpu().double().numpy() @ k.T * dim ** -0.5
+    p = np.exp(x - x.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    small = 2.0 ** (scale - 127)
+    want = p @ (v * small)
+    # a score: 3 D/32 + 36 roundings of sum |q k|; a probability twice that, as does their sum; 2^-17 for a
+    # probability's own rounding in the 16-bit types and 2^-17 for the sums, exp2 and the division
+    size = (np.abs(q[0].cpu().double().numpy()) @ np.abs(k.T)).max(1, keepdims=True) * dim ** -0.5
+    tol = (4 * (3 * dim / 32 + 36) * 2.0 ** -24 * size + 2.0 ** -16 + torch.finfo(t).eps / 2) * want + 2.0 ** -133 * v.sum(0) + 2.0 ** -133
+    assert (np.abs(got - want) <= tol).all(), (np.abs(got - want) / tol).max()

@@ -76,3 +76,16 @@ def test_views_that_start_between_16_bytes_are_refused(t):
                  lambda: qwg.kv8_attend(k, pages, *cache[1:], table, lens)):
         with pytest.raises(qwg.QwgError):
             call()
+
+
+@pytest.mark.parametrize("batch,n_out", [(1, 640), (7, 640), (16, 8192)])
+@pytest.mark.parametrize("e", [-104, -110, -116, -122, -126, -131])
+def test_gemm_smallest_fp32_activations(batch, n_out, e):
+    # an activation's bits below 2^-133, the last of its three parts' smallest, are left out; the output's
+    # own step, 2^-149, is finer than that of any term
+    g = torch.Generator(device=DEV).manual_seed(batch - e)
+    c, s, w = repeated(g, 1024, 3, 512)
+    x = (1 + torch.rand(batch, 1024, device=DEV, generator=g)) * 2.0 ** e
+    y = qwg.gemm_mxfp4(c.repeat(n_out // ROWS, 1), s.repeat(n_out // ROWS, 1), x)[:, :ROWS].double()
+    want = x.double() @ w.T
+    assert bool(((y - want).abs() <= (16 + 1024 / 32) * U * want + 2.0 ** -133 * w.sum(1) + 2.0 ** -149 * 32).all())
