@@ -302,7 +302,8 @@ def kv8_attend(q: torch.Tensor, k_pages: torch.Tensor, k_scales: torch.Tensor,
     slice of a fused q|k|v result may be given). lens int32 [n_seqs]: the positions held, the
     queries' own among them; query t of a sequence sees positions up to lens - q_len + t, the last
     `window` of them (0: all). scale defaults to head_dim ** -0.5. max_len: the largest length, if
-    known. Returns a contiguous tensor of q's shape and type; rows that see nothing are zero."""
+    known; a table cut to it is faster than one that is much wider. Returns a contiguous tensor of q's
+    shape and type; rows that see nothing are zero."""
     _on_device(q, "q")
     kind = _type(q.dtype, "q")
     cache = _cache(k_pages, k_scales, v_pages, v_scales, q.device)

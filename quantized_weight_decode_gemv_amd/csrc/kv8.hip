@@ -49,7 +49,7 @@ __device__ __forceinline__ uint32_t fp8_shifted(uint32_t w, float shift) {
 // takes four consecutive positions of eight channels: 8-byte stores to a K page,
 // 4-byte stores (one per channel) to a transposed V page. The page's largest new
 // magnitude comes first (one pass over the values, a cross-lane and an LDS step);
-// a thread's last tile stays in registers meanwhile, so that a page of up to 256
+// a thread's last tile stays in registers meanwhile, so that a page of up to `threads`
 // tiles is read once. Memory bounds it where there is much: 9 prompts of up to 2000
 // tokens, 8 heads of 128, bf16 (62 MB read and written): 17.4 us, 3.5 TB/s. One token
 // each of 33 sequences takes 5.4 us: the launch and four round trips in a row (length,

@@ -76,7 +76,7 @@ hipError_t launch_mxfp4_gemm(const MxGemmArgs &a, int type, hipStream_t s);
 hipError_t launch_mxfp4_matmul(const MxMatmulArgs &a, int type, hipStream_t s);
 hipError_t launch_kv8_append(const Kv8AppendArgs &a, int type, hipStream_t s);
 bool kv8_dim_supported(int dim);
-// Row tiles of 16 (query token, head of the group) rows that one workgroup takes.
+// Sets what shapes the launch: row_tiles, chunk, max_splits, few and brief.
 void kv8_attend_plan(Kv8AttendArgs &a, int64_t max_len, int cus);
 int64_t kv8_attend_partial_bytes(const Kv8AttendArgs &a);
 hipError_t launch_kv8_attend(const Kv8AttendArgs &a, int type, hipStream_t s);
