@@ -629,14 +629,14 @@ int qwg_matmul_mxfp4(void *c, int type, const void *a_codes, const void *a_scale
  * themselves and as often up as down. What lies below 2^-133 of a query, or of a
  * probability times its page's V scale, is lost; the sums of q times K's codes, which
  * are scaled afterwards, have to lie within fp32.
- * max_len is the largest length, if known, or 0: it shapes the split only. Launch and
- * workspace are sized for sequences that fill the table, so a table cut to the longest
- * length is the faster one. The
- * positions are split over workgroups where there are few rows; the parts then
- * meet in `workspace` (device, 16-byte aligned, qwg_kv8_attend_workspace bytes
- * for the same arguments: 0 where the table holds at most 1024 positions, 512 for
- * a head_dim above 128, and may be 0 elsewhere; a negative status for a refusal),
- * which is the caller's: calls that may overlap in time need one each.
+ * max_len is the largest length, if known, or 0: it shapes the split only. Launch
+ * and workspace are sized for sequences that fill the table, so a table cut to the
+ * longest length is the faster one. The positions are split over workgroups where
+ * there are few rows; the parts then meet in `workspace` (device, 16-byte aligned,
+ * qwg_kv8_attend_workspace bytes for the same arguments: 0 where the table holds at
+ * most 1024 positions, 512 for a head_dim above 128, and may be 0 elsewhere; a
+ * negative status for a refusal), which is the caller's: calls that may overlap in
+ * time need one each.
  */
 typedef struct qwg_kv8 {
     void *k_pages;

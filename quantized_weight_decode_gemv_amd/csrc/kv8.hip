@@ -852,10 +852,13 @@ void kv8_attend_plan(Kv8AttendArgs &a, int64_t max_len, int cus) {
     chunk = (chunk + 255) / 256 * 256;
     const bool idle = a.cache.dim > 128 && groups * 4 <= cus;
     if (max_len <= (idle ? 512 : 1024)) chunk = 1024;
-    if (chunk > kMaxChunk) chunk = kMaxChunk;
+    // Sequences of one split as far as known stay whole in longer ones, and the table needs
+    // fewer of those (32 of 500 positions, 8 heads of 128, max_len 500, a table of 131,072:
+    // 268 us in splits of 1024 and, most of them empty, workgroups of eight wavefronts; 150).
+    if (chunk > kMaxChunk || (max_len <= chunk && cap > chunk)) chunk = kMaxChunk;
     a.chunk = (int)chunk;
     a.max_splits = (int)((cap + chunk - 1) / chunk);
-    a.few = max_len <= chunk && groups <= cus;
+    a.few = max_len <= chunk && groups * a.max_splits <= cus;
     a.brief = max_len <= 512 && groups > slots;
 }
 

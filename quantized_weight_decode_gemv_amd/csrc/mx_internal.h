@@ -64,7 +64,7 @@ struct Kv8AttendArgs {
     int chunk;       // positions per split (a multiple of 64)
     int max_splits;  // splits of a sequence that fills its table or window
     bool brief;      // more workgroups than fit at once, as far as known of 512 positions at most
-    bool few;        // as far as known one split each, and no more of them than compute units
+    bool few;        // as far as known one split each, and no more workgroups, empty ones too, than compute units
     float *partial;  // [n_seqs][max_splits][q_len * n_heads][dim + 2], or null for one split
 };
 

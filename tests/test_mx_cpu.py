@@ -154,3 +154,19 @@ def test_the_binding_asks_for_a_workspace_wherever_one_is_needed(L):  # noqa: F8
         # and one twice as long needs one, for one sequence at least
         c = desc(head_dim=dim, page_tokens=128, n_kv_heads=1)
         assert L.qwg_kv8_attend_workspace(c, 2 * most // 128, 1, 1, 1, 0, 0) > 0
+
+
+def test_a_known_length_of_one_split_costs_no_workspace(L):  # noqa: F811
+    """max_len shapes the split: where it makes every sequence one split, the workspace that the table's
+    width still asks for is no larger than without it."""
+    size = L.qwg_kv8_attend_workspace
+    for dim in _mx.KV8_HEAD_DIMS:
+        for page in (16, 128):
+            c = desc(head_dim=dim, page_tokens=page, n_kv_heads=8)
+            for seqs in (1, 8, 32, 200):
+                for q_len in (1, 5, 1024):
+                    for positions in (1024, 2048, 5120, 131072):
+                        for known in (1, 100, 512):
+                            for window in (0, 3000):
+                                a = (positions // page, seqs, q_len, 32, window)
+                                assert 0 <= size(c, *a, known) <= size(c, *a, 0), (dim, page, seqs, q_len, positions, known, window)
