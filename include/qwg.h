@@ -99,6 +99,7 @@ extern "C" {
 #define QWG_ERR_TIMEOUT 8  /* a wait of a layer-chain launch gave up (qwg_chain_status) */
 #define QWG_ERR_GRID 9     /* a codebook value is not exactly representable in fp16 */
 #define QWG_ERR_TYPE 10    /* unknown element type (QWG_F32, QWG_F16, QWG_BF16) */
+#define QWG_ERR_OVERLAP 11 /* a result would overwrite what the call still reads */
 
 /* format ids */
 #define QWG_FMT_Q4K 0
@@ -659,6 +660,70 @@ int qwg_kv8_attend(const qwg_kv8 *cache, void *out, const void *q, int type, int
                    const int32_t *table, int64_t table_width, const int32_t *lens, int64_t n_seqs,
                    int q_len, int n_heads, float scale, int64_t window, int64_t max_len,
                    void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * What a layer needs around that cache.
+ *
+ * qwg_kv8_append_rotary: qwg_kv8_append of keys that are rotated by their position on
+ * the way, and the rotation of the queries. Token i of sequence s is at position
+ * prefix_len[0] + lens[s] + i (prefix_len: int32 in device memory, or NULL: 0). Its pair
+ * (a, b) of channels (j, j + rotary_dim/2), or (2j, 2j + 1) where interleaved is not 0,
+ * becomes (a cos - b sin, b cos + a sin) of position * freqs[j] radians, freqs [rotary_dim/2]
+ * fp32 in device memory; channels past rotary_dim stay. rotary_dim is a multiple of 16
+ * up to head_dim. The angle is computed in 64 bits and exact to 2^-52 of itself; q and k
+ * are rotated in fp32 and rounded once to `type`, keys on the way to their page
+ * in 64 bits and rounded once to fp32. q [n_tokens][n_heads][head_dim] -> q_out,
+ * tokens q_stride and q_out_stride elements apart; q_out may be q itself with the same
+ * stride. k_out: the rotated keys as `type` too, or NULL. Neither may overlap k or v, nor k_out q
+ * (QWG_ERR_OVERLAP; slices of one fused result interleave and do not). Tokens of a sequence that the
+ * cache does not take (no page, past the table, a negative length) are rotated all the same;
+ * rows of tokens that belong to no sequence are left as they were. Everything else as
+ * qwg_kv8_append.
+ *
+ * qwg_prompt_attend: out[t, h] = sum_j softmax_j(scale q[t, h] . k[j, g]) v[j, g], g = h /
+ * (n_heads / n_kv_heads), over the positions j of t's sequence up to t itself, the last
+ * `window` of them (0: all). q [n_tokens][n_heads][head_dim], k and v [n_tokens]
+ * [n_kv_heads][head_dim] of `type`, tokens the given strides apart (heads contiguous),
+ * out [n_tokens][n_heads][head_dim] contiguous; head_dim as the cache's. Sequence s holds
+ * tokens starts[s] .. starts[s+1]-1 (int32 [n_seqs+1], device, ascending; NULL: n_tokens /
+ * n_seqs each); a sequence may be empty, and rows of tokens that belong to none are left as
+ * they were. n_tokens * n_heads <= 2^28, n_seqs * n_kv_heads <= 2^22. Products, sums and softmax are
+ * fp32; a probability is rounded to `type` before it meets v. What masked positions and
+ * neighbouring sequences hold (NaN and infinities too) has no effect; a row whose visible
+ * scores are all -infinity, or one of them +infinity or NaN, is NaN. max_len is the longest
+ * sequence, if known, or 0: it shapes the launch only. No workspace.
+ *
+ * qwg_kv8_attend_shared: qwg_kv8_attend (without a window) for sequences that begin with
+ * the same positions, which are read once for all of them. prefix [prefix_width] holds the
+ * shared pages in order and prefix_len[0] their positions (any number: the last page need
+ * not be full); table, lens and q are those of qwg_kv8_attend for each sequence's own
+ * positions behind the prefix (the queries' own among them), the first of which lies in slot
+ * 0 of its table's first page. Token t of sequence s is at position prefix_len + lens[s] -
+ * q_len + t of the whole and sees it up to there. Every row is NaN where prefix_len is
+ * negative or past the prefix's pages; otherwise as qwg_kv8_attend. n_seqs * q_len * n_heads <=
+ * 2^20. The parts meet in `workspace` (device, 16-byte aligned,
+ * qwg_kv8_attend_shared_workspace bytes for the same arguments, never 0), which is the
+ * caller's: calls that may overlap in time need one each.
+ */
+int qwg_kv8_append_rotary(const qwg_kv8 *cache, void *q_out, int64_t q_out_stride, void *k_out,
+                          int64_t k_out_stride, const void *q, int64_t q_stride, const void *k,
+                          int64_t k_stride, const void *v, int64_t v_stride, int type, int n_heads,
+                          const float *freqs, int rotary_dim, int interleaved,
+                          const int32_t *prefix_len, int64_t n_tokens, const int32_t *starts,
+                          const int32_t *table, int64_t table_width, const int32_t *lens,
+                          int64_t n_seqs, int64_t max_new, void *stream);
+int qwg_prompt_attend(void *out, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                      const void *v, int64_t v_stride, int type, int64_t n_tokens,
+                      const int32_t *starts, int64_t n_seqs, int64_t max_len, int n_heads,
+                      int n_kv_heads, int head_dim, float scale, int64_t window, void *stream);
+int64_t qwg_kv8_attend_shared_workspace(const qwg_kv8 *cache, int64_t prefix_width,
+                                        int64_t table_width, int64_t n_seqs, int q_len,
+                                        int n_heads);
+int qwg_kv8_attend_shared(const qwg_kv8 *cache, void *out, const void *q, int type, int64_t q_stride,
+                          const int32_t *prefix, int64_t prefix_width, const int32_t *prefix_len,
+                          const int32_t *table, int64_t table_width, const int32_t *lens,
+                          int64_t n_seqs, int q_len, int n_heads, float scale, void *workspace,
+                          int64_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

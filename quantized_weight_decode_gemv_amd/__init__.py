@@ -14,7 +14,8 @@ from ._binding import (Group, Iq3Group, Q4kChain, Iq3sGroup, Iq4xsGroup, MAX_BAT
                        pack_q4k_tiles, plan_splits, row_bytes, tiled_bytes, workspace_release,
                        workspace_reserve)
 from ._mx import (KV8_HEAD_DIMS, KV8_PAGE_TOKENS, MX_BLOCK, MX_MAX_BATCH, dequant_mxfp4, encode_mxfp4,
-                  gemm_mxfp4, gemv_mxfp4, kv8_append, kv8_attend, kv8_pages, matmul_mxfp4)
+                  gemm_mxfp4, gemv_mxfp4, kv8_append, kv8_append_rotary, kv8_attend, kv8_attend_shared, kv8_pages,
+                  matmul_mxfp4, prompt_attend)
 
 __all__ = ["Group", "Iq3Group", "Q4kChain", "Iq3sGroup", "Iq4xsGroup", "MAX_BATCH", "Q4kBatchedGroup", "Q4kGroup", "QWG_FMT_IQ3",
            "QWG_FMT_IQ3_S", "QWG_FMT_IQ3_XXS", "QWG_FMT_IQ4_XS", "QWG_FMT_Q4K", "QwgError",
@@ -25,4 +26,5 @@ __all__ = ["Group", "Iq3Group", "Q4kChain", "Iq3sGroup", "Iq4xsGroup", "MAX_BATC
            "pack_q4k_tiles", "plan_splits", "row_bytes", "tiled_bytes", "workspace_release",
            "workspace_reserve",
            "KV8_HEAD_DIMS", "KV8_PAGE_TOKENS", "MX_BLOCK", "MX_MAX_BATCH", "dequant_mxfp4", "encode_mxfp4",
-           "gemm_mxfp4", "gemv_mxfp4", "kv8_append", "kv8_attend", "kv8_pages", "matmul_mxfp4"]
+           "gemm_mxfp4", "gemv_mxfp4", "kv8_append", "kv8_append_rotary", "kv8_attend", "kv8_attend_shared", "kv8_pages",
+           "matmul_mxfp4", "prompt_attend"]

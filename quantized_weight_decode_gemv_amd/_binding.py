@@ -113,10 +113,19 @@ def lib() -> ctypes.CDLL:
         L.qwg_kv8_attend_workspace.argtypes = [P, I64, I64, I, I, I64, I64]
         L.qwg_kv8_attend.argtypes = [P, P, P, I, I64, P, I64, P, I64, I, I, ctypes.c_float, I64, I64,
                                      P, I64, P]
+        L.qwg_kv8_append_rotary.argtypes = [P, P, I64, P, I64, P, I64, P, I64, P, I64, I, I, P, I, I, P, I64,
+                                            P, P, I64, P, I64, I64, P]
+        L.qwg_prompt_attend.argtypes = [P, P, I64, P, I64, P, I64, I, I64, P, I64, I64, I, I, I,
+                                        ctypes.c_float, I64, P]
+        L.qwg_kv8_attend_shared_workspace.argtypes = [P, I64, I64, I64, I, I]
+        L.qwg_kv8_attend_shared.argtypes = [P, P, P, I, I64, P, I64, P, P, I64, P, I64, I, I,
+                                            ctypes.c_float, P, I64, P]
         for f in ("qwg_encode_mxfp4", "qwg_dequant_mxfp4", "qwg_gemv_mxfp4", "qwg_gemm_mxfp4",
-                  "qwg_matmul_mxfp4", "qwg_kv8_append", "qwg_kv8_attend"):
+                  "qwg_matmul_mxfp4", "qwg_kv8_append", "qwg_kv8_attend",
+                  "qwg_kv8_append_rotary", "qwg_prompt_attend", "qwg_kv8_attend_shared"):
             getattr(L, f).restype = I
         L.qwg_kv8_attend_workspace.restype = I64
+        L.qwg_kv8_attend_shared_workspace.restype = I64
         _lib = L
     return _lib
 

@@ -265,6 +265,15 @@ def kv8_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, k_scales
     starts int32 [n_seqs + 1]: sequence s appends tokens starts[s] .. starts[s+1]-1; without it
     every sequence appends as many. max_new: the most that one appends, if known. The caller
     advances lens. A page that is written must belong to one sequence."""
+    kind, cache, n_seqs, width, n, k_stride, v_stride, most = _new_tokens(
+        k, v, k_pages, k_scales, v_pages, v_scales, table, lens, starts, max_new)
+    _run("qwg_kv8_append", k.device, ctypes.byref(cache), k.data_ptr(), v.data_ptr(), kind,
+         k_stride, v_stride, n, None if starts is None else starts.data_ptr(), table.data_ptr(),
+         width, lens.data_ptr(), n_seqs, most)
+
+
+def _new_tokens(k, v, k_pages, k_scales, v_pages, v_scales, table, lens, starts, max_new):
+    """What kv8_append and kv8_append_rotary check alike."""
     _on_device(k, "k")
     _on_device(v, "v", k.device)
     kind = _type(k.dtype, "k")
@@ -287,9 +296,113 @@ def kv8_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, k_scales
         most = n if max_new is None else max_new
         if most < 1:
             raise ValueError("max_new must be at least 1")
-    _run("qwg_kv8_append", k.device, ctypes.byref(cache), k.data_ptr(), v.data_ptr(), kind,
-         k_stride, v_stride, n, None if starts is None else starts.data_ptr(), table.data_ptr(),
-         width, lens.data_ptr(), n_seqs, most)
+    return kind, cache, n_seqs, width, n, k_stride, v_stride, most
+
+
+def _out_tokens(out, like, name: str, heads: int, dim: int, n: int):
+    """`out`, checked, or a new contiguous tensor of the shape of `like`; and its token stride."""
+    if out is None:
+        return like.new_empty(like.shape), heads * dim
+    _on_device(out, name, like.device)
+    if out.dtype != like.dtype or out.shape != like.shape:
+        raise ValueError(f"{name} must be {like.dtype} {list(like.shape)}")
+    return out, _tokens(out, name, heads, dim)[1]
+
+
+def kv8_append_rotary(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, freqs: torch.Tensor,
+                      k_pages: torch.Tensor, k_scales: torch.Tensor, v_pages: torch.Tensor,
+                      v_scales: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                      starts: torch.Tensor | None = None, max_new: int | None = None,
+                      interleaved: bool = False, out: torch.Tensor | None = None,
+                      k_out: torch.Tensor | None = None,
+                      prefix_len: torch.Tensor | None = None) -> torch.Tensor:
+    """Rotate new queries and keys by their positions, and encode the keys and values into the
+    pages of an 8-bit cache, as kv8_append does. Returns the rotated queries.
+
+    q: [n_tokens, n_heads, head_dim] or [n_seqs, tokens, n_heads, head_dim], like k and v (slices of
+    a fused q|k|v result may be given). Token i of sequence s is at position lens[s] + i
+    (behind prefix_len others). freqs:
+    fp32 [rotary_dim / 2] (rotary_dim a multiple of 16, head_dim at most), radians per position;
+    the angle is exact for every position. Channels (j, j + rotary_dim / 2), or with `interleaved`
+    (2j, 2j + 1), turn by position * freqs[j]; those past rotary_dim stay. out: where the queries go
+    (q itself may be given), else a new tensor. k_out: a tensor of k's shape that gets the rotated
+    keys too (for prompt_attend); it must not overlap q, k or v. prefix_len int32 [1]: positions of a
+    prefix that the sequences share (kv8_attend_shared), before the first of their own. Rows of tokens that belong to no
+    sequence are left as they were."""
+    kind, cache, n_seqs, width, n, k_stride, v_stride, most = _new_tokens(
+        k, v, k_pages, k_scales, v_pages, v_scales, table, lens, starts, max_new)
+    dim = cache.head_dim
+    _on_device(q, "q", k.device)
+    heads = q.shape[-2] if q.dim() in (3, 4) else 0
+    if q.dtype != k.dtype:
+        raise ValueError("q must be of the type of k and v")
+    if heads < 1 or heads % cache.n_kv_heads or q.shape[:-2] != k.shape[:-2]:
+        raise ValueError(f"q must hold the tokens of k, n_heads a multiple of {cache.n_kv_heads}")
+    q_stride = _tokens(q, "q", heads, dim)[1]
+    _plain(freqs, "freqs", torch.float32, k.device)
+    rotary = 2 * freqs.numel()
+    if freqs.dim() != 1 or rotary < 16 or rotary % 16 or rotary > dim:
+        raise ValueError(f"freqs must be [rotary_dim / 2] with rotary_dim a multiple of 16, at most {dim}")
+    if prefix_len is not None:
+        _plain(prefix_len, "prefix_len", _I32, k.device)
+        if prefix_len.numel() != 1:
+            raise ValueError("prefix_len must be [1]")
+    out, out_stride = _out_tokens(out, q, "out", heads, dim, n)
+    k_out_stride = 0
+    if k_out is not None:
+        k_out, k_out_stride = _out_tokens(k_out, k, "k_out", cache.n_kv_heads, dim, n)
+    _run("qwg_kv8_append_rotary", k.device, ctypes.byref(cache), out.data_ptr(), out_stride,
+         None if k_out is None else k_out.data_ptr(), k_out_stride, q.data_ptr(), q_stride,
+         k.data_ptr(), k_stride, v.data_ptr(), v_stride, kind, heads, freqs.data_ptr(), rotary,
+         int(interleaved), None if prefix_len is None else prefix_len.data_ptr(), n, None if starts is None else starts.data_ptr(), table.data_ptr(), width,
+         lens.data_ptr(), n_seqs, most)
+    return out
+
+
+def prompt_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                  starts: torch.Tensor | None = None, max_len: int | None = None,
+                  scale: float | None = None, window: int = 0,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """Causal attention over whole prompts.
+
+    q: fp32, fp16 or bf16 [n_tokens, n_heads, head_dim], k and v [n_tokens, n_kv_heads, head_dim]
+    (slices of a fused q|k|v result may be given), or all of them [n_seqs, tokens, ...]. starts int32
+    [n_seqs + 1]: sequence s holds tokens starts[s] .. starts[s+1]-1; without it three-dimensional
+    tensors hold one sequence, four-dimensional ones n_seqs. A token sees its sequence up to itself,
+    the last `window` positions (0: all). scale defaults to head_dim ** -0.5. max_len: the longest
+    sequence, if known; it shapes the launch only. Returns a contiguous tensor of q's shape and type;
+    rows of tokens that belong to no sequence are left as they were (in a new tensor: undefined)."""
+    _on_device(q, "q")
+    _on_device(k, "k", q.device)
+    _on_device(v, "v", q.device)
+    kind = _type(q.dtype, "q")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v must be of one type")
+    if q.dim() not in (3, 4) or k.dim() != q.dim() or v.shape != k.shape or q.shape[:-2] != k.shape[:-2]:
+        raise ValueError("q must be [n_tokens, n_heads, head_dim] and k and v [n_tokens, n_kv_heads, head_dim], "
+                         "or [n_seqs, tokens, ...] alike")
+    heads, dim = q.shape[-2:]
+    kv = k.shape[-2]
+    if dim not in KV8_HEAD_DIMS or kv < 1 or heads < 1 or heads % kv:
+        raise ValueError(f"head_dim must be one of {KV8_HEAD_DIMS} and n_heads a multiple of n_kv_heads")
+    n, q_stride = _tokens(q, "q", heads, dim)
+    k_stride, v_stride = _tokens(k, "k", kv, dim)[1], _tokens(v, "v", kv, dim)[1]
+    if n < 1:
+        raise ValueError("a call needs at least one token")
+    if starts is None:
+        n_seqs = 1 if q.dim() == 3 else q.shape[0]
+    else:
+        _plain(starts, "starts", _I32, q.device)
+        if starts.dim() != 1 or starts.shape[0] < 2:
+            raise ValueError("starts must be [n_seqs + 1]")
+        n_seqs = starts.shape[0] - 1
+    if window < 0 or (max_len is not None and max_len < 0):
+        raise ValueError("window and max_len must not be negative")
+    out = _out(out, q.shape, q)
+    _run("qwg_prompt_attend", q.device, out.data_ptr(), q.data_ptr(), q_stride, k.data_ptr(),
+         k_stride, v.data_ptr(), v_stride, kind, n, None if starts is None else starts.data_ptr(),
+         n_seqs, max_len or 0, heads, kv, dim, dim ** -0.5 if scale is None else scale, window)
+    return out
 
 
 def kv8_attend(q: torch.Tensor, k_pages: torch.Tensor, k_scales: torch.Tensor,
@@ -332,4 +445,48 @@ def kv8_attend(q: torch.Tensor, k_pages: torch.Tensor, k_scales: torch.Tensor,
          table.data_ptr(), width, lens.data_ptr(), n_seqs, q_len, heads,
          dim ** -0.5 if scale is None else scale, window, most,
          space.data_ptr() if size else None, size)
+    return out
+
+
+def kv8_attend_shared(q: torch.Tensor, k_pages: torch.Tensor, k_scales: torch.Tensor,
+                      v_pages: torch.Tensor, v_scales: torch.Tensor, prefix: torch.Tensor,
+                      prefix_len: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                      scale: float | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of the last tokens of sequences that share a prefix, over an 8-bit cache
+    (kv8_pages): kv8_attend over the prefix's positions and each sequence's own behind them, but the
+    prefix is read once for all sequences.
+
+    q: as kv8_attend's. prefix int32 [pages]: the shared pages in order; prefix_len int32 [1]: the
+    positions that they hold (any number: the last page need not be full). table int32 [n_seqs, pages]
+    and lens int32 [n_seqs]: each sequence's own pages and positions, the first right behind the
+    prefix, the queries' own among them (kv8_append and kv8_append_rotary fill them; the latter's
+    takes prefix_len too). scale defaults to head_dim ** -0.5. Returns a
+    contiguous tensor of q's shape and type."""
+    _on_device(q, "q")
+    kind = _type(q.dtype, "q")
+    cache = _cache(k_pages, k_scales, v_pages, v_scales, q.device)
+    n_seqs, width = _sequences(table, lens, q.device)
+    _plain(prefix, "prefix", _I32, q.device)
+    _plain(prefix_len, "prefix_len", _I32, q.device)
+    if prefix.dim() != 1 or prefix.numel() < 1 or prefix_len.numel() != 1:
+        raise ValueError("prefix must be [pages] and prefix_len [1]")
+    heads, dim = q.shape[-2:] if q.dim() in (3, 4) else (0, 0)
+    if dim != cache.head_dim or heads < 1 or heads % cache.n_kv_heads or q.shape[0] != n_seqs:
+        raise ValueError(f"q must be [{n_seqs}, (q_len,) n_heads, {cache.head_dim}] with n_heads a "
+                         f"multiple of {cache.n_kv_heads}")
+    n, stride = _tokens(q, "q", heads, dim)
+    q_len = n // n_seqs
+    if q_len < 1 or q_len * heads > 65535:
+        raise ValueError("q_len * n_heads must be in 1..65535")
+    out = _out(out, q.shape, q)
+    ref = ctypes.byref(cache)
+    size = lib().qwg_kv8_attend_shared_workspace(ref, prefix.numel(), width, n_seqs, q_len, heads)
+    if size < 0:
+        _check(-size, "qwg_kv8_attend_shared_workspace")
+    # of this call's stream (or of the graph that captures it): no two calls share one
+    space = table.new_empty(size // 4)
+    _run("qwg_kv8_attend_shared", q.device, ref, out.data_ptr(), q.data_ptr(), kind, stride,
+         prefix.data_ptr(), prefix.numel(), prefix_len.data_ptr(), table.data_ptr(), width,
+         lens.data_ptr(), n_seqs, q_len, heads, dim ** -0.5 if scale is None else scale,
+         space.data_ptr(), size)
     return out

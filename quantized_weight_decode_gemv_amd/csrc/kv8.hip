@@ -45,6 +45,106 @@ __device__ __forceinline__ uint32_t fp8_shifted(uint32_t w, float shift) {
                      __builtin_amdgcn_cvt_f32_fp8((int)w, 3) * shift, 1.0f);
 }
 
+// sin and cos of 2 pi t, t in turns. A position times a frequency is exact enough in 64
+// bits alone (position 10^5 at one radian each: fp32 leaves 2^-8 of a radian), and there the
+// rest is cheap too: the quarter turn comes off exactly, and the Taylor sums of what is
+// left, at most pi/4, end where the next term is below 2^-45.
+__device__ __forceinline__ void sincos_turns(double t, double &s, double &c) {
+    const double quarter = __builtin_rint(t * 4.0);
+    const double x = __builtin_fma(quarter, -0.25, t) * 6.283185307179586, x2 = x * x;
+    double a = 1.0 / 6227020800.0, b = -1.0 / 87178291200.0;
+    a = __builtin_fma(a, x2, -1.0 / 39916800.0);
+    b = __builtin_fma(b, x2, 1.0 / 479001600.0);
+    a = __builtin_fma(a, x2, 1.0 / 362880.0);
+    b = __builtin_fma(b, x2, -1.0 / 3628800.0);
+    a = __builtin_fma(a, x2, -1.0 / 5040.0);
+    b = __builtin_fma(b, x2, 1.0 / 40320.0);
+    a = __builtin_fma(a, x2, 1.0 / 120.0);
+    b = __builtin_fma(b, x2, -1.0 / 720.0);
+    a = __builtin_fma(a, x2, -1.0 / 6.0);
+    b = __builtin_fma(b, x2, 1.0 / 24.0);
+    b = __builtin_fma(b, x2, -0.5);
+    a = __builtin_fma(a * x2, x, x);  // sin x
+    b = __builtin_fma(b, x2, 1.0);    // cos x
+    const double round = quarter * 0.25;
+    const int k = (int)((round - __builtin_floor(round)) * 4.0);  // quarter mod 4
+    const double u = k & 1 ? b : a, w = k & 1 ? a : b;
+    s = k & 2 ? -u : u;
+    c = (k + 1) & 2 ? -w : w;
+}
+
+constexpr double kTurnsPerRadian = 0.15915494309189535;
+// how the channels of a head pair up: not at all, the first half with the second, neighbours
+constexpr int kPlain = 0, kHalves = 1, kNeighbours = 2;
+constexpr int kSliceHeads = 8;  // heads that a workgroup rotates for q_out or k_out
+constexpr int kHeadsAtOnce = 4;  // of them under the same angles
+
+// The tokens of a sequence, rotated, to q_out or k_out: eight heads at most of one chunk of
+// `page` tokens after another. A thread takes eight channels (and the eight that they pair with)
+// of four heads of one token: the angles are the same for all of them, and cost what two
+// heads' loads do.
+template <typename T, int ROT, int threads>
+__device__ __forceinline__ void rotate_rows(const T *x, int64_t x_stride, T *to, int64_t to_stride, int heads,
+                                            const Kv8RotaryArgs &a, int64_t first, int64_t count, int64_t held) {
+    const int dim = a.cache.dim, page = a.cache.page, half = a.rotary / 2;
+    const bool vec = (((uintptr_t)x | (uintptr_t)to | (uintptr_t)x_stride * sizeof(T) |
+                       (uintptr_t)to_stride * sizeof(T)) & 15) == 0;
+    const int units = (ROT == kHalves ? dim - half : dim) / 8;
+    const int sets = (heads + kHeadsAtOnce - 1) / kHeadsAtOnce;
+    auto load = [&](const T *p, float (&v)[8]) { vec ? load8<T, true>(p, v) : load8<T, false>(p, v); };
+    auto store = [&](T *p, const float (&v)[8]) { vec ? store8<T, true>(p, v) : store8<T, false>(p, v); };
+    for (int64_t i0 = (int64_t)blockIdx.x * page; i0 < count; i0 += (int64_t)gridDim.x * page) {
+        const int items = (int)min((int64_t)page, count - i0) * sets * units;
+        for (int i = threadIdx.x; i < items; i += threads) {
+            const int u = i % units, r = i / units, h0 = r % sets * kHeadsAtOnce;
+            const int64_t token = i0 + r / sets;
+            const int d = ROT == kHalves && u >= half / 8 ? u * 8 + half : u * 8;
+            const T *p = x + (first + token) * x_stride + (int64_t)h0 * dim + d;
+            T *o = to + (first + token) * to_stride + (int64_t)h0 * dim + d;
+            const int n = min(kHeadsAtOnce, heads - h0);
+            float v[kHeadsAtOnce][8], w[kHeadsAtOnce][8];
+#pragma unroll
+            for (int h = 0; h < kHeadsAtOnce; ++h)
+                if (h < n) {
+                    load(p + h * dim, v[h]);
+                    if (ROT == kHalves && d < half) load(p + h * dim + half, w[h]);
+                }
+            if (d < (ROT == kHalves ? half : a.rotary)) {
+                const double pos = (double)(held + token);
+#pragma unroll
+                for (int e = 0; e < (ROT == kHalves ? 8 : 4); ++e) {
+                    double s, c;
+                    sincos_turns(pos * (a.freqs[ROT == kHalves ? d + e : d / 2 + e] * kTurnsPerRadian), s, c);
+                    const float sf = (float)s, cf = (float)c;
+#pragma unroll
+                    for (int h = 0; h < kHeadsAtOnce; ++h) {
+                        float &p0 = ROT == kHalves ? v[h][e] : v[h][e * 2 & 7];
+                        float &p1 = ROT == kHalves ? w[h][e] : v[h][(e * 2 + 1) & 7];
+                        const float x0 = p0, x1 = p1;
+                        p0 = __builtin_fmaf(x0, cf, -(x1 * sf));
+                        p1 = __builtin_fmaf(x1, cf, x0 * sf);
+                    }
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < kHeadsAtOnce; ++h)
+                if (h < n) {
+                    store(o + h * dim, v[h]);
+                    if (ROT == kHalves && d < half) store(o + h * dim + half, w[h]);
+                }
+        }
+    }
+}
+
+template <int ROT>
+struct AppendArgs {
+    typedef Kv8RotaryArgs type;
+};
+template <>
+struct AppendArgs<kPlain> {
+    typedef Kv8AppendArgs type;
+};
+
 // One workgroup per (page of a sequence, sequence, head of K or V). A thread
 // takes four consecutive positions of eight channels: 8-byte stores to a K page,
 // 4-byte stores (one per channel) to a transposed V page. The page's largest new
@@ -55,8 +155,12 @@ __device__ __forceinline__ uint32_t fp8_shifted(uint32_t w, float shift) {
 // each of 33 sequences takes 5.4 us: the launch and four round trips in a row (length,
 // page number, values, exponent).
 // VEC: the values of a token start on 16 bytes.
-template <int TYPE, bool VEC, int threads>
-__global__ __launch_bounds__(threads) void kv8_append_kernel(Kv8AppendArgs a) {
+// ROT: keys are rotated on the way, in 64 bits and rounded once (a code then differs from
+// the exact key's by what 2^-24 of the key decides), and workgroups past the heads' rotate
+// q and, where asked for, k into q_out and k_out. The partner channels of a thread's eight are
+// read too (they come from the cache) rather than exchanged.
+template <int TYPE, bool VEC, int threads, int ROT>
+__global__ __launch_bounds__(threads) void kv8_append_kernel(typename AppendArgs<ROT>::type a) {
     typedef typename Elem<TYPE>::T T;
     __shared__ uint32_t tops[threads / 64];
     const Kv8 &c = a.cache;
@@ -71,6 +175,21 @@ __global__ __launch_bounds__(threads) void kv8_append_kernel(Kv8AppendArgs a) {
     } else {
         count = a.n_tokens / a.n_seqs;
         first = seq * count;
+    }
+    int64_t before = 0;
+    if constexpr (ROT != kPlain) {
+        if (a.before) before = a.before[0];
+        int slice = (int)blockIdx.z - 2 * c.n_kv;
+        if (slice >= 0) {
+            const int of_q = (a.n_heads + kSliceHeads - 1) / kSliceHeads;
+            const bool q = slice < of_q;
+            const int h0 = (q ? slice : slice - of_q) * kSliceHeads, heads = (q ? a.n_heads : c.n_kv) - h0;
+            rotate_rows<T, ROT, threads>((const T *)(q ? a.q : a.k) + (int64_t)h0 * c.dim, q ? a.q_stride : a.k_stride,
+                                         (T *)(q ? a.q_out : a.k_out) + (int64_t)h0 * c.dim,
+                                         q ? a.q_out_stride : a.k_out_stride, min(heads, kSliceHeads), a, first,
+                                         count, held + before);
+            return;
+        }
     }
     if (held < 0 || count <= 0) return;
     const T *x = (const T *)(is_v ? a.v : a.k) + (int64_t)head * c.dim;
@@ -99,6 +218,38 @@ __global__ __launch_bounds__(threads) void kv8_append_kernel(Kv8AppendArgs a) {
                 for (int e = 0; e < 8; ++e) v[t][e] = 0;
                 if (slot + t >= old && slot + t < stop)
                     load8<T, VEC>(x0 + (slot + t) * stride + d, v[t]);
+            }
+            if constexpr (ROT != kPlain) {
+                if (is_v || d >= a.rotary) return;
+                const int half = a.rotary / 2;
+                const bool upper = d >= half;
+                float w[4][8];
+                if constexpr (ROT == kHalves) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w[t][e] = 0;
+                        if (slot + t >= old && slot + t < stop)
+                            load8<T, VEC>(x0 + (slot + t) * stride + (upper ? d - half : d + half), w[t]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < (ROT == kHalves ? 8 : 4); ++e) {
+                    const double f = a.freqs[ROT == kHalves ? (upper ? d - half : d) + e : d / 2 + e] * kTurnsPerRadian;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        double sn, cs;
+                        sincos_turns((double)(before + pos0 + slot + t) * f, sn, cs);
+                        if constexpr (ROT == kHalves) {
+                            const double x = v[t][e], y = w[t][e];
+                            v[t][e] = (float)__builtin_fma(x, cs, upper ? y * sn : -(y * sn));
+                        } else {
+                            const double x = v[t][e * 2 & 7], y = v[t][(e * 2 + 1) & 7];
+                            v[t][e * 2 & 7] = (float)__builtin_fma(x, cs, -(y * sn));
+                            v[t][(e * 2 + 1) & 7] = (float)__builtin_fma(y, cs, x * sn);
+                        }
+                    }
+                }
             }
         };
         uint32_t top = 0;
@@ -367,6 +518,7 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
     float top[R], sum[R];
     f32x4 out[R][DT];
     int last[R];  // the last position that this lane's row sees
+    int by_all = len - a.q_len + 1;  // every row sees the positions before it
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         top[r] = -__builtin_inff();
@@ -375,6 +527,19 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
         for (int t = 0; t < DT; ++t) out[r][t] = f32x4{0, 0, 0, 0};
         const int row = row0 + r * 16 + n;
         last[r] = row < rows ? len - a.q_len + row / group : -1;
+        if (a.tails && row < rows) {
+            // a shared prefix: all of it, but for a query whose own position lies in it
+            const int token = row / group, s = token / a.tail_q_len;
+            const int own = a.tails[s] - a.tail_q_len + token % a.tail_q_len;
+            last[r] = len - 1 + min(own + 1, 0);
+        }
+    }
+    if (a.tails) {
+        by_all = len;
+#pragma unroll
+        for (int r = 0; r < R; ++r) by_all = min(by_all, row0 + r * 16 + n < rows ? last[r] + 1 : len);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) by_all = min(by_all, __shfl_xor(by_all, o));
     }
     const int64_t head_bytes = (int64_t)c.page * D;
     auto page_at = [&](int pos) { return pages[(pos >> shift) - first_page]; };
@@ -484,7 +649,7 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
         const float vs = e8m0(page.y >> 8 & 255);
         if (lost) ks = __builtin_nanf("");
         // every row sees the whole block, or the rows' masks decide
-        const bool whole = b0 + kBlk <= len - a.q_len + 1 && (window <= 0 || b0 >= len - window);
+        const bool whole = b0 + kBlk <= by_all && (window <= 0 || b0 >= len - window);
         uint32_t seen[R];  // of this lane's sixteen positions, which lie in one page
 #pragma unroll
         for (int r = 0; r < R; ++r) seen[r] = 0xffffu;
@@ -665,7 +830,7 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
             o += f * *(const f32x4 *)(so + (w * R * 16 + lr) * RP + d);
         }
         const int t = row / group, h = head * group + row % group;
-        if (splits == 1) {
+        if (splits == 1 && !a.parts) {
             T *dst = (T *)a.out + ((row_base + t) * a.n_heads + h) * D + d;
             const float inv = bad ? __builtin_nanf("") : 1.0f / total;
 #pragma unroll
@@ -734,6 +899,69 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8AttendArgs a) {
     }
 }
 
+// Joins what the two passes of attention behind a shared prefix left: the splits of the
+// prefix and those of the sequence's own positions.
+template <int TYPE, int D>
+__global__ __launch_bounds__(256) void kv8_join_shared_kernel(Kv8SharedArgs a) {
+    typedef typename Elem<TYPE>::T T;
+    constexpr int V = D / 4;   // lanes that hold one row, four channels each
+    constexpr int S = 64 / V;  // splits that a wavefront reads at once
+    __shared__ float sums[4 * S][D + 1];
+    __shared__ float red[2][4];
+    const int64_t seq = blockIdx.y;
+    const int row = blockIdx.x;  // token * n_heads + head
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t rows = (int64_t)a.own.q_len * a.own.n_heads;
+    const int plen = a.prefix.lens[0], olen = a.own.lens[seq];
+    const bool bad = plen < 0 || plen > a.prefix.width * a.prefix.cache.page || olen < 0 ||
+                     olen > a.own.width * a.own.cache.page;
+    const int psplits = bad ? 0 : (plen + a.prefix.chunk - 1) / a.prefix.chunk;
+    const int osplits = bad ? 0 : (olen + a.own.chunk - 1) / a.own.chunk;
+    const int splits = psplits + osplits;
+    const int64_t p_each = partial_floats(a.own.n_seqs * rows, D), o_each = partial_floats(rows, D);
+    auto sums_of = [&](int s) {
+        return s < psplits ? a.prefix.partial + s * p_each + (seq * rows + row) * D
+                           : a.own.partial + (seq * a.own.max_splits + s - psplits) * o_each + row * D;
+    };
+    auto ml_of = [&](int s) {
+        return s < psplits ? a.prefix.partial + s * p_each + a.own.n_seqs * rows * D + (seq * rows + row) * 2
+                           : a.own.partial + (seq * a.own.max_splits + s - psplits) * o_each + rows * D + row * 2;
+    };
+    float m = -__builtin_inff();
+    for (int s = threadIdx.x; s < splits; s += 256) m = fmaxf(m, *ml_of(s));
+#pragma unroll
+    for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if (lane == 0) red[0][wave] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    const float base = m == -__builtin_inff() ? 0.0f : m;
+    float total = 0;
+    for (int s = threadIdx.x; s < splits; s += 256) {
+        const float *ml = ml_of(s);
+        total += __builtin_amdgcn_exp2f(ml[0] - base) * ml[1];
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) total += __shfl_xor(total, o);
+    if (lane == 0) red[1][wave] = total;
+    f32x4 o = {0, 0, 0, 0};
+    const int sub = lane / V, d = lane % V * 4;
+    if (sub < S) {
+        for (int s = wave * S + sub; s < splits; s += 4 * S)
+            o += __builtin_amdgcn_exp2f(ml_of(s)[0] - base) * *(const f32x4 *)(sums_of(s) + d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sums[wave * S + sub][d + e] = o[e];
+    }
+    __syncthreads();
+    total = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    for (int d = threadIdx.x; d < D; d += 256) {
+        float o = 0;
+#pragma unroll
+        for (int s = 0; s < 4 * S; ++s) o += sums[s][d];
+        ((T *)a.own.out)[(seq * rows + row) * D + d] =
+            (T)(bad ? __builtin_nanf("") : total == 0 ? 0.0f : o / total);
+    }
+}
+
 template <int TYPE, int D, int R, int W = waves_of(D, R, TYPE)>
 hipError_t attend(const Kv8AttendArgs &a, hipStream_t s) {
     if constexpr (W == waves_of(D, R, TYPE)) {
@@ -760,7 +988,7 @@ hipError_t attend(const Kv8AttendArgs &a, hipStream_t s) {
             kv8_attend_kernel<TYPE, D, R, W, false><<<grid, W * 64, lds, s>>>(a);
     }
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.max_splits == 1) return e;
+    if (e != hipSuccess || a.max_splits == 1 || a.parts) return e;
     kv8_join_kernel<TYPE, D><<<dim3(a.q_len * a.n_heads, (unsigned)a.n_seqs), 256, 0, s>>>(a);
     return hipGetLastError();
 }
@@ -777,14 +1005,19 @@ hipError_t attend_dim(const Kv8AttendArgs &a, hipStream_t s) {
     }
 }
 
-template <int TYPE>
-hipError_t append(const Kv8AppendArgs &a, hipStream_t s) {
+template <int TYPE, int ROT, typename Args>
+hipError_t append(const Args &a, hipStream_t s) {
     // pages that max_new tokens touch at most; a sequence with more of them takes more trips
     int64_t pages = a.max_new / a.cache.page + 2;
     if (a.max_new <= 1) pages = 1;
     if (pages > a.width) pages = a.width;
     if (pages > 4096) pages = 4096;
-    const dim3 grid((unsigned)pages, (unsigned)a.n_seqs, (unsigned)(a.cache.n_kv * 2));
+    int heads = a.cache.n_kv * 2;
+    if constexpr (ROT != kPlain) {
+        heads += (a.n_heads + kSliceHeads - 1) / kSliceHeads;
+        if (a.k_out) heads += (a.cache.n_kv + kSliceHeads - 1) / kSliceHeads;
+    }
+    const dim3 grid((unsigned)pages, (unsigned)a.n_seqs, (unsigned)heads);
     const uintptr_t size = sizeof(typename Elem<TYPE>::T);
     // (head_dim values are whole 16 bytes in every type)
     const bool vec = ((uintptr_t)a.k | (uintptr_t)a.v) % 16 == 0 &&
@@ -795,8 +1028,8 @@ hipError_t append(const Kv8AppendArgs &a, hipStream_t s) {
     // with 512)
     const int tiles = a.cache.page * a.cache.dim / 32;
     auto run = [&](auto threads) {
-        if (vec) kv8_append_kernel<TYPE, true, threads.value><<<grid, threads.value, 0, s>>>(a);
-        else kv8_append_kernel<TYPE, false, threads.value><<<grid, threads.value, 0, s>>>(a);
+        if (vec) kv8_append_kernel<TYPE, true, threads.value, ROT><<<grid, threads.value, 0, s>>>(a);
+        else kv8_append_kernel<TYPE, false, threads.value, ROT><<<grid, threads.value, 0, s>>>(a);
     };
     if (tiles <= 64) run(std::integral_constant<int, 64>{});
     else if (tiles <= 256) run(std::integral_constant<int, 256>{});
@@ -811,9 +1044,20 @@ bool kv8_dim_supported(int dim) {
 }
 
 hipError_t launch_kv8_append(const Kv8AppendArgs &a, int type, hipStream_t s) {
-    if (type == kF32) return append<kF32>(a, s);
-    if (type == kF16) return append<kF16>(a, s);
-    return append<kBF16>(a, s);
+    if (type == kF32) return append<kF32, kPlain>(a, s);
+    if (type == kF16) return append<kF16, kPlain>(a, s);
+    return append<kBF16, kPlain>(a, s);
+}
+
+hipError_t launch_kv8_append_rotary(const Kv8RotaryArgs &a, int type, hipStream_t s) {
+    if (a.neighbours) {
+        if (type == kF32) return append<kF32, kNeighbours>(a, s);
+        if (type == kF16) return append<kF16, kNeighbours>(a, s);
+        return append<kBF16, kNeighbours>(a, s);
+    }
+    if (type == kF32) return append<kF32, kHalves>(a, s);
+    if (type == kF16) return append<kF16, kHalves>(a, s);
+    return append<kBF16, kHalves>(a, s);
 }
 
 // Splits. A workgroup's start and end cost as much as three or four of its turns,
@@ -862,9 +1106,43 @@ void kv8_attend_plan(Kv8AttendArgs &a, int64_t max_len, int cus) {
     a.brief = max_len <= 512 && groups > slots;
 }
 
+void kv8_shared_plan(Kv8SharedArgs &a, int cus) {
+    kv8_attend_plan(a.prefix, 0, cus);
+    kv8_attend_plan(a.own, 0, cus);
+}
+
+static int64_t shared_bytes(const Kv8AttendArgs &a) {
+    return a.n_seqs * a.max_splits * partial_floats((int64_t)a.q_len * a.n_heads, a.cache.dim) * 4;
+}
+
+int64_t kv8_shared_partial_bytes(const Kv8SharedArgs &a) {
+    return shared_bytes(a.prefix) + shared_bytes(a.own);
+}
+
 int64_t kv8_attend_partial_bytes(const Kv8AttendArgs &a) {
     if (a.max_splits <= 1) return 0;
     return a.n_seqs * a.max_splits * partial_floats((int64_t)a.q_len * a.n_heads, a.cache.dim) * 4;
+}
+
+hipError_t launch_kv8_attend_shared(Kv8SharedArgs &a, int type, hipStream_t s) {
+    a.own.partial = a.prefix.partial + shared_bytes(a.prefix) / 4;
+    hipError_t e = launch_kv8_attend(a.prefix, type, s);
+    if (e == hipSuccess) e = launch_kv8_attend(a.own, type, s);
+    if (e != hipSuccess) return e;
+    const dim3 grid(a.own.q_len * a.own.n_heads, (unsigned)a.own.n_seqs);
+    auto join = [&](auto t) {
+        switch (a.own.cache.dim) {
+            case 64: kv8_join_shared_kernel<t.value, 64><<<grid, 256, 0, s>>>(a); break;
+            case 96: kv8_join_shared_kernel<t.value, 96><<<grid, 256, 0, s>>>(a); break;
+            case 128: kv8_join_shared_kernel<t.value, 128><<<grid, 256, 0, s>>>(a); break;
+            case 192: kv8_join_shared_kernel<t.value, 192><<<grid, 256, 0, s>>>(a); break;
+            default: kv8_join_shared_kernel<t.value, 256><<<grid, 256, 0, s>>>(a);
+        }
+    };
+    if (type == kF32) join(std::integral_constant<int, kF32>{});
+    else if (type == kF16) join(std::integral_constant<int, kF16>{});
+    else join(std::integral_constant<int, kBF16>{});
+    return hipGetLastError();
 }
 
 hipError_t launch_kv8_attend(const Kv8AttendArgs &a, int type, hipStream_t s) {

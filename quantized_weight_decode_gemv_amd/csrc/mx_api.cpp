@@ -31,6 +31,10 @@ bool mx_count(int64_t n) { return n >= 1 && n <= QWG_MAX_N_OUT; }
 // stays below the 2^32 threads of a launch. In 16 bits they are 512 GB, more than the memory.
 constexpr int64_t kMaxOutputs = (int64_t)1 << 38;
 
+// (token, head) rows of qwg_prompt_attend, and its (sequence, key/value head) pairs: a grid of
+// tiles of 32 rows then stays below the 2^32 threads of a launch.
+constexpr int64_t kMaxPromptRows = (int64_t)1 << 28, kMaxPromptPairs = (int64_t)1 << 22;
+
 // Compute units of a current MI355X; the plan of a split needs no exact figure.
 constexpr int kCus = 256;
 
@@ -61,6 +65,50 @@ int attend_shape(const qwg_kv8 *c, int64_t width, int64_t n_seqs, int q_len, int
         (int64_t)q_len * n_heads > 65535 || max_len < 0)
         return QWG_ERR_SHAPE;
     return QWG_OK;
+}
+
+// `rows` rows of `width` elements, `stride` apart, from `p`: where they lie.
+struct Rows {
+    const void *p;
+    int64_t rows, width, stride;
+    uintptr_t size;
+};
+
+// Whether two such blocks may share memory: rows at one distance interleave as the slices of
+// a fused result do, others are told apart by their ends.
+bool may_share(const Rows &a, const Rows &b) {
+    const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
+    const uintptr_t a1 = a0 + ((uintptr_t)(a.rows - 1) * a.stride + a.width) * a.size;
+    const uintptr_t b1 = b0 + ((uintptr_t)(b.rows - 1) * b.stride + b.width) * b.size;
+    if (a1 <= b0 || b1 <= a0) return false;
+    if (a.rows == 1 || b.rows == 1 || a.stride != b.stride) return true;
+    const uintptr_t pitch = (uintptr_t)a.stride * a.size;
+    const uintptr_t ahead = b0 >= a0 ? (b0 - a0) % pitch : (pitch - (a0 - b0) % pitch) % pitch;
+    return ahead < a.width * a.size || pitch - ahead < b.width * b.size;
+}
+
+// Rows of qwg_kv8_attend_shared: the prefix's tiles of 16 then fit the y of a grid.
+constexpr int64_t kMaxSharedRows = 1 << 20;
+
+int shared_shape(const qwg_kv8 *c, int64_t prefix_width, int64_t width, int64_t n_seqs, int q_len,
+                 int n_heads) {
+    const int rc = attend_shape(c, width, n_seqs, q_len, n_heads, 0);
+    if (rc) return rc;
+    if (!cache_seqs(c, prefix_width, 1) || n_seqs * q_len * n_heads > kMaxSharedRows)
+        return QWG_ERR_SHAPE;
+    return QWG_OK;
+}
+
+Kv8SharedArgs shared_of(const qwg_kv8 *cache, int64_t prefix_width, int64_t width, int64_t n_seqs,
+                        int q_len, int n_heads) {
+    Kv8SharedArgs a = {};
+    a.own.cache = cache_of(cache), a.own.width = width, a.own.n_seqs = n_seqs;
+    a.own.q_len = q_len, a.own.n_heads = n_heads, a.own.parts = true;
+    a.prefix = a.own;
+    a.prefix.width = prefix_width, a.prefix.n_seqs = 1, a.prefix.q_len = (int)n_seqs * q_len;
+    a.prefix.tail_q_len = q_len;
+    kv8_shared_plan(a, kCus);
+    return a;
 }
 
 }  // namespace
@@ -140,6 +188,50 @@ int qwg_kv8_append(const qwg_kv8 *cache, const void *k, const void *v, int type,
     return hip_status(launch_kv8_append(a, type, (hipStream_t)stream));
 }
 
+int qwg_kv8_append_rotary(const qwg_kv8 *cache, void *q_out, int64_t q_out_stride, void *k_out,
+                          int64_t k_out_stride, const void *q, int64_t q_stride, const void *k,
+                          int64_t k_stride, const void *v, int64_t v_stride, int type, int n_heads,
+                          const float *freqs, int rotary_dim, int interleaved,
+                          const int32_t *prefix_len, int64_t n_tokens,
+                          const int32_t *starts, const int32_t *table, int64_t table_width,
+                          const int32_t *lens, int64_t n_seqs, int64_t max_new, void *stream) {
+    if (!cache || !q_out || !q || !k || !v || !freqs || !table || !lens) return QWG_ERR_NULL;
+    if (!known_type(type)) return QWG_ERR_TYPE;
+    const int rc = check_cache(cache);
+    if (rc) return rc;
+    if (n_heads < 1 || n_heads > 65535 || n_heads % cache->n_kv_heads || rotary_dim < 16 ||
+        rotary_dim % 16 || rotary_dim > cache->head_dim)
+        return QWG_ERR_SHAPE;
+    const int64_t width = (int64_t)cache->n_kv_heads * cache->head_dim;
+    const int64_t q_width = (int64_t)n_heads * cache->head_dim;
+    if (!cache_seqs(cache, table_width, n_seqs) || n_tokens < 1 || n_tokens > INT32_MAX ||
+        max_new < 1 || (!starts && n_tokens % n_seqs) ||
+        (n_tokens > 1 && (k_stride < width || v_stride < width || q_stride < q_width ||
+                          q_out_stride < q_width || (k_out && k_out_stride < width))))
+        return QWG_ERR_SHAPE;
+    const uintptr_t size = size_of(type);
+    if (!aligned(k, size) || !aligned(v, size) || !aligned(q, size) || !aligned(q_out, size) ||
+        !aligned(k_out, size) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(starts, 4) ||
+        !aligned(freqs, 4) || !aligned(prefix_len, 4))
+        return QWG_ERR_ALIGN;
+    // workgroups read and write in no order: q alone may be turned in place
+    const Rows rk = {k, n_tokens, width, k_stride, size}, rv = {v, n_tokens, width, v_stride, size};
+    const Rows rq = {q, n_tokens, q_width, q_stride, size};
+    const Rows oq = {q_out, n_tokens, q_width, q_out_stride, size};
+    const Rows ok = {k_out, n_tokens, width, k_out_stride, size};
+    const bool in_place = q_out == q && (n_tokens == 1 || q_out_stride == q_stride);
+    if (may_share(oq, rk) || may_share(oq, rv) || (!in_place && may_share(oq, rq)) ||
+        (k_out && (may_share(ok, rk) || may_share(ok, rv) || may_share(ok, rq) || may_share(ok, oq))))
+        return QWG_ERR_OVERLAP;
+    Kv8RotaryArgs a = {};
+    static_cast<Kv8AppendArgs &>(a) = {cache_of(cache), k, v, k_stride, v_stride, n_tokens, starts,
+                                       table, lens, table_width, n_seqs, max_new};
+    a.q = q, a.q_out = q_out, a.k_out = k_out;
+    a.q_stride = q_stride, a.q_out_stride = q_out_stride, a.k_out_stride = k_out_stride;
+    a.freqs = freqs, a.before = prefix_len, a.n_heads = n_heads, a.rotary = rotary_dim, a.neighbours = interleaved != 0;
+    return hip_status(launch_kv8_append_rotary(a, type, (hipStream_t)stream));
+}
+
 int64_t qwg_kv8_attend_workspace(const qwg_kv8 *cache, int64_t table_width, int64_t n_seqs,
                                  int q_len, int n_heads, int64_t window, int64_t max_len) {
     int rc = check_cache(cache);
@@ -179,6 +271,67 @@ int qwg_kv8_attend(const qwg_kv8 *cache, void *out, const void *q, int type, int
     if (need > workspace_bytes) return QWG_ERR_SHAPE;
     a.partial = (float *)workspace;
     return hip_status(launch_kv8_attend(a, type, (hipStream_t)stream));
+}
+
+int64_t qwg_kv8_attend_shared_workspace(const qwg_kv8 *cache, int64_t prefix_width,
+                                        int64_t table_width, int64_t n_seqs, int q_len,
+                                        int n_heads) {
+    int rc = check_cache(cache);
+    if (!rc) rc = shared_shape(cache, prefix_width, table_width, n_seqs, q_len, n_heads);
+    if (rc) return -rc;
+    return kv8_shared_partial_bytes(shared_of(cache, prefix_width, table_width, n_seqs, q_len, n_heads));
+}
+
+int qwg_kv8_attend_shared(const qwg_kv8 *cache, void *out, const void *q, int type, int64_t q_stride,
+                          const int32_t *prefix, int64_t prefix_width, const int32_t *prefix_len,
+                          const int32_t *table, int64_t table_width, const int32_t *lens,
+                          int64_t n_seqs, int q_len, int n_heads, float scale, void *workspace,
+                          int64_t workspace_bytes, void *stream) {
+    if (!cache || !out || !q || !prefix || !prefix_len || !table || !lens || !workspace)
+        return QWG_ERR_NULL;
+    if (!known_type(type)) return QWG_ERR_TYPE;
+    int rc = check_cache(cache);
+    if (!rc) rc = shared_shape(cache, prefix_width, table_width, n_seqs, q_len, n_heads);
+    if (rc) return rc;
+    if (n_seqs * q_len > 1 && q_stride < (int64_t)n_heads * cache->head_dim) return QWG_ERR_SHAPE;
+    if (!aligned(q, size_of(type)) || !aligned(out, size_of(type)) || !aligned(prefix, 4) ||
+        !aligned(prefix_len, 4) || !aligned(table, 4) || !aligned(lens, 4) ||
+        !aligned(workspace, 16))
+        return QWG_ERR_ALIGN;
+    Kv8SharedArgs a = shared_of(cache, prefix_width, table_width, n_seqs, q_len, n_heads);
+    if (kv8_shared_partial_bytes(a) > workspace_bytes) return QWG_ERR_SHAPE;
+    for (Kv8AttendArgs *p : {&a.prefix, &a.own}) p->q = q, p->out = out, p->q_stride = q_stride, p->scale = scale;
+    a.prefix.table = prefix, a.prefix.lens = prefix_len, a.prefix.tails = lens;
+    a.own.table = table, a.own.lens = lens;
+    a.prefix.partial = (float *)workspace;
+    return hip_status(launch_kv8_attend_shared(a, type, (hipStream_t)stream));
+}
+
+int qwg_prompt_attend(void *out, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                      const void *v, int64_t v_stride, int type, int64_t n_tokens,
+                      const int32_t *starts, int64_t n_seqs, int64_t max_len, int n_heads,
+                      int n_kv_heads, int head_dim, float scale, int64_t window, void *stream) {
+    if (!out || !q || !k || !v) return QWG_ERR_NULL;
+    if (!known_type(type)) return QWG_ERR_TYPE;
+    if (!kv8_dim_supported(head_dim) || n_kv_heads < 1 || n_kv_heads > 1024 || n_heads < 1 ||
+        n_heads > 65535 || n_heads % n_kv_heads)
+        return QWG_ERR_SHAPE;
+    const int64_t width = (int64_t)n_kv_heads * head_dim, q_width = (int64_t)n_heads * head_dim;
+    if (n_seqs < 1 || n_seqs * n_kv_heads > kMaxPromptPairs || n_seqs > kMaxPromptPairs ||
+        n_tokens < 1 || n_tokens > kMaxPromptRows || n_tokens * n_heads > kMaxPromptRows ||
+        max_len < 0 || window < 0 || (!starts && n_tokens % n_seqs) ||
+        (n_tokens > 1 && (q_stride < q_width || k_stride < width || v_stride < width)))
+        return QWG_ERR_SHAPE;
+    const uintptr_t size = size_of(type);
+    if (!aligned(q, size) || !aligned(k, size) || !aligned(v, size) || !aligned(out, size) ||
+        !aligned(starts, 4))
+        return QWG_ERR_ALIGN;
+    PromptArgs a = {q, k, v, out, q_stride, k_stride, v_stride, starts, n_tokens, n_seqs, window,
+                    n_heads, n_kv_heads, head_dim, scale, false};
+    if (n_tokens == 1) a.q_stride = q_width, a.k_stride = a.v_stride = width;
+    a.vec = aligned(q, 16) && aligned(k, 16) && aligned(v, 16) &&
+            (a.q_stride | a.k_stride | a.v_stride) * size % 16 == 0;
+    return hip_status(launch_prompt_attend(a, type, (hipStream_t)stream));
 }
 
 }  // extern "C"

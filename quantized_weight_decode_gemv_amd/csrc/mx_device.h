@@ -79,4 +79,19 @@ __device__ __forceinline__ void load8(const T *p, float (&v)[8]) {
     }
 }
 
+// The other way, each value rounded once.
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T *p, const float (&v)[8]) {
+    if constexpr (VEC) {
+        typedef T t8 __attribute__((ext_vector_type(8), aligned(16)));
+        t8 x;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (T)v[i];
+        *(t8 *)p = x;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = (T)v[i];
+    }
+}
+
 }  // namespace qwg

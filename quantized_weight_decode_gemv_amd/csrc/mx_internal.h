@@ -1,6 +1,6 @@
 // Interfaces between the host boundary (mx_api.cpp) and the kernels of the
-// microscaled weights (mx.hip, mx_gemm.hip, mx_matmul.hip) and of the 8-bit
-// key/value cache (kv8.hip).
+// microscaled weights (mx.hip, mx_gemm.hip, mx_matmul.hip), of the 8-bit
+// key/value cache (kv8.hip) and of attention over prompts (prompt.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -50,6 +50,16 @@ struct Kv8AppendArgs {
     int64_t width, n_seqs, max_new;
 };
 
+struct Kv8RotaryArgs : Kv8AppendArgs {
+    const void *q;          // [n_tokens][n_heads][dim]
+    void *q_out, *k_out;    // the same shapes as q and k; k_out may be null
+    int64_t q_stride, q_out_stride, k_out_stride;
+    const float *freqs;     // [rotary / 2], radians per position
+    const int32_t *before;  // positions before every sequence's own (a shared prefix), or null
+    int n_heads, rotary;    // rotary: channels that turn, a multiple of 16
+    bool neighbours;        // pairs (2j, 2j + 1), or (j, j + rotary / 2)
+};
+
 struct Kv8AttendArgs {
     Kv8 cache;
     const void *q;  // [n_seqs * q_len][n_heads][dim], token stride below
@@ -66,6 +76,27 @@ struct Kv8AttendArgs {
     bool brief;      // more workgroups than fit at once, as far as known of 512 positions at most
     bool few;        // as far as known one split each, and no more workgroups, empty ones too, than compute units
     float *partial;  // [n_seqs][max_splits][q_len * n_heads][dim + 2], or null for one split
+    // the prefix that sequences share, as one sequence that holds the rows of all of them:
+    const int32_t *tails;  // each one's own positions, or null
+    int tail_q_len;        // its query tokens
+    bool parts;            // what one split sums goes to `partial` too
+};
+
+// Attention behind a shared prefix: its two passes, whose parts are joined.
+struct Kv8SharedArgs {
+    Kv8AttendArgs prefix, own;
+};
+
+// Attention over prompts as their products give them, tokens of all sequences in a row.
+struct PromptArgs {
+    const void *q, *k, *v;  // [n_tokens][n_heads or n_kv][dim], token strides below
+    void *out;              // [n_tokens][n_heads][dim]
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t *starts;  // [n_seqs + 1], or null: n_tokens / n_seqs tokens each
+    int64_t n_tokens, n_seqs, window;
+    int n_heads, n_kv, dim;
+    float scale;
+    bool vec;  // q, k and v rows start on 16 bytes
 };
 
 hipError_t launch_mxfp4_encode(uint8_t *codes, uint8_t *scales, const void *x, int type,
@@ -75,10 +106,15 @@ hipError_t launch_mxfp4_dequant(const uint8_t *codes, const uint8_t *scales, voi
 hipError_t launch_mxfp4_gemm(const MxGemmArgs &a, int type, hipStream_t s);
 hipError_t launch_mxfp4_matmul(const MxMatmulArgs &a, int type, hipStream_t s);
 hipError_t launch_kv8_append(const Kv8AppendArgs &a, int type, hipStream_t s);
+hipError_t launch_kv8_append_rotary(const Kv8RotaryArgs &a, int type, hipStream_t s);
 bool kv8_dim_supported(int dim);
 // Sets what shapes the launch: row_tiles, chunk, max_splits, few and brief.
 void kv8_attend_plan(Kv8AttendArgs &a, int64_t max_len, int cus);
 int64_t kv8_attend_partial_bytes(const Kv8AttendArgs &a);
 hipError_t launch_kv8_attend(const Kv8AttendArgs &a, int type, hipStream_t s);
+hipError_t launch_prompt_attend(const PromptArgs &a, int type, hipStream_t s);
+void kv8_shared_plan(Kv8SharedArgs &a, int cus);
+int64_t kv8_shared_partial_bytes(const Kv8SharedArgs &a);
+hipError_t launch_kv8_attend_shared(Kv8SharedArgs &a, int type, hipStream_t s);
 
 }  // namespace qwg

@@ -1,0 +1,424 @@
+// Causal attention over whole prompts, packed one behind another, before their keys and
+// values are held in 8 bits: out[t, h] = sum_j softmax_j(scale q[t, h] . k[j, h / group])
+// v[j, h / group] over the positions j <= t of the same sequence (the last `window` of them).
+#include <algorithm>
+#include <type_traits>
+
+#include "mx_device.h"
+#include "mx_lds.h"
+
+namespace qwg {
+
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Two fp32 values rounded to a 16-bit type (nearest, ties to even) in one word.
+template <int TYPE>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (TYPE == kF16) return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+    else return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+}
+
+// 32 x 32 outputs of 16 products each from two operands of eight 16-bit values a lane.
+template <int TYPE>
+__device__ __forceinline__ f32x16 mfma16(u32x4 a, u32x4 b, f32x16 c) {
+    if constexpr (TYPE == kF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// Four positions of one channel each from a [position][channel] tile of 16-bit values: of
+// sixteen lanes, lane i gives the address of four channels of position i / 4 and takes channel i.
+__device__ __forceinline__ u32x2 read_turned(const uint8_t *p) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                         (__attribute__((address_space(3))) s16x4 *)p));
+}
+
+__device__ __forceinline__ float max_halves(float v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(f2u(v), f2u(v), false, false);
+    return fmaxf(u2f(a[0]), u2f(a[1]));
+}
+
+__device__ __forceinline__ float sum_halves(float v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(f2u(v), f2u(v), false, false);
+    return u2f(a[0]) + u2f(a[1]);
+}
+
+constexpr int kInSlack = 8;  // a maximum may grow by this many powers of two before sums shrink
+
+// Positions of a block of keys and values in LDS.
+constexpr int block_of(int type, int d) { return type == kF32 && d > 128 ? 32 : 64; }
+
+// The first token of a sequence, its length and which of its tiles the workgroup takes:
+// false past the last tile. Every wavefront looks for itself.
+__device__ __forceinline__ bool find_tile(const PromptArgs &a, int64_t at, int tile_rows, int group,
+                                          int64_t &first, int &len, int &tile) {
+    const int lane = threadIdx.x & 63;
+    for (int64_t s0 = 0; s0 < a.n_seqs; s0 += 64) {
+        const int64_t s = s0 + lane;
+        int64_t begin = 0, end = 0;
+        if (s < a.n_seqs) {
+            if (a.starts) {
+                begin = min(max((int64_t)a.starts[s], (int64_t)0), a.n_tokens);
+                end = min(max((int64_t)a.starts[s + 1], begin), a.n_tokens);
+            } else {
+                const int64_t each = a.n_tokens / a.n_seqs;
+                begin = s * each, end = begin + each;
+            }
+        }
+        const int tiles = (int)(((end - begin) * group + tile_rows - 1) / tile_rows);
+        int upto = tiles;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(upto, o);
+            if (lane >= o) upto += v;
+        }
+        const uint64_t past = __ballot(at < upto);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            first = ((int64_t)__shfl((int)(begin >> 32), l) << 32) | (uint32_t)__shfl((int)begin, l);
+            len = __shfl((int)(end - begin), l);
+            // the tiles that see the most come first
+            tile = __shfl(upto, l) - 1 - (int)at;
+            return true;
+        }
+        at -= __shfl(upto, 63);
+    }
+    return false;
+}
+
+// One workgroup: one tile of rows of one sequence and key/value head; a row is a (token, head
+// of the group) pair, so that the heads that read the same keys take them from LDS together. A
+// wavefront holds R x 32 rows (their queries and sums in registers); all share the blocks of keys
+// and values, which come by LDS DMA, two blocks in turn.
+//
+// S^T = K Q^T on 32 x 32 tiles gives a lane sixteen scores of one row, at positions
+// 8(i/4) + 4(lane/32) + i%4: with the other half lane's a whole row of them, so that maximum and sum
+// cross lanes once. The lane's scores eight by eight are the B operand of O^T = V^T P^T as they
+// stand; the A operand's eight positions of a channel are two transposing reads of V.
+//
+// Probabilities of the 16-bit types are rounded to that type (by 2^-8 or 2^-11
+// of themselves at most, as often up as down: the output's own rounding once more); their
+// sum is taken before.
+//
+// Non-finite values in V where some row of the tile does not see them are set to zero in
+// LDS (0 times infinity is NaN) and added at the end for the rows that do see them.
+template <int TYPE, int D, int W, int R>
+__global__ __launch_bounds__(W * 64) void prompt_kernel(PromptArgs a) {
+    typedef typename Elem<TYPE>::T T;
+    constexpr int B = block_of(TYPE, D);
+    constexpr int U = B / 32;                       // score tiles of a block
+    constexpr int G = D * (int)sizeof(T) / 16;      // 16-byte granules of a row
+    constexpr int kTile = B * G * 16;               // bytes of a block's K (or V)
+    constexpr int DT = D / 32;                      // channel tiles
+    constexpr int E = 16 / (int)sizeof(T);          // values of a granule
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int n = lane & 31, g = lane >> 5;
+    const int group = a.n_heads / a.n_kv;
+    const int head = (int)(blockIdx.x % a.n_kv);
+    int64_t first;
+    int len, tile;
+    if (!find_tile(a, blockIdx.x / a.n_kv, W * R * 32, group, first, len, tile)) return;
+    const int64_t rows = (int64_t)len * group;
+    const int64_t row0 = (int64_t)tile * (W * R * 32), wrow0 = row0 + wave * R * 32;
+    // tokens of the workgroup's rows and of the wavefront's
+    const int t_lo = (int)(row0 / group), t_hi = (int)min((row0 + W * R * 32 - 1) / group, (int64_t)len - 1);
+    const int w_lo = (int)(wrow0 / group), w_hi = (int)min((wrow0 + R * 32 - 1) / group, (int64_t)len - 1);
+    const bool idle = wrow0 >= rows;
+    const int window = (int)min(a.window, (int64_t)1 << 30);  // 0: all
+
+    extern __shared__ __align__(16) uint8_t lds[];
+    int *const dirty = (int *)(lds + 4 * kTile);
+    if (threadIdx.x == 0) *dirty = 0;
+
+    // queries: the B operand's lane takes row n, eight channels (four of fp32) per half
+    const bool flip = a.scale < 0;  // the maximum is taken before the scale
+    const float to_log2 = fabsf(a.scale) * 1.4426950408889634f;
+    u32x4 q[R][G / 2];
+    int token[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int64_t row = wrow0 + r * 32 + n;
+        token[r] = row < rows ? (int)(row / group) : -1;
+        const T *p = (const T *)a.q + (first + max(token[r], 0)) * a.q_stride +
+                     (int64_t)(head * group + (int)(row % group)) * D;
+#pragma unroll
+        for (int s = 0; s < G / 2; ++s) {
+            u32x4 w = {0, 0, 0, 0};
+            if (token[r] >= 0) {
+                if (a.vec) {
+                    w = *(const u32x4 *)(p + (s * 2 + g) * E);
+                } else {
+                    T v[E];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[e] = p[(s * 2 + g) * E + e];
+                    __builtin_memcpy(&w, v, 16);
+                }
+            }
+            const uint32_t sign = flip ? (sizeof(T) == 4 ? 0x80000000u : 0x80008000u) : 0u;
+            q[r][s] = w ^ sign;
+        }
+    }
+
+    // granule f of a tile in LDS holds granule (f % G) ^ key of row f / G: what eight lanes
+    // read at once lies in eight different ones of the 128 bytes that LDS gives at a time
+    auto k_key = [](int row) {
+        if constexpr (G % 8 == 0) return row & 7;
+        else return row >> 1 & 3;  // (12 granules: rows start at 0 and 64 bytes in turn)
+    };
+    auto v_key = [](int row) {
+        if constexpr (TYPE == kF32) return 0;
+        else if constexpr (G % 8 == 0) return (row & 3) * 2;
+        else return (row >> 1 & 1) * 2;
+    };
+    const T *const kp = (const T *)a.k + first * a.k_stride + (int64_t)head * D;
+    const T *const vp = (const T *)a.v + first * a.v_stride + (int64_t)head * D;
+    auto issue = [&](int b0, int buf) {
+        const uint32_t to = buf * 2 * kTile;
+        for (int i = wave; i < B * G / 64; i += W) {
+            const int f = i * 64 + lane, row = f / G, s = f - row * G;
+            const int64_t pos = min(b0 + row, len - 1);  // past the end: masked
+            const T *pk = kp + pos * a.k_stride + (s ^ k_key(row)) * E;
+            const T *pv = vp + pos * a.v_stride + (s ^ v_key(row)) * E;
+            if (a.vec) {
+                dma16(pk, to + i * 1024);
+                dma16(pv, to + kTile + i * 1024);
+            } else {
+                T x[E], y[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[e] = pk[e], y[e] = pv[e];
+                __builtin_memcpy(lds + to + f * 16, x, 16);
+                __builtin_memcpy(lds + to + kTile + f * 16, y, 16);
+            }
+        }
+    };
+
+    float top[R], sum[R];  // maximum times to_log2, sum of this half lane's probabilities
+    f32x16 out[R][DT];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        top[r] = -__builtin_inff();
+        sum[r] = 0;
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) out[r][t][i] = 0;
+    }
+    const int low = window > 0 ? max(0, t_lo - window + 1) / B * B : 0;
+    // whether every one of the tokens from lo to hi sees the whole block
+    auto whole = [&](int b0, int lo, int hi) { return b0 + B - 1 <= lo && (window == 0 || b0 > hi - window); };
+
+    issue(low, 0);
+    int buf = 0;
+    for (int b0 = low; b0 <= t_hi; b0 += B, buf ^= 1) {
+        wait_vmcnt<0>();
+        __syncthreads();
+        if (b0 + B <= t_hi) issue(b0 + B, buf ^ 1);
+        uint8_t *const k_lds = lds + buf * 2 * kTile, *const v_lds = k_lds + kTile;
+        if (!whole(b0, t_lo, t_hi)) {
+            bool found = false;
+            for (int f = threadIdx.x; f < B * G; f += W * 64) {
+                u32x4 w = *(u32x4 *)(v_lds + f * 16);
+                bool here = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    constexpr uint32_t x = TYPE == kF32 ? 0x7f800000u : TYPE == kF16 ? 0x7c00u : 0x7f80u;
+                    if constexpr (TYPE == kF32) {
+                        if ((w[e] & x) == x) w[e] = 0, here = true;
+                    } else {
+                        if ((w[e] & x) == x) w[e] &= 0xffff0000u, here = true;
+                        if ((w[e] >> 16 & x) == x) w[e] &= 0xffffu, here = true;
+                    }
+                }
+                if (here) *(u32x4 *)(v_lds + f * 16) = w, found = true;
+            }
+            if (found) *dirty = 1;
+            __syncthreads();
+        }
+        if (idle || b0 > w_hi || (window > 0 && b0 + B - 1 <= w_lo - window)) continue;
+
+        f32x16 s[R][U];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[r][u][i] = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint8_t *const row = k_lds + (u * 32 + n) * G * 16;
+            const int key = k_key(n);
+#pragma unroll
+            for (int c = 0; c < G / 2; ++c) {
+                const u32x4 k = *(const u32x4 *)(row + ((c * 2 + g) ^ key) * 16);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    if constexpr (TYPE == kF32) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            s[r][u] = __builtin_amdgcn_mfma_f32_32x32x2f32(u2f(k[e]), u2f(q[r][c][e]), s[r][u], 0, 0, 0);
+                    } else {
+                        s[r][u] = mfma16<TYPE>(k, q[r][c], s[r][u]);
+                    }
+                }
+            }
+        }
+        const bool clear = whole(b0, w_lo, w_hi);
+        u32x4 p[R][TYPE == kF32 ? 1 : U * 2];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            auto seen = [&](int u, int i) {
+                const int pos = b0 + u * 32 + (i >> 2) * 8 + g * 4 + (i & 3);
+                return pos <= token[r] && (window == 0 || pos > token[r] - window);
+            };
+            float m = -__builtin_inff();
+            if (clear) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) m = fmaxf(m, s[r][u][i]);
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (seen(u, i)) m = fmaxf(m, s[r][u][i]);
+            }
+            m = max_halves(m);
+            m = m == -__builtin_inff() ? m : m * to_log2;
+            if (__any(m > top[r] + (top[r] == -__builtin_inff() ? 0 : kInSlack))) {
+                const float now = fmaxf(top[r], m);
+                const float alpha = now == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(top[r] - now);
+                top[r] = now;
+                sum[r] *= alpha;
+#pragma unroll
+                for (int t = 0; t < DT; ++t) out[r][t] *= alpha;
+            }
+            const float base = top[r] == -__builtin_inff() ? 0.0f : top[r];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    s[r][u][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][u][i], to_log2, -base));
+            if (!clear) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (!seen(u, i)) s[r][u][i] = 0;
+            }
+            float part[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) part[i & 3] += s[r][u][i];
+            sum[r] += (part[0] + part[1]) + (part[2] + part[3]);
+            if constexpr (TYPE != kF32) {
+#pragma unroll
+                for (int j = 0; j < U * 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        p[r][j][e] = pack2<TYPE>(s[r][j / 2][(j & 1) * 8 + e * 2], s[r][j / 2][(j & 1) * 8 + e * 2 + 1]);
+            }
+        }
+        if constexpr (TYPE == kF32) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float *row = (const float *)(v_lds + (u * 32 + (i >> 2) * 8 + g * 4 + (i & 3)) * G * 16);
+#pragma unroll
+                    for (int t = 0; t < DT; ++t)
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+                            out[r][t] = __builtin_amdgcn_mfma_f32_32x32x2f32(row[t * 32 + n], s[r][u][i], out[r][t], 0, 0, 0);
+                }
+        } else {
+            const int row = g * 4 + (n >> 2 & 3);  // (+ 8, for the second four positions)
+            const int at = (n >> 4) * 2 + (n >> 1 & 1);
+#pragma unroll
+            for (int j = 0; j < U * 2; ++j)
+#pragma unroll
+                for (int t = 0; t < DT; ++t) {
+                    const uint8_t *v = v_lds + ((j * 16 + row) * G + ((t * 4 + at) ^ v_key(row))) * 16 + (n & 1) * 8;
+                    const u32x2 x = read_turned(v), y = read_turned(v + 8 * G * 16);
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        out[r][t] = mfma16<TYPE>(u32x4{x[0], x[1], y[0], y[1]}, p[r][j], out[r][t]);
+                }
+        }
+    }
+
+    __syncthreads();
+    const bool mend = *dirty != 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float total = sum_halves(sum[r]);
+        if (token[r] < 0) continue;
+        const int64_t row = wrow0 + r * 32 + n;
+        const float inv = 1.0f / total;
+        T *dst = (T *)a.out + ((first + token[r]) * a.n_heads + head * group + (int)(row % group)) * D;
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const int d = t * 32 + i * 2 + g * 4;
+                float o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = out[r][t][i + e] * inv;
+                if (mend) {
+                    for (int b0 = low; b0 <= token[r]; b0 += B) {
+                        if (whole(b0, t_lo, t_hi)) continue;
+                        for (int j = b0; j < b0 + B && j <= token[r]; ++j) {
+                            if (window > 0 && j <= token[r] - window) continue;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float v = (float)vp[(int64_t)j * a.v_stride + d + e];
+                                if (!(fabsf(v) < __builtin_inff())) o[e] += v;
+                            }
+                        }
+                    }
+                }
+                typedef T t4 __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+                *(t4 *)(dst + d) = t4{(T)o[0], (T)o[1], (T)o[2], (T)o[3]};
+            }
+    }
+}
+
+template <int TYPE, int D>
+hipError_t prompt(const PromptArgs &a, hipStream_t s) {
+    constexpr int W = 4, R = 1;
+    constexpr size_t lds = 4 * (size_t)block_of(TYPE, D) * D * sizeof(typename Elem<TYPE>::T) + 16;
+    static_assert(lds <= 160 * 1024, "LDS");
+    const int64_t group = a.n_heads / a.n_kv;
+    const int64_t tiles = a.n_tokens * group / (W * R * 32) + a.n_seqs;
+    prompt_kernel<TYPE, D, W, R><<<dim3((unsigned)(tiles * a.n_kv)), W * 64, lds, s>>>(a);
+    return hipGetLastError();
+}
+
+template <int TYPE>
+hipError_t prompt_dim(const PromptArgs &a, hipStream_t s) {
+    switch (a.dim) {
+        case 64: return prompt<TYPE, 64>(a, s);
+        case 96: return prompt<TYPE, 96>(a, s);
+        case 128: return prompt<TYPE, 128>(a, s);
+        case 192: return prompt<TYPE, 192>(a, s);
+        default: return prompt<TYPE, 256>(a, s);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_prompt_attend(const PromptArgs &a, int type, hipStream_t s) {
+    if (type == kF32) return prompt_dim<kF32>(a, s);
+    if (type == kF16) return prompt_dim<kF16>(a, s);
+    return prompt_dim<kBF16>(a, s);
+}
+
+}  // namespace qwg

@@ -440,6 +440,7 @@ const char *qwg_strerror(int status) {
         case QWG_ERR_TIMEOUT:
             return "a wait of the layer-chain launch gave up (its flags have been reset)";
         case QWG_ERR_TYPE: return "unknown element type (QWG_F32, QWG_F16 or QWG_BF16)";
+        case QWG_ERR_OVERLAP: return "a result would overwrite what the call still reads";
         case QWG_ERR_CAPTURE:
             return "the stream is being captured and has no split-sum workspace yet "
                    "(qwg_workspace_reserve it before capture, or call qwg_gemm_q4k_noalloc)";
