@@ -11,322 +11,13 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "kv8_append.h"
 #include "mx_device.h"
 #include "mx_lds.h"
 
 namespace qwg {
 
 namespace {
-
-// ------------------------------------------------------------------- append
-
-// The biased exponent of the smallest power of two s with top / s <= 448 =
-// 1.75 * 2^8, `top` given as the bits of a finite magnitude.
-__device__ __forceinline__ uint32_t page_exponent(uint32_t top) {
-    const int e = (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
-    return e > 0 ? (uint32_t)e : 0;
-}
-
-// Four codes of a value each, the first in the low byte. NaN and infinity become
-// NaN codes.
-__device__ __forceinline__ uint32_t fp8_codes(float a, float b, float c, float d, float scale) {
-    typedef short s16x2 __attribute__((ext_vector_type(2)));
-    s16x2 v = {0, 0};
-    v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v, a, b, scale, false);
-    v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v, c, d, scale, true);
-    return __builtin_bit_cast(uint32_t, v);
-}
-
-// The four codes of a word, times `shift`, as codes.
-__device__ __forceinline__ uint32_t fp8_shifted(uint32_t w, float shift) {
-    return fp8_codes(__builtin_amdgcn_cvt_f32_fp8((int)w, 0) * shift,
-                     __builtin_amdgcn_cvt_f32_fp8((int)w, 1) * shift,
-                     __builtin_amdgcn_cvt_f32_fp8((int)w, 2) * shift,
-                     __builtin_amdgcn_cvt_f32_fp8((int)w, 3) * shift, 1.0f);
-}
-
-// sin and cos of 2 pi t, t in turns. A position times a frequency is exact enough in 64
-// bits alone (position 10^5 at one radian each: fp32 leaves 2^-8 of a radian), and there the
-// rest is cheap too: the quarter turn comes off exactly, and the Taylor sums of what is
-// left, at most pi/4, end where the next term is below 2^-45.
-__device__ __forceinline__ void sincos_turns(double t, double &s, double &c) {
-    const double quarter = __builtin_rint(t * 4.0);
-    const double x = __builtin_fma(quarter, -0.25, t) * 6.283185307179586, x2 = x * x;
-    double a = 1.0 / 6227020800.0, b = -1.0 / 87178291200.0;
-    a = __builtin_fma(a, x2, -1.0 / 39916800.0);
-    b = __builtin_fma(b, x2, 1.0 / 479001600.0);
-    a = __builtin_fma(a, x2, 1.0 / 362880.0);
-    b = __builtin_fma(b, x2, -1.0 / 3628800.0);
-    a = __builtin_fma(a, x2, -1.0 / 5040.0);
-    b = __builtin_fma(b, x2, 1.0 / 40320.0);
-    a = __builtin_fma(a, x2, 1.0 / 120.0);
-    b = __builtin_fma(b, x2, -1.0 / 720.0);
-    a = __builtin_fma(a, x2, -1.0 / 6.0);
-    b = __builtin_fma(b, x2, 1.0 / 24.0);
-    b = __builtin_fma(b, x2, -0.5);
-    a = __builtin_fma(a * x2, x, x);  // sin x
-    b = __builtin_fma(b, x2, 1.0);    // cos x
-    const double round = quarter * 0.25;
-    const int k = (int)((round - __builtin_floor(round)) * 4.0);  // quarter mod 4
-    const double u = k & 1 ? b : a, w = k & 1 ? a : b;
-    s = k & 2 ? -u : u;
-    c = (k + 1) & 2 ? -w : w;
-}
-
-constexpr double kTurnsPerRadian = 0.15915494309189535;
-// how the channels of a head pair up: not at all, the first half with the second, neighbours
-constexpr int kPlain = 0, kHalves = 1, kNeighbours = 2;
-constexpr int kSliceHeads = 8;  // heads that a workgroup rotates for q_out or k_out
-constexpr int kHeadsAtOnce = 4;  // of them under the same angles
-
-// The tokens of a sequence, rotated, to q_out or k_out: eight heads at most of one chunk of
-// `page` tokens after another. A thread takes eight channels (and the eight that they pair with)
-// of four heads of one token: the angles are the same for all of them, and cost what two
-// heads' loads do.
-template <typename T, int ROT, int threads>
-__device__ __forceinline__ void rotate_rows(const T *x, int64_t x_stride, T *to, int64_t to_stride, int heads,
-                                            const Kv8RotaryArgs &a, int64_t first, int64_t count, int64_t held) {
-    const int dim = a.cache.dim, page = a.cache.page, half = a.rotary / 2;
-    const bool vec = (((uintptr_t)x | (uintptr_t)to | (uintptr_t)x_stride * sizeof(T) |
-                       (uintptr_t)to_stride * sizeof(T)) & 15) == 0;
-    const int units = (ROT == kHalves ? dim - half : dim) / 8;
-    const int sets = (heads + kHeadsAtOnce - 1) / kHeadsAtOnce;
-    auto load = [&](const T *p, float (&v)[8]) { vec ? load8<T, true>(p, v) : load8<T, false>(p, v); };
-    auto store = [&](T *p, const float (&v)[8]) { vec ? store8<T, true>(p, v) : store8<T, false>(p, v); };
-    for (int64_t i0 = (int64_t)blockIdx.x * page; i0 < count; i0 += (int64_t)gridDim.x * page) {
-        const int items = (int)min((int64_t)page, count - i0) * sets * units;
-        for (int i = threadIdx.x; i < items; i += threads) {
-            const int u = i % units, r = i / units, h0 = r % sets * kHeadsAtOnce;
-            const int64_t token = i0 + r / sets;
-            const int d = ROT == kHalves && u >= half / 8 ? u * 8 + half : u * 8;
-            const T *p = x + (first + token) * x_stride + (int64_t)h0 * dim + d;
-            T *o = to + (first + token) * to_stride + (int64_t)h0 * dim + d;
-            const int n = min(kHeadsAtOnce, heads - h0);
-            float v[kHeadsAtOnce][8], w[kHeadsAtOnce][8];
-#pragma unroll
-            for (int h = 0; h < kHeadsAtOnce; ++h)
-                if (h < n) {
-                    load(p + h * dim, v[h]);
-                    if (ROT == kHalves && d < half) load(p + h * dim + half, w[h]);
-                }
-            if (d < (ROT == kHalves ? half : a.rotary)) {
-                const double pos = (double)(held + token);
-#pragma unroll
-                for (int e = 0; e < (ROT == kHalves ? 8 : 4); ++e) {
-                    double s, c;
-                    sincos_turns(pos * (a.freqs[ROT == kHalves ? d + e : d / 2 + e] * kTurnsPerRadian), s, c);
-                    const float sf = (float)s, cf = (float)c;
-#pragma unroll
-                    for (int h = 0; h < kHeadsAtOnce; ++h) {
-                        float &p0 = ROT == kHalves ? v[h][e] : v[h][e * 2 & 7];
-                        float &p1 = ROT == kHalves ? w[h][e] : v[h][(e * 2 + 1) & 7];
-                        const float x0 = p0, x1 = p1;
-                        p0 = __builtin_fmaf(x0, cf, -(x1 * sf));
-                        p1 = __builtin_fmaf(x1, cf, x0 * sf);
-                    }
-                }
-            }
-#pragma unroll
-            for (int h = 0; h < kHeadsAtOnce; ++h)
-                if (h < n) {
-                    store(o + h * dim, v[h]);
-                    if (ROT == kHalves && d < half) store(o + h * dim + half, w[h]);
-                }
-        }
-    }
-}
-
-template <int ROT>
-struct AppendArgs {
-    typedef Kv8RotaryArgs type;
-};
-template <>
-struct AppendArgs<kPlain> {
-    typedef Kv8AppendArgs type;
-};
-
-// One workgroup per (page of a sequence, sequence, head of K or V). A thread
-// takes four consecutive positions of eight channels: 8-byte stores to a K page,
-// 4-byte stores (one per channel) to a transposed V page. The page's largest new
-// magnitude comes first (one pass over the values, a cross-lane and an LDS step);
-// a thread's last tile stays in registers meanwhile, so that a page of up to `threads`
-// tiles is read once. Memory bounds it where there is much: 9 prompts of up to 2000
-// tokens, 8 heads of 128, bf16 (62 MB read and written): 17.4 us, 3.5 TB/s. One token
-// each of 33 sequences takes 5.4 us: the launch and four round trips in a row (length,
-// page number, values, exponent).
-// VEC: the values of a token start on 16 bytes.
-// ROT: keys are rotated on the way, in 64 bits and rounded once (a code then differs from
-// the exact key's by what 2^-24 of the key decides), and workgroups past the heads' rotate
-// q and, where asked for, k into q_out and k_out. The partner channels of a thread's eight are
-// read too (they come from the cache) rather than exchanged.
-template <int TYPE, bool VEC, int threads, int ROT>
-__global__ __launch_bounds__(threads) void kv8_append_kernel(typename AppendArgs<ROT>::type a) {
-    typedef typename Elem<TYPE>::T T;
-    __shared__ uint32_t tops[threads / 64];
-    const Kv8 &c = a.cache;
-    const int64_t seq = blockIdx.y;
-    const int head = (int)blockIdx.z >> 1;
-    const bool is_v = blockIdx.z & 1;
-    const int64_t held = a.lens[seq];
-    int64_t first, count;
-    if (a.starts) {
-        first = max((int64_t)a.starts[seq], (int64_t)0);
-        count = min((int64_t)a.starts[seq + 1], a.n_tokens) - first;
-    } else {
-        count = a.n_tokens / a.n_seqs;
-        first = seq * count;
-    }
-    int64_t before = 0;
-    if constexpr (ROT != kPlain) {
-        if (a.before) before = a.before[0];
-        int slice = (int)blockIdx.z - 2 * c.n_kv;
-        if (slice >= 0) {
-            const int of_q = (a.n_heads + kSliceHeads - 1) / kSliceHeads;
-            const bool q = slice < of_q;
-            const int h0 = (q ? slice : slice - of_q) * kSliceHeads, heads = (q ? a.n_heads : c.n_kv) - h0;
-            rotate_rows<T, ROT, threads>((const T *)(q ? a.q : a.k) + (int64_t)h0 * c.dim, q ? a.q_stride : a.k_stride,
-                                         (T *)(q ? a.q_out : a.k_out) + (int64_t)h0 * c.dim,
-                                         q ? a.q_out_stride : a.k_out_stride, min(heads, kSliceHeads), a, first,
-                                         count, held + before);
-            return;
-        }
-    }
-    if (held < 0 || count <= 0) return;
-    const T *x = (const T *)(is_v ? a.v : a.k) + (int64_t)head * c.dim;
-    const int64_t stride = is_v ? a.v_stride : a.k_stride;
-    const int64_t end = min(held + count, a.width * c.page);
-    const int octs = c.dim / 8;
-    for (int64_t p = held / c.page + blockIdx.x; p * c.page < end; p += gridDim.x) {
-        const int64_t id = a.table[seq * a.width + p];
-        if (id < 0 || id >= c.n_pages) continue;
-        const int64_t pos0 = p * c.page;
-        const int old = (int)max((int64_t)0, held - pos0);               // slots filled before
-        const int stop = (int)min((int64_t)c.page, end - pos0);          // slots filled after
-        uint8_t *codes = (is_v ? c.v : c.k) + (id * c.n_kv + head) * (int64_t)c.page * c.dim;
-        uint8_t *scale = (is_v ? c.v_scales : c.k_scales) + id * c.n_kv + head;
-        const T *x0 = x + (first + pos0 - held) * stride;                // token of slot 0
-        // tiles: groups of four slots from the one that holds slot `old`, by channel octets;
-        // neighbouring threads take neighbouring octets of K, neighbouring slots of V
-        const int g0 = old >> 2, groups = ((stop + 3) >> 2) - g0, tiles = groups * octs;
-        float v[4][8];
-        auto load = [&](int i, int &slot, int &d) {
-            const int by = is_v ? groups : octs, q = i / by, r = i - q * by;
-            slot = (g0 + (is_v ? r : q)) * 4, d = (is_v ? q : r) * 8;
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[t][e] = 0;
-                if (slot + t >= old && slot + t < stop)
-                    load8<T, VEC>(x0 + (slot + t) * stride + d, v[t]);
-            }
-            if constexpr (ROT != kPlain) {
-                if (is_v || d >= a.rotary) return;
-                const int half = a.rotary / 2;
-                const bool upper = d >= half;
-                float w[4][8];
-                if constexpr (ROT == kHalves) {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) w[t][e] = 0;
-                        if (slot + t >= old && slot + t < stop)
-                            load8<T, VEC>(x0 + (slot + t) * stride + (upper ? d - half : d + half), w[t]);
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < (ROT == kHalves ? 8 : 4); ++e) {
-                    const double f = a.freqs[ROT == kHalves ? (upper ? d - half : d) + e : d / 2 + e] * kTurnsPerRadian;
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        double sn, cs;
-                        sincos_turns((double)(before + pos0 + slot + t) * f, sn, cs);
-                        if constexpr (ROT == kHalves) {
-                            const double x = v[t][e], y = w[t][e];
-                            v[t][e] = (float)__builtin_fma(x, cs, upper ? y * sn : -(y * sn));
-                        } else {
-                            const double x = v[t][e * 2 & 7], y = v[t][(e * 2 + 1) & 7];
-                            v[t][e * 2 & 7] = (float)__builtin_fma(x, cs, -(y * sn));
-                            v[t][(e * 2 + 1) & 7] = (float)__builtin_fma(y, cs, x * sn);
-                        }
-                    }
-                }
-            }
-        };
-        uint32_t top = 0;
-        // the last tile of a thread is loaded last, and kept for the second pass
-        const int last = (int)threadIdx.x < tiles
-                             ? (int)threadIdx.x + (tiles - 1 - (int)threadIdx.x) / threads * threads
-                             : -1;
-        int slot = 0, d = 0;
-        for (int i = threadIdx.x; i < tiles; i += threads) {
-            load(i, slot, d);
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t m = f2u(v[t][e]) & 0x7fffffffu;
-                    top = max(top, m < 0x7f800000u ? m : 0u);
-                }
-        }
-#pragma unroll
-        for (int o = 32; o; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
-        __syncthreads();
-        if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < threads / 64; ++w) top = max(top, tops[w]);
-        const uint32_t before = old ? *scale : 0;
-        const uint32_t now = max(before, page_exponent(top));
-        const float sc = e8m0(now);
-        for (int i = last; i >= 0; i -= threads) {
-            if (i != last) load(i, slot, d);
-            const int lo = max(old - slot, 0), hi = min(stop - slot, 4);
-            if (!is_v) {
-                for (int t = lo; t < hi; ++t) {
-                    u32x2 w = {0, 0};
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        if (s == t)
-                            w = u32x2{fp8_codes(v[s][0], v[s][1], v[s][2], v[s][3], sc),
-                                      fp8_codes(v[s][4], v[s][5], v[s][6], v[s][7], sc)};
-                    *(u32x2 *)(codes + (slot + t) * c.dim + d) = w;
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t w = fp8_codes(v[0][e], v[1][e], v[2][e], v[3][e], sc);
-                    uint8_t *to = codes + (d + e) * c.page + slot;
-                    if (lo == 0 && hi == 4) {
-                        *(uint32_t *)to = w;
-                    } else {
-                        for (int t = lo; t < hi; ++t) to[t] = (uint8_t)(w >> (8 * t));
-                    }
-                }
-            }
-        }
-        if (old && now > before) {
-            // the page's scale rises: its earlier codes are rounded to the new one
-            const float shift = __builtin_ldexpf(1.0f, (int)before - (int)now);
-            if (!is_v) {
-                for (int i = threadIdx.x; i < old * c.dim / 4; i += threads)
-                    ((uint32_t *)codes)[i] = fp8_shifted(((uint32_t *)codes)[i], shift);
-            } else {
-                const int words = (old + 3) >> 2;
-                for (int i = threadIdx.x; i < words * c.dim; i += threads) {
-                    const int ch = i / words, s = (i - ch * words) * 4;
-                    uint8_t *at = codes + ch * c.page + s;
-                    if (s + 4 <= old) {
-                        *(uint32_t *)at = fp8_shifted(*(uint32_t *)at, shift);
-                    } else {  // the word's other slots may be getting new codes
-                        for (int t = 0; s + t < old; ++t) at[t] = (uint8_t)fp8_shifted(at[t], shift);
-                    }
-                }
-            }
-        }
-        __syncthreads();  // every thread has read the scale
-        if (threadIdx.x == 0) *scale = (uint8_t)now;
-    }
-}
 
 // ------------------------------------------------------------------- attend
 
@@ -1005,38 +696,6 @@ hipError_t attend_dim(const Kv8AttendArgs &a, hipStream_t s) {
     }
 }
 
-template <int TYPE, int ROT, typename Args>
-hipError_t append(const Args &a, hipStream_t s) {
-    // pages that max_new tokens touch at most; a sequence with more of them takes more trips
-    int64_t pages = a.max_new / a.cache.page + 2;
-    if (a.max_new <= 1) pages = 1;
-    if (pages > a.width) pages = a.width;
-    if (pages > 4096) pages = 4096;
-    int heads = a.cache.n_kv * 2;
-    if constexpr (ROT != kPlain) {
-        heads += (a.n_heads + kSliceHeads - 1) / kSliceHeads;
-        if (a.k_out) heads += (a.cache.n_kv + kSliceHeads - 1) / kSliceHeads;
-    }
-    const dim3 grid((unsigned)pages, (unsigned)a.n_seqs, (unsigned)heads);
-    const uintptr_t size = sizeof(typename Elem<TYPE>::T);
-    // (head_dim values are whole 16 bytes in every type)
-    const bool vec = ((uintptr_t)a.k | (uintptr_t)a.v) % 16 == 0 &&
-                     (a.n_tokens == 1 || (a.k_stride * size % 16 == 0 && a.v_stride * size % 16 == 0));
-    // a thread per tile of a full page, or per two (44 prompts of up to 491 tokens on
-    // pages of 16, 4 heads of 96, fp16: 32.8 us with 256 threads for the 48 tiles, 14.6
-    // with 64; 34 of 44 on pages of 64, 8 heads of 192: 20.9 with 1024 for the 384, 11.5
-    // with 512)
-    const int tiles = a.cache.page * a.cache.dim / 32;
-    auto run = [&](auto threads) {
-        if (vec) kv8_append_kernel<TYPE, true, threads.value, ROT><<<grid, threads.value, 0, s>>>(a);
-        else kv8_append_kernel<TYPE, false, threads.value, ROT><<<grid, threads.value, 0, s>>>(a);
-    };
-    if (tiles <= 64) run(std::integral_constant<int, 64>{});
-    else if (tiles <= 256) run(std::integral_constant<int, 256>{});
-    else run(std::integral_constant<int, 512>{});
-    return hipGetLastError();
-}
-
 }  // namespace
 
 bool kv8_dim_supported(int dim) {
@@ -1047,17 +706,6 @@ hipError_t launch_kv8_append(const Kv8AppendArgs &a, int type, hipStream_t s) {
     if (type == kF32) return append<kF32, kPlain>(a, s);
     if (type == kF16) return append<kF16, kPlain>(a, s);
     return append<kBF16, kPlain>(a, s);
-}
-
-hipError_t launch_kv8_append_rotary(const Kv8RotaryArgs &a, int type, hipStream_t s) {
-    if (a.neighbours) {
-        if (type == kF32) return append<kF32, kNeighbours>(a, s);
-        if (type == kF16) return append<kF16, kNeighbours>(a, s);
-        return append<kBF16, kNeighbours>(a, s);
-    }
-    if (type == kF32) return append<kF32, kHalves>(a, s);
-    if (type == kF16) return append<kF16, kHalves>(a, s);
-    return append<kBF16, kHalves>(a, s);
 }
 
 // Splits. A workgroup's start and end cost as much as three or four of its turns,

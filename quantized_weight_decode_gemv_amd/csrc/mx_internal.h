@@ -58,6 +58,8 @@ struct Kv8RotaryArgs : Kv8AppendArgs {
     const int32_t *before;  // positions before every sequence's own (a shared prefix), or null
     int n_heads, rotary;    // rotary: channels that turn, a multiple of 16
     bool neighbours;        // pairs (2j, 2j + 1), or (j, j + rotary / 2)
+    int slice, per_thread;  // heads of q or k_out that a workgroup rotates, and a thread
+    int rows;               // rotated keys that a workgroup holds at a time
 };
 
 struct Kv8AttendArgs {
@@ -106,7 +108,7 @@ hipError_t launch_mxfp4_dequant(const uint8_t *codes, const uint8_t *scales, voi
 hipError_t launch_mxfp4_gemm(const MxGemmArgs &a, int type, hipStream_t s);
 hipError_t launch_mxfp4_matmul(const MxMatmulArgs &a, int type, hipStream_t s);
 hipError_t launch_kv8_append(const Kv8AppendArgs &a, int type, hipStream_t s);
-hipError_t launch_kv8_append_rotary(const Kv8RotaryArgs &a, int type, hipStream_t s);
+hipError_t launch_kv8_append_rotary(Kv8RotaryArgs &a, int type, hipStream_t s);
 bool kv8_dim_supported(int dim);
 // Sets what shapes the launch: row_tiles, chunk, max_splits, few and brief.
 void kv8_attend_plan(Kv8AttendArgs &a, int64_t max_len, int cus);
