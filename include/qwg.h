@@ -687,7 +687,8 @@ int qwg_kv8_attend(const qwg_kv8 *cache, void *out, const void *q, int type, int
  * out [n_tokens][n_heads][head_dim] contiguous; head_dim as the cache's. Sequence s holds
  * tokens starts[s] .. starts[s+1]-1 (int32 [n_seqs+1], device, ascending; NULL: n_tokens /
  * n_seqs each); a sequence may be empty, and rows of tokens that belong to none are left as
- * they were. n_tokens * n_heads <= 2^28, n_seqs * n_kv_heads <= 2^22. Products, sums and softmax are
+ * they were. n_tokens * n_heads <= 2^28, n_seqs * n_kv_heads <= 2^22, k_stride and v_stride
+ * <= 2^23. Products, sums and softmax are
  * fp32; a probability is rounded to `type` before it meets v. What masked positions and
  * neighbouring sequences hold (NaN and infinities too) has no effect; a row whose visible
  * scores are all -infinity, or one of them +infinity or NaN, is NaN. max_len is the longest

@@ -35,6 +35,9 @@ constexpr int64_t kMaxOutputs = (int64_t)1 << 38;
 // tiles of 32 rows then stays below the 2^32 threads of a launch.
 constexpr int64_t kMaxPromptRows = (int64_t)1 << 28, kMaxPromptPairs = (int64_t)1 << 22;
 
+// Elements between two of its tokens' keys: a block of 64 then spans less than 2^32 bytes.
+constexpr int64_t kMaxPromptStride = 1 << 23;
+
 // Compute units of a current MI355X; the plan of a split needs no exact figure.
 constexpr int kCus = 256;
 
@@ -320,7 +323,8 @@ int qwg_prompt_attend(void *out, const void *q, int64_t q_stride, const void *k,
     if (n_seqs < 1 || n_seqs * n_kv_heads > kMaxPromptPairs || n_seqs > kMaxPromptPairs ||
         n_tokens < 1 || n_tokens > kMaxPromptRows || n_tokens * n_heads > kMaxPromptRows ||
         max_len < 0 || window < 0 || (!starts && n_tokens % n_seqs) ||
-        (n_tokens > 1 && (q_stride < q_width || k_stride < width || v_stride < width)))
+        (n_tokens > 1 && (q_stride < q_width || k_stride < width || v_stride < width ||
+                          k_stride > kMaxPromptStride || v_stride > kMaxPromptStride)))
         return QWG_ERR_SHAPE;
     const uintptr_t size = size_of(type);
     if (!aligned(q, size) || !aligned(k, size) || !aligned(v, size) || !aligned(out, size) ||

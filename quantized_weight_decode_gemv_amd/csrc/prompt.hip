@@ -39,9 +39,14 @@ __device__ __forceinline__ u32x2 read_turned(const uint8_t *p) {
                                          (__attribute__((address_space(3))) s16x4 *)p));
 }
 
+// One instruction; a NaN stays one.
+__device__ __forceinline__ float maximum3(float a, float b, float c) {
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
+}
+
 __device__ __forceinline__ float max_halves(float v) {
     const auto a = __builtin_amdgcn_permlane32_swap(f2u(v), f2u(v), false, false);
-    return fmaxf(u2f(a[0]), u2f(a[1]));
+    return __builtin_elementwise_maximum(u2f(a[0]), u2f(a[1]));
 }
 
 __device__ __forceinline__ float sum_halves(float v) {
@@ -49,7 +54,7 @@ __device__ __forceinline__ float sum_halves(float v) {
     return u2f(a[0]) + u2f(a[1]);
 }
 
-constexpr int kInSlack = 8;  // a maximum may grow by this many powers of two before sums shrink
+constexpr int kSlack = 8;  // a maximum may grow by this many powers of two before sums shrink
 
 // Positions of a block of keys and values in LDS.
 constexpr int block_of(int type, int d) { return type == kF32 && d > 128 ? 32 : 64; }
@@ -81,13 +86,14 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int64_t at, int t
         const uint64_t past = __ballot(at < upto);
         if (past) {
             const int l = __builtin_ctzll(past);
-            first = ((int64_t)__shfl((int)(begin >> 32), l) << 32) | (uint32_t)__shfl((int)begin, l);
-            len = __shfl((int)(end - begin), l);
+            auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+            first = ((int64_t)of((int)(begin >> 32)) << 32) | (uint32_t)of((int)begin);
+            len = of((int)(end - begin));
             // the tiles that see the most come first
-            tile = __shfl(upto, l) - 1 - (int)at;
+            tile = of(upto) - 1 - (int)at;
             return true;
         }
-        at -= __shfl(upto, 63);
+        at -= __builtin_amdgcn_readlane(upto, 63);
     }
     return false;
 }
@@ -109,7 +115,7 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int64_t at, int t
 // Non-finite values in V where some row of the tile does not see them are set to zero in
 // LDS (0 times infinity is NaN) and added at the end for the rows that do see them.
 template <int TYPE, int D, int W, int R>
-__global__ __launch_bounds__(W * 64) void prompt_kernel(PromptArgs a) {
+__global__ __launch_bounds__(W * 64, 2) void prompt_kernel(PromptArgs a) {
     typedef typename Elem<TYPE>::T T;
     constexpr int B = block_of(TYPE, D);
     constexpr int U = B / 32;                       // score tiles of a block
@@ -166,35 +172,45 @@ __global__ __launch_bounds__(W * 64) void prompt_kernel(PromptArgs a) {
         }
     }
 
-    // granule f of a tile in LDS holds granule (f % G) ^ key of row f / G: what eight lanes
-    // read at once lies in eight different ones of the 128 bytes that LDS gives at a time
-    auto k_key = [](int row) {
-        if constexpr (G % 8 == 0) return row & 7;
-        else return row >> 1 & 3;  // (12 granules: rows start at 0 and 64 bytes in turn)
-    };
+    // Granule f of a tile in LDS holds granule (f % G) ^ key of row f / G: the granules that
+    // sixteen lanes read of K at once, and thirty-two of V, lie in all of the 256 bytes that LDS gives
+    // (of rows of 16 granules a multiple, of 8, and of 12).
+    auto k_key = [](int row) { return G % 16 == 0 ? row & 15 : G % 8 == 0 ? row >> 1 & 7 : row >> 2 & 3; };
     auto v_key = [](int row) {
-        if constexpr (TYPE == kF32) return 0;
-        else if constexpr (G % 8 == 0) return (row & 3) * 2;
-        else return (row >> 1 & 1) * 2;
+        return TYPE == kF32 ? 0 : G % 16 == 0 ? (row & 3) * 4 : G % 8 == 0 ? (row & 3) * 2 : 0;
     };
     const T *const kp = (const T *)a.k + first * a.k_stride + (int64_t)head * D;
     const T *const vp = (const T *)a.v + first * a.v_stride + (int64_t)head * D;
+    // a wavefront's DMAs of a block: byte offsets from the block's first key and value
+    constexpr int N = (B * G / 64 + W - 1) / W;
+    uint32_t k_off[N], v_off[N];
+    auto offsets = [&](int last) {  // last: the block's last position, or the sequence's
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int f = (i * W + wave) * 64 + lane, row = f / G, c = f - row * G;
+            const uint32_t pos = min(row, last);  // past the end: masked
+            k_off[i] = (pos * (uint32_t)a.k_stride + (c ^ k_key(row)) * E) * sizeof(T);
+            v_off[i] = (pos * (uint32_t)a.v_stride + (c ^ v_key(row)) * E) * sizeof(T);
+        }
+    };
+    offsets(B - 1);
     auto issue = [&](int b0, int buf) {
-        const uint32_t to = buf * 2 * kTile;
-        for (int i = wave; i < B * G / 64; i += W) {
-            const int f = i * 64 + lane, row = f / G, s = f - row * G;
-            const int64_t pos = min(b0 + row, len - 1);  // past the end: masked
-            const T *pk = kp + pos * a.k_stride + (s ^ k_key(row)) * E;
-            const T *pv = vp + pos * a.v_stride + (s ^ v_key(row)) * E;
+        const uint32_t to = buf * 2 * kTile + wave * 1024;
+        const T *const k0 = kp + b0 * a.k_stride, *const v0 = vp + b0 * a.v_stride;
+        if (b0 + B > len) offsets(len - 1 - b0);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (B * G / 64 % W != 0 && i * W + wave >= B * G / 64) break;
             if (a.vec) {
-                dma16(pk, to + i * 1024);
-                dma16(pv, to + kTile + i * 1024);
+                dma16(k0, k_off[i], to + i * W * 1024);
+                dma16(v0, v_off[i], to + kTile + i * W * 1024);
             } else {
                 T x[E], y[E];
 #pragma unroll
-                for (int e = 0; e < E; ++e) x[e] = pk[e], y[e] = pv[e];
-                __builtin_memcpy(lds + to + f * 16, x, 16);
-                __builtin_memcpy(lds + to + kTile + f * 16, y, 16);
+                for (int e = 0; e < E; ++e)
+                    x[e] = k0[k_off[i] / sizeof(T) + e], y[e] = v0[v_off[i] / sizeof(T) + e];
+                __builtin_memcpy(lds + to + i * W * 1024 + lane * 16, x, 16);
+                __builtin_memcpy(lds + to + kTile + i * W * 1024 + lane * 16, y, 16);
             }
         }
     };
@@ -213,6 +229,14 @@ __global__ __launch_bounds__(W * 64) void prompt_kernel(PromptArgs a) {
     const int low = window > 0 ? max(0, t_lo - window + 1) / B * B : 0;
     // whether every one of the tokens from lo to hi sees the whole block
     auto whole = [&](int b0, int lo, int hi) { return b0 + B - 1 <= lo && (window == 0 || b0 > hi - window); };
+
+    // what a lane reads of V first: four channels of the position of its quarter
+    int v_at[DT];
+#pragma unroll
+    for (int t = 0; t < DT; ++t) {
+        const int row = g * 4 + (n >> 2 & 3), granule = t * 4 + (n >> 4) * 2 + (n >> 1 & 1);
+        v_at[t] = (row * G + (granule ^ v_key(row))) * 16 + (n & 1) * 8;
+    }
 
     issue(low, 0);
     int buf = 0;
@@ -269,31 +293,33 @@ __global__ __launch_bounds__(W * 64) void prompt_kernel(PromptArgs a) {
                 }
             }
         }
-        const bool clear = whole(b0, w_lo, w_hi);
         u32x4 p[R][TYPE == kF32 ? 1 : U * 2];
+        const bool clear = whole(b0, w_lo, w_hi);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+            // the positions that the lane's row sees, from the lane's first of the block
+            const int hi = token[r] - b0 - g * 4, lo = window > 0 ? hi - window : -1;
             auto seen = [&](int u, int i) {
-                const int pos = b0 + u * 32 + (i >> 2) * 8 + g * 4 + (i & 3);
-                return pos <= token[r] && (window == 0 || pos > token[r] - window);
+                const int pos = u * 32 + (i >> 2) * 8 + (i & 3);
+                return pos <= hi && pos > lo;
             };
-            float m = -__builtin_inff();
-            if (clear) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) m = fmaxf(m, s[r][u][i]);
-            } else {
+            if (!clear) {
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        if (seen(u, i)) m = fmaxf(m, s[r][u][i]);
+                        if (!seen(u, i)) s[r][u][i] = -__builtin_inff();
             }
-            m = max_halves(m);
-            m = m == -__builtin_inff() ? m : m * to_log2;
-            if (__any(m > top[r] + (top[r] == -__builtin_inff() ? 0 : kInSlack))) {
-                const float now = fmaxf(top[r], m);
+            float m[2] = {-__builtin_inff(), -__builtin_inff()};
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; i += 2)
+                    m[i >> 1 & 1] = maximum3(m[i >> 1 & 1], s[r][u][i], s[r][u][i + 1]);
+            const float t = max_halves(maximum3(m[0], m[1], m[1]));
+            const float scaled = t == -__builtin_inff() ? t : t * to_log2;
+            if (__any(scaled > top[r] + kSlack)) {  // (every number is more than -infinity)
+                const float now = fmaxf(top[r], scaled);
                 const float alpha = now == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(top[r] - now);
                 top[r] = now;
                 sum[r] *= alpha;
@@ -306,7 +332,7 @@ __global__ __launch_bounds__(W * 64) void prompt_kernel(PromptArgs a) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     s[r][u][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][u][i], to_log2, -base));
-            if (!clear) {
+            if (!clear) {  // (-infinity times a scale of zero is none)
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -340,13 +366,11 @@ __global__ __launch_bounds__(W * 64) void prompt_kernel(PromptArgs a) {
                             out[r][t] = __builtin_amdgcn_mfma_f32_32x32x2f32(row[t * 32 + n], s[r][u][i], out[r][t], 0, 0, 0);
                 }
         } else {
-            const int row = g * 4 + (n >> 2 & 3);  // (+ 8, for the second four positions)
-            const int at = (n >> 4) * 2 + (n >> 1 & 1);
 #pragma unroll
             for (int j = 0; j < U * 2; ++j)
 #pragma unroll
                 for (int t = 0; t < DT; ++t) {
-                    const uint8_t *v = v_lds + ((j * 16 + row) * G + ((t * 4 + at) ^ v_key(row))) * 16 + (n & 1) * 8;
+                    const uint8_t *v = v_lds + v_at[t] + j * 16 * G * 16;
                     const u32x2 x = read_turned(v), y = read_turned(v + 8 * G * 16);
 #pragma unroll
                     for (int r = 0; r < R; ++r)
