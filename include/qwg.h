@@ -717,7 +717,7 @@ int qwg_prompt_attend(void *out, const void *q, int64_t q_stride, const void *k,
                       const void *v, int64_t v_stride, int type, int64_t n_tokens,
                       const int32_t *starts, int64_t n_seqs, int64_t max_len, int n_heads,
                       int n_kv_heads, int head_dim, float scale, int64_t window, void *stream);
-int64_t qwg_kv8_attend_shared_workspace(const qwg_kv8 *cache, int64_t prefix_width,
+int64_t qwg_kv8_attend_shared_workspace(const qwg_kv8 *cache, int type, int64_t prefix_width,
                                         int64_t table_width, int64_t n_seqs, int q_len,
                                         int n_heads);
 int qwg_kv8_attend_shared(const qwg_kv8 *cache, void *out, const void *q, int type, int64_t q_stride,

@@ -117,7 +117,7 @@ def lib() -> ctypes.CDLL:
                                             P, P, I64, P, I64, I64, P]
         L.qwg_prompt_attend.argtypes = [P, P, I64, P, I64, P, I64, I, I64, P, I64, I64, I, I, I,
                                         ctypes.c_float, I64, P]
-        L.qwg_kv8_attend_shared_workspace.argtypes = [P, I64, I64, I64, I, I]
+        L.qwg_kv8_attend_shared_workspace.argtypes = [P, I, I64, I64, I64, I, I]
         L.qwg_kv8_attend_shared.argtypes = [P, P, P, I, I64, P, I64, P, P, I64, P, I64, I, I,
                                             ctypes.c_float, P, I64, P]
         for f in ("qwg_encode_mxfp4", "qwg_dequant_mxfp4", "qwg_gemv_mxfp4", "qwg_gemm_mxfp4",

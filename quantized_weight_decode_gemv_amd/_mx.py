@@ -480,7 +480,7 @@ def kv8_attend_shared(q: torch.Tensor, k_pages: torch.Tensor, k_scales: torch.Te
         raise ValueError("q_len * n_heads must be in 1..65535")
     out = _out(out, q.shape, q)
     ref = ctypes.byref(cache)
-    size = lib().qwg_kv8_attend_shared_workspace(ref, prefix.numel(), width, n_seqs, q_len, heads)
+    size = lib().qwg_kv8_attend_shared_workspace(ref, kind, prefix.numel(), width, n_seqs, q_len, heads)
     if size < 0:
         _check(-size, "qwg_kv8_attend_shared_workspace")
     # of this call's stream (or of the graph that captures it): no two calls share one

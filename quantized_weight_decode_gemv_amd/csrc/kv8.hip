@@ -12,6 +12,7 @@
 #include <type_traits>
 
 #include "kv8_append.h"
+#include "kv8_device.h"
 #include "mx_device.h"
 #include "mx_lds.h"
 
@@ -30,16 +31,6 @@ __device__ __forceinline__ bf16x8 fp8x8(uint32_t a, uint32_t b) {
     return bf16x8{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
 }
 
-constexpr int kBlk = 64;          // positions a wavefront takes at once
-constexpr int kMaxChunk = 4096;   // positions of a split, at most
-constexpr int kMaxPages = (kMaxChunk + kBlk) / 16 + 1;
-constexpr int kPageBytes = (kMaxPages * 8 + 15) & ~15;
-
-// Bytes of a word that hold a NaN code, as 0x80 each.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-    return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-}
-
 // The largest of the four lanes' values with the same lane % 16, without LDS.
 __device__ __forceinline__ float max_groups(float v) {
     const auto a = __builtin_amdgcn_permlane16_swap(f2u(v), f2u(v), false, false);
@@ -48,26 +39,10 @@ __device__ __forceinline__ float max_groups(float v) {
     return fmaxf(u2f(b[0]), u2f(b[1]));
 }
 
-// Two fp32 values' upper halves in one word, the first one's low.
-__device__ __forceinline__ uint32_t upper_halves(float a, float b) {
-    return __builtin_amdgcn_perm(f2u(b), f2u(a), 0x07060302u);
-}
-
-// Two fp32 values rounded to bf16 (nearest, ties to even) in one word, the first one low.
-__device__ __forceinline__ uint32_t nearest_halves(float a, float b) {
-    return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
-}
-
 // The block of positions that the first row's window starts in: what some row
 // sees is from there to the end, and the splits begin there.
 __device__ __forceinline__ int first_seen(int len, int q_len, int window) {
     return window > 0 ? max(0, len - q_len + 1 - window) & -kBlk : 0;
-}
-
-// Floats of one split's partial result: rows of D sums, then a (maximum, total)
-// pair per row, in whole 16 bytes.
-__device__ __host__ __forceinline__ int64_t partial_floats(int64_t rows, int dim) {
-    return (rows * (dim + 2) + 3) & ~(int64_t)3;
 }
 
 // LDS of an attention workgroup: Q parts, the split's pages, then per wavefront a
@@ -504,6 +479,51 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
     __syncthreads();
     const int64_t row_base = seq * a.q_len;
     const int64_t all = (int64_t)a.q_len * a.n_heads;
+    if (a.prefix_partial) {
+        // behind a shared prefix: its parts are joined here, by a launch that runs anyway, and
+        // the sequence's own sums never leave the compute unit
+        float *const meet = sm + W * R * 16 * 2;  // per row: the largest maximum, the total
+        const int n_pre = a.prefix_len[0];
+        const bool none = bad || n_pre < 0 || n_pre > a.prefix_cap;
+        const int parts = none ? 0 : (n_pre + a.prefix_chunk - 1) / a.prefix_chunk;
+        const int64_t rows_all = all * a.n_seqs, each = partial_floats(rows_all, D);
+        auto of_all = [&](int row) { return (row_base + row / group) * a.n_heads + head * group + row % group; };
+        {
+            constexpr int L = W * 64 / (R * 16);  // lanes that take one row's parts in turn
+            const int lr = threadIdx.x / L, l = threadIdx.x % L, row = row0 + lr;
+            const float *ml = a.prefix_partial + rows_all * D + (row < rows ? of_all(row) : 0) * 2;
+            float m = l < W ? sm[(l * R * 16 + lr) * 2] : -__builtin_inff();
+            for (int s = l; s < parts; s += L) m = fmaxf(m, ml[s * each]);
+#pragma unroll
+            for (int o = 1; o < L; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+            m = m == -__builtin_inff() ? 0.0f : m;
+            float t = l < W ? __builtin_amdgcn_exp2f(sm[(l * R * 16 + lr) * 2] - m) * sm[(l * R * 16 + lr) * 2 + 1] : 0.0f;
+            for (int s = l; s < parts; s += L) t += __builtin_amdgcn_exp2f(ml[s * each] - m) * ml[s * each + 1];
+#pragma unroll
+            for (int o = 1; o < L; o <<= 1) t += __shfl_xor(t, o);
+            if (l == 0) meet[lr * 2] = m, meet[lr * 2 + 1] = t;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < R * 16 * (D / 4); i += W * 64) {
+            const int d = i % (D / 4) * 4, lr = i / (D / 4), row = row0 + lr;
+            if (row >= rows) continue;
+            const float m = meet[lr * 2], total = meet[lr * 2 + 1];
+            const int64_t at = of_all(row);
+            const float *const ml = a.prefix_partial + rows_all * D + at * 2, *const po = a.prefix_partial + at * D + d;
+            f32x4 o = {0, 0, 0, 0};
+#pragma unroll 8
+            for (int s = 0; s < parts; ++s)
+                o += __builtin_amdgcn_exp2f(ml[s * each] - m) * *(const f32x4 *)(po + s * each);
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                o += __builtin_amdgcn_exp2f(sm[(w * R * 16 + lr) * 2] - m) * *(const f32x4 *)(so + (w * R * 16 + lr) * RP + d);
+            T *dst = (T *)a.out + at * D + d;
+            const float inv = none ? __builtin_nanf("") : 1.0f / total;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dst[e] = (T)(total == 0 && !none ? 0.0f : o[e] * inv);
+        }
+        return;
+    }
     float *part = a.partial + (seq * a.max_splits + split) * partial_floats(all, D);
     for (int i = threadIdx.x; i < R * 16 * (D / 4); i += W * 64) {
         const int d = i % (D / 4) * 4, lr = i / (D / 4), row = row0 + lr;
@@ -664,7 +684,7 @@ hipError_t attend(const Kv8AttendArgs &a, hipStream_t s) {
     const int rows = a.q_len * (a.n_heads / a.cache.n_kv);
     const int tiles = (rows + 16 * R - 1) / (16 * R);
     constexpr size_t work = q_bytes(TYPE, D, R) + kPageBytes + W * (k_zone(D) + v_zone(D));
-    constexpr size_t join = (size_t)W * R * 16 * (D + 4 + 2) * 4;
+    constexpr size_t join = (size_t)R * 16 * (W * (D + 4 + 2) + 2) * 4;
     static_assert(work <= 160 * 1024 && join <= 160 * 1024, "LDS");
     const dim3 grid(a.max_splits, a.cache.n_kv * tiles, (unsigned)a.n_seqs);
     const size_t lds = work > join ? work : join;
@@ -754,9 +774,11 @@ void kv8_attend_plan(Kv8AttendArgs &a, int64_t max_len, int cus) {
     a.brief = max_len <= 512 && groups > slots;
 }
 
-void kv8_shared_plan(Kv8SharedArgs &a, int cus) {
-    kv8_attend_plan(a.prefix, 0, cus);
+void kv8_shared_plan(Kv8SharedArgs &a, int type, int cus) {
+    a.many = kv8_prefix_plan(a.prefix, type, cus);
+    if (!a.many) kv8_attend_plan(a.prefix, 0, cus);
     kv8_attend_plan(a.own, 0, cus);
+    a.own.parts = a.own.max_splits > 1;
 }
 
 static int64_t shared_bytes(const Kv8AttendArgs &a) {
@@ -764,7 +786,7 @@ static int64_t shared_bytes(const Kv8AttendArgs &a) {
 }
 
 int64_t kv8_shared_partial_bytes(const Kv8SharedArgs &a) {
-    return shared_bytes(a.prefix) + shared_bytes(a.own);
+    return shared_bytes(a.prefix) + (a.own.parts ? shared_bytes(a.own) : 0);
 }
 
 int64_t kv8_attend_partial_bytes(const Kv8AttendArgs &a) {
@@ -774,9 +796,13 @@ int64_t kv8_attend_partial_bytes(const Kv8AttendArgs &a) {
 
 hipError_t launch_kv8_attend_shared(Kv8SharedArgs &a, int type, hipStream_t s) {
     a.own.partial = a.prefix.partial + shared_bytes(a.prefix) / 4;
-    hipError_t e = launch_kv8_attend(a.prefix, type, s);
+    if (!a.own.parts) {
+        a.own.prefix_partial = a.prefix.partial, a.own.prefix_len = a.prefix.lens;
+        a.own.prefix_chunk = a.prefix.chunk, a.own.prefix_cap = (int)a.prefix.width * a.prefix.cache.page;
+    }
+    hipError_t e = a.many ? launch_kv8_prefix(a.prefix, type, s) : launch_kv8_attend(a.prefix, type, s);
     if (e == hipSuccess) e = launch_kv8_attend(a.own, type, s);
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || !a.own.parts) return e;
     const dim3 grid(a.own.q_len * a.own.n_heads, (unsigned)a.own.n_seqs);
     auto join = [&](auto t) {
         switch (a.own.cache.dim) {

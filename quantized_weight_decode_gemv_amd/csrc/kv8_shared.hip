@@ -1,0 +1,391 @@
+// Attention behind a shared prefix of the 8-bit cache: the prefix's pass over the rows of all
+// sequences at once. The sequences' own positions, and the meeting of both: kv8.hip.
+#include <algorithm>
+
+#include "attend_device.h"
+#include "kv8_device.h"
+
+namespace qwg {
+
+namespace {
+
+// Four e4m3 codes as fp16 (HALF) or bf16, exact in both.
+template <bool HALF>
+__device__ __forceinline__ u32x2 widened(uint32_t w) {
+    if constexpr (HALF)
+        return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true))};
+    else
+        return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true))};
+}
+
+// Parts of a query and of a probability: fp32 ones are three bf16s, which hold every bit.
+constexpr int parts_of(int type) { return type == kF32 ? 3 : 1; }
+
+// What a page's positions share: its number (-1: none of the pool), its scale of the scores
+// (log2 e and the call's scale in it), the exponent of its values and what that leaves out.
+struct Page {
+    int id;
+    float scale, power, rest;
+};
+
+// Exponents of values that a split's products take in: at most so far below the largest.
+constexpr int kPowers = 64;
+constexpr int kPrefixPages = kMaxPages * (int)sizeof(Page);
+
+// LDS: two blocks of keys and of values in 16 bits, the split's pages, the exponents' range, a flag.
+constexpr size_t shared_lds(int d) { return 4 * (size_t)kBlk * d * 2 + kPrefixPages + 16; }
+
+// One workgroup: one split of the prefix, one key/value head, W x 32 rows; a row is a (token of
+// any sequence, head of the group) pair. 64 positions of keys and values at a time are made 16 bits
+// wide by the workgroup together (in registers on the way from memory, a block ahead) and
+// lie in LDS for all wavefronts: each would spend as long on the conversion alone as on the
+// products. The values' transposed rows go in the order in which the second product's lanes take
+// positions: of sixteen, 0-3 and 8-11, then 4-7 and 12-15.
+//
+// S^T = K Q^T and O^T = V^T P^T as in attention over prompts: a lane's scores are the second
+// product's operand as they stand. Keys and values are codes, exact in 16 bits; with k and v the
+// scales of a position's page, q.k times k goes into the exponential and v with it: P = 2^(q.k k
+// + log2 v - M), M the running maximum of q.k k + log2 v. So P is at most one (2^8 in between) whatever
+// the pages' scales, what it loses by its rounding to fp16 (2^-11 of itself, 2^-25 of the largest) is
+// small against the row's sum, and no product overflows. The softmax's total is the sum of P / v, in fp32.
+// Where a page's v is below 2^-64 of the split's largest, P takes that in the exponent and the
+// rest after the total. fp32: queries and P as three bf16 parts, which lose nothing.
+template <int TYPE, int D, int W>
+__global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
+    typedef typename Elem<TYPE>::T T;
+    constexpr int PARTS = parts_of(TYPE);
+    constexpr bool KH = TYPE == kF16, VH = TYPE != kF32;  // keys, values and P in fp16, or bf16
+    constexpr int G = D / 8;                 // granules of a row of keys
+    constexpr int S = D / 16;                // steps of the first product
+    constexpr int DT = D / 32;               // channel tiles
+    constexpr int kTile = kBlk * D * 2;      // bytes of a block's keys (or values)
+    constexpr int N = (4 * D + W * 64 - 1) / (W * 64);  // 16-byte chunks of a block that a thread fetches
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int n = lane & 31, g = lane >> 5;
+    const Kv8 &c = a.cache;
+    const int group = a.n_heads / c.n_kv;
+    const int rows = a.q_len * group;
+    const int tiles = (rows + W * 32 - 1) / (W * 32);
+    const int head = (int)blockIdx.x % c.n_kv, at = (int)blockIdx.x / c.n_kv;
+    const int row0 = at % tiles * W * 32 + wave * 32, split = at / tiles;
+    const int shift = __builtin_ctz(c.page);
+    const int len0 = a.lens[0], cap = (int)a.width << shift;
+    const int len = len0 < 0 || len0 > cap ? 0 : len0;  // (no such length: the join's NaN)
+    const int begin = split * a.chunk, end = min(begin + a.chunk, len);
+    if (begin >= end) return;
+
+    extern __shared__ __align__(16) uint8_t lds[];
+    Page *const pages = (Page *)(lds + 4 * kTile);
+    int *const range = (int *)(lds + 4 * kTile + kPrefixPages);  // largest, smallest exponent
+    int *const dirty = range + 2;
+    if (threadIdx.x == 0) range[0] = 0, range[1] = 255, *dirty = 0;
+    __syncthreads();
+    const float to_log2 = fabsf(a.scale) * 1.4426950408889634f;
+    const int first_page = begin >> shift;
+    for (int i = threadIdx.x; i << shift < a.chunk + kBlk; i += W * 64) {
+        const int pos = (first_page + i) << shift;
+        Page e = {0, 0, 0, 127};  // past the end: any page does, its codes are masked
+        if (pos < end) {
+            const int id = a.table[first_page + i];
+            if (id < 0 || id >= c.n_pages) {
+                e.id = -1;
+            } else {
+                const int64_t p = (int64_t)id * c.n_kv + head;
+                const int v = c.v_scales[p];
+                e.id = id, e.scale = e8m0(c.k_scales[p]) * to_log2, e.rest = v;
+                if (v != 255) atomicMax(&range[0], v), atomicMin(&range[1], v);
+            }
+            if (e.id < 0 || e.rest == 255) e.scale = __builtin_nanf("");
+        }
+        pages[i] = e;
+    }
+    __syncthreads();
+    const int largest = range[0], least = max(largest - kPowers, 0);
+    const bool far = range[1] < least;
+    for (int i = threadIdx.x; i << shift < a.chunk + kBlk; i += W * 64) {
+        const int v = (int)pages[i].rest;
+        pages[i].power = max(v, least) - largest;
+        pages[i].rest = v < least ? __builtin_amdgcn_exp2f(v - least) : 1.0f;
+    }
+
+    // the row, its queries' parts, the last position that it sees
+    const bool live = row0 + n < rows;
+    const int token = live ? (row0 + n) / group : 0;
+    const int64_t out_row = (int64_t)token * a.n_heads + head * group + (row0 + n) % group;
+    u32x4 q[S][PARTS];
+    {
+        const T *p = (const T *)a.q + token * a.q_stride + (int64_t)(head * group + (row0 + n) % group) * D;
+        const bool vec = ((uintptr_t)a.q | (uintptr_t)a.q_stride * sizeof(T)) % 16 == 0;
+        const float sign = a.scale < 0 ? -1.0f : 1.0f;  // (the maximum is taken before the scale)
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            float v[8];
+            vec ? load8<T, true>(p + s * 16 + g * 8, v) : load8<T, false>(p + s * 16 + g * 8, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float v0 = v[2 * e] * sign, v1 = v[2 * e + 1] * sign;
+                if constexpr (TYPE == kF32) {
+                    uint32_t h0, m0, l0, h1, m1, l1;
+                    split3(v0, h0, m0, l0);
+                    split3(v1, h1, m1, l1);
+                    q[s][0][e] = h0 | h1 << 16, q[s][1][e] = m0 | m1 << 16, q[s][2][e] = l0 | l1 << 16;
+                } else {
+                    q[s][0][e] = pack2<KH>(v0, v1);
+                }
+            }
+        }
+    }
+    const int own = a.tails[token / a.tail_q_len] - a.tail_q_len + token % a.tail_q_len;
+    const int last = len - 1 + min(own + 1, 0);
+    // positions that every row of the workgroup sees
+    int by_all = len;
+    {
+        const int r0 = at % tiles * W * 32, s0 = r0 / group / a.tail_q_len;
+        const int s1 = min(r0 + W * 32 - 1, rows - 1) / group / a.tail_q_len;
+        for (int s = s0 + lane; s <= s1; s += 64) by_all = min(by_all, len + min(a.tails[s] - a.tail_q_len + 1, 0));
+#pragma unroll
+        for (int o = 32; o; o >>= 1) by_all = min(by_all, __shfl_xor(by_all, o));
+        by_all = __builtin_amdgcn_readfirstlane(by_all);
+    }
+    __syncthreads();
+
+    // A block ahead in registers: chunk f of the keys is sixteen channels of position f / (D/16), of the
+    // values sixteen positions (all in one page) of channel f / 4.
+    u32x4 kr[N], vr[N];
+    auto fetch = [&](int b0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int f = i * W * 64 + threadIdx.x;
+            if (4 * D % (W * 64) != 0 && f >= 4 * D) break;
+            const int kpos = b0 + f / (D / 16), vpos = b0 + f % 4 * 16;
+            const int64_t kid = max((int)pages[(kpos >> shift) - first_page].id, 0);
+            const int64_t vid = max((int)pages[(vpos >> shift) - first_page].id, 0);
+            kr[i] = *(const u32x4 *)(c.k + (((kid * c.n_kv + head) << shift) + (kpos & (c.page - 1))) * D + f % (D / 16) * 16);
+            vr[i] = *(const u32x4 *)(c.v + (((vid * c.n_kv + head) * D + f / 4) << shift) + (vpos & (c.page - 1)));
+        }
+    };
+    auto put = [&](int b0, int buf) {
+        uint8_t *const k_lds = lds + buf * 2 * kTile, *const v_lds = k_lds + kTile;
+        const bool whole = b0 + kBlk <= by_all;
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int f = i * W * 64 + threadIdx.x;
+            if (4 * D % (W * 64) != 0 && f >= 4 * D) break;
+            const int r = f / (D / 16), gr = f % (D / 16) * 2, ch = f / 4, piece = f % 4;
+            u32x4 k = kr[i], v = vr[i];
+            if (!whole) {
+                // codes past the end are whatever the pool held; a NaN that some rows do not see
+                // is left to the end
+                const int keep = min(max(len - b0 - piece * 16, 0), 16);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int x = keep - w * 4;
+                    v[w] &= x >= 4 ? ~0u : x <= 0 ? 0u : (1u << (8 * x)) - 1u;
+                    const uint32_t bad = nan_bytes(v[w]) >> 7;
+                    if (bad) v[w] &= ~(bad * 0xffu), found = true;
+                }
+            }
+            const u32x2 k0 = widened<KH>(k[0]), k1 = widened<KH>(k[1]), k2 = widened<KH>(k[2]), k3 = widened<KH>(k[3]);
+            const u32x2 v0 = widened<VH>(v[0]), v1 = widened<VH>(v[1]), v2 = widened<VH>(v[2]), v3 = widened<VH>(v[3]);
+            const int kk = row_key<G>(r), vk = row_key<8>(ch);
+            *(u32x4 *)(k_lds + (r * G + (gr ^ kk)) * 16) = u32x4{k0[0], k0[1], k1[0], k1[1]};
+            *(u32x4 *)(k_lds + (r * G + ((gr + 1) ^ kk)) * 16) = u32x4{k2[0], k2[1], k3[0], k3[1]};
+            *(u32x4 *)(v_lds + (ch * 8 + ((piece * 2) ^ vk)) * 16) = u32x4{v0[0], v0[1], v2[0], v2[1]};
+            *(u32x4 *)(v_lds + (ch * 8 + ((piece * 2 + 1) ^ vk)) * 16) = u32x4{v1[0], v1[1], v3[0], v3[1]};
+        }
+        if (found) *dirty = 1;
+    };
+
+    float top = -__builtin_inff(), sum = 0;
+    f32x16 out[DT];
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) out[t][i] = 0;
+    int v_at[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v_at[j] = (n * 8 + ((j * 2 + g) ^ row_key<8>(n))) * 16;
+
+    fetch(begin);
+    put(begin, 0);
+    if (begin + kBlk < end) fetch(begin + kBlk);
+    int buf = 0;
+    for (int b0 = begin; b0 < end; b0 += kBlk, buf ^= 1) {
+        __syncthreads();  // the block is in LDS, and nobody reads the other buffer any more
+        if (b0 + kBlk < end) put(b0 + kBlk, buf ^ 1);
+        if (b0 + 2 * kBlk < end) fetch(b0 + 2 * kBlk);
+        if (row0 >= rows) continue;
+        const uint8_t *const k_lds = lds + buf * 2 * kTile, *const v_lds = k_lds + kTile;
+        f32x16 s[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[u][i] = 0;
+            const uint8_t *const row = k_lds + (u * 32 + n) * G * 16;
+            const int key = row_key<G>(n);
+#pragma unroll
+            for (int x = 0; x < S; ++x) {
+                const u32x4 k = *(const u32x4 *)(row + ((x * 2 + g) ^ key) * 16);
+#pragma unroll
+                for (int p = PARTS - 1; p >= 0; --p) s[u] = mfma32<KH>(k, q[x][p], s[u]);
+            }
+        }
+        const bool whole = b0 + kBlk <= by_all;
+        const int hi = last - b0 - g * 4;
+        auto seen = [&](int u, int i) { return u * 32 + (i >> 2) * 8 + (i & 3) <= hi; };
+        if (!whole) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (!seen(u, i)) s[u][i] = -__builtin_inff();
+        }
+        // sixteen positions at a time, which lie in one page: this lane's eight of them
+        float scale[4], power[4], rest[4], m = -__builtin_inff();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const Page p = pages[((b0 + j * 16) >> shift) - first_page];
+            scale[j] = p.scale, power[j] = p.power, rest[j] = p.rest;
+            const f32x16 &x = s[j / 2];
+            const int i = (j & 1) * 8;
+            const float t = maximum3(maximum3(maximum3(x[i], x[i + 1], x[i + 2]), x[i + 3], x[i + 4]),
+                                     maximum3(x[i + 5], x[i + 6], x[i + 7]), x[i]);
+            const float y = t == -__builtin_inff() ? t : __builtin_fmaf(t, scale[j], power[j]);
+            m = maximum3(m, y, y);
+        }
+        m = max_halves(m);
+        if (__any(m > top + kSlack)) {  // (every number is more than -infinity)
+            const float now = fmaxf(top, m);
+            const float alpha = now == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(top - now);
+            top = now;
+            sum *= alpha;
+#pragma unroll
+            for (int t = 0; t < DT; ++t) out[t] *= alpha;
+        }
+        const float base = top == -__builtin_inff() ? 0.0f : top;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f32x16 &x = s[j / 2];
+            const int i0 = (j & 1) * 8;
+            const float less = power[j] - base;
+#pragma unroll
+            for (int i = i0; i < i0 + 8; ++i) x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], scale[j], less));
+            if (!whole) {  // (-infinity times a scale of zero, or of NaN, is none)
+#pragma unroll
+                for (int i = i0; i < i0 + 8; ++i)
+                    if (!seen(j / 2, i)) x[i] = 0;
+            }
+            const float part = ((x[i0] + x[i0 + 1]) + (x[i0 + 2] + x[i0 + 3])) + ((x[i0 + 4] + x[i0 + 5]) + (x[i0 + 6] + x[i0 + 7]));
+            sum = __builtin_fmaf(part, __builtin_amdgcn_exp2f(-power[j]), sum);
+            if (far) {
+#pragma unroll
+                for (int i = i0; i < i0 + 8; ++i) x[i] *= rest[j];
+            }
+            u32x4 w[PARTS];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float p0 = x[i0 + e * 2], p1 = x[i0 + e * 2 + 1];
+                if constexpr (TYPE == kF32) {
+                    w[0][e] = upper_halves(p0, p1);
+                    const float r0 = p0 - u2f(w[0][e] << 16), r1 = p1 - u2f(w[0][e] & 0xffff0000u);
+                    w[1][e] = upper_halves(r0, r1);
+                    w[2][e] = upper_halves(r0 - u2f(f2u(r0) & 0xffff0000u), r1 - u2f(f2u(r1) & 0xffff0000u));
+                } else {
+                    w[0][e] = pack2<VH>(p0, p1);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < DT; ++t) {
+                const u32x4 v = *(const u32x4 *)(v_lds + v_at[j] + t * 32 * 8 * 16);
+#pragma unroll
+                for (int p = PARTS - 1; p >= 0; --p) out[t] = mfma32<VH>(v, w[p], out[t]);
+            }
+        }
+    }
+    __syncthreads();
+    const bool mend = *dirty != 0;
+    const float total = sum_halves(sum);
+    if (!live) return;
+    const int64_t all = (int64_t)a.q_len * a.n_heads;
+    float *part = a.partial + split * partial_floats(all, D);
+    const float unit = e8m0(largest);  // (P's exponents count from the largest v)
+    if (g == 0) part[all * D + out_row * 2] = top, part[all * D + out_row * 2 + 1] = total;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const int d = t * 32 + i * 2 + g * 4;
+            f32x4 o = f32x4{out[t][i], out[t][i + 1], out[t][i + 2], out[t][i + 3]} * unit;
+            if (mend) {  // the NaNs of positions that some rows do not see
+                for (int pos = max(begin, by_all & -kBlk); pos <= min(last, end - 1); ++pos) {
+                    const int64_t row = ((int64_t)max(pages[(pos >> shift) - first_page].id, 0) * c.n_kv + head) * D + d;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if ((c.v[((row + e) << shift) + (pos & (c.page - 1))] & 127) == 127) o[e] = __builtin_nanf("");
+                }
+            }
+            *(f32x4 *)(part + out_row * D + d) = o;
+        }
+}
+
+template <int TYPE, int D, int W>
+hipError_t prefix(const Kv8AttendArgs &a, hipStream_t s) {
+    static_assert(shared_lds(D) <= 160 * 1024, "LDS");
+    const int64_t rows = (int64_t)a.q_len * (a.n_heads / a.cache.n_kv), tiles = (rows + W * 32 - 1) / (W * 32);
+    kv8_prefix_kernel<TYPE, D, W>
+        <<<(unsigned)(tiles * a.max_splits * a.cache.n_kv), W * 64, shared_lds(D), s>>>(a);
+    return hipGetLastError();
+}
+
+// Whether eight wavefronts' registers (256 each) hold the queries' parts and the sums.
+constexpr bool eight_fit(int type, int d) { return d * (parts_of(type) + 2) <= 640 && d < 256; }
+
+template <int TYPE, int D>
+hipError_t prefix_rows(const Kv8AttendArgs &a, hipStream_t s) {
+    if constexpr (eight_fit(TYPE, D)) {
+        if (a.row_tiles == 8) return prefix<TYPE, D, 8>(a, s);
+    }
+    return prefix<TYPE, D, 4>(a, s);
+}
+
+}  // namespace
+
+// Whether the prefix's pass takes kv8_prefix_kernel, and its splits.
+bool kv8_prefix_plan(Kv8AttendArgs &a, int type, int cus) {
+    const int64_t rows = (int64_t)a.q_len * (a.n_heads / a.cache.n_kv);
+    if (rows <= 32 || a.cache.dim * parts_of(type) > 384) return false;
+    a.row_tiles = rows > 128 && eight_fit(type, a.cache.dim) ? 8 : 4;  // wavefronts of 32 rows
+    const int64_t groups = a.cache.n_kv * ((rows + a.row_tiles * 32 - 1) / (a.row_tiles * 32));
+    const int64_t slots = a.row_tiles == 8 ? cus : 2 * cus;
+    const int64_t cap = a.width * a.cache.page;
+    int64_t chunk = (cap * groups + slots - 1) / slots;
+    chunk = std::min<int64_t>(std::max<int64_t>((chunk + kBlk - 1) / kBlk * kBlk, 256), kMaxChunk);
+    a.chunk = (int)chunk;
+    a.max_splits = (int)((cap + chunk - 1) / chunk);
+    return true;
+}
+
+hipError_t launch_kv8_prefix(const Kv8AttendArgs &a, int type, hipStream_t s) {
+    switch (a.cache.dim * 4 + type) {
+        case 64 * 4 + kF32: return prefix_rows<kF32, 64>(a, s);
+        case 64 * 4 + kF16: return prefix_rows<kF16, 64>(a, s);
+        case 64 * 4 + kBF16: return prefix_rows<kBF16, 64>(a, s);
+        case 96 * 4 + kF32: return prefix_rows<kF32, 96>(a, s);
+        case 96 * 4 + kF16: return prefix_rows<kF16, 96>(a, s);
+        case 96 * 4 + kBF16: return prefix_rows<kBF16, 96>(a, s);
+        case 128 * 4 + kF32: return prefix_rows<kF32, 128>(a, s);
+        case 128 * 4 + kF16: return prefix_rows<kF16, 128>(a, s);
+        case 128 * 4 + kBF16: return prefix_rows<kBF16, 128>(a, s);
+        case 192 * 4 + kF16: return prefix_rows<kF16, 192>(a, s);
+        case 192 * 4 + kBF16: return prefix_rows<kBF16, 192>(a, s);
+        case 256 * 4 + kF16: return prefix_rows<kF16, 256>(a, s);
+        case 256 * 4 + kBF16: return prefix_rows<kBF16, 256>(a, s);
+    }
+    return hipErrorInvalidValue;  // (kv8_prefix_plan refuses the others)
+}
+
+}  // namespace qwg

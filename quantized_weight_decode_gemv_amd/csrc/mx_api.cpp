@@ -102,15 +102,16 @@ int shared_shape(const qwg_kv8 *c, int64_t prefix_width, int64_t width, int64_t 
     return QWG_OK;
 }
 
-Kv8SharedArgs shared_of(const qwg_kv8 *cache, int64_t prefix_width, int64_t width, int64_t n_seqs,
+Kv8SharedArgs shared_of(const qwg_kv8 *cache, int type, int64_t prefix_width, int64_t width, int64_t n_seqs,
                         int q_len, int n_heads) {
     Kv8SharedArgs a = {};
     a.own.cache = cache_of(cache), a.own.width = width, a.own.n_seqs = n_seqs;
-    a.own.q_len = q_len, a.own.n_heads = n_heads, a.own.parts = true;
+    a.own.q_len = q_len, a.own.n_heads = n_heads;
     a.prefix = a.own;
+    a.prefix.parts = true;
     a.prefix.width = prefix_width, a.prefix.n_seqs = 1, a.prefix.q_len = (int)n_seqs * q_len;
     a.prefix.tail_q_len = q_len;
-    kv8_shared_plan(a, kCus);
+    kv8_shared_plan(a, type, kCus);
     return a;
 }
 
@@ -276,13 +277,14 @@ int qwg_kv8_attend(const qwg_kv8 *cache, void *out, const void *q, int type, int
     return hip_status(launch_kv8_attend(a, type, (hipStream_t)stream));
 }
 
-int64_t qwg_kv8_attend_shared_workspace(const qwg_kv8 *cache, int64_t prefix_width,
+int64_t qwg_kv8_attend_shared_workspace(const qwg_kv8 *cache, int type, int64_t prefix_width,
                                         int64_t table_width, int64_t n_seqs, int q_len,
                                         int n_heads) {
     int rc = check_cache(cache);
+    if (!rc && !known_type(type)) rc = QWG_ERR_TYPE;
     if (!rc) rc = shared_shape(cache, prefix_width, table_width, n_seqs, q_len, n_heads);
     if (rc) return -rc;
-    return kv8_shared_partial_bytes(shared_of(cache, prefix_width, table_width, n_seqs, q_len, n_heads));
+    return kv8_shared_partial_bytes(shared_of(cache, type, prefix_width, table_width, n_seqs, q_len, n_heads));
 }
 
 int qwg_kv8_attend_shared(const qwg_kv8 *cache, void *out, const void *q, int type, int64_t q_stride,
@@ -301,7 +303,7 @@ int qwg_kv8_attend_shared(const qwg_kv8 *cache, void *out, const void *q, int ty
         !aligned(prefix_len, 4) || !aligned(table, 4) || !aligned(lens, 4) ||
         !aligned(workspace, 16))
         return QWG_ERR_ALIGN;
-    Kv8SharedArgs a = shared_of(cache, prefix_width, table_width, n_seqs, q_len, n_heads);
+    Kv8SharedArgs a = shared_of(cache, type, prefix_width, table_width, n_seqs, q_len, n_heads);
     if (kv8_shared_partial_bytes(a) > workspace_bytes) return QWG_ERR_SHAPE;
     for (Kv8AttendArgs *p : {&a.prefix, &a.own}) p->q = q, p->out = out, p->q_stride = q_stride, p->scale = scale;
     a.prefix.table = prefix, a.prefix.lens = prefix_len, a.prefix.tails = lens;

@@ -82,11 +82,16 @@ struct Kv8AttendArgs {
     const int32_t *tails;  // each one's own positions, or null
     int tail_q_len;        // its query tokens
     bool parts;            // what one split sums goes to `partial` too
+    // behind a shared prefix, where a sequence's own positions are one split: what to join
+    const float *prefix_partial;  // the prefix's parts, or null
+    const int32_t *prefix_len;
+    int prefix_chunk, prefix_cap;  // positions of one of its splits, of its pages
 };
 
 // Attention behind a shared prefix: its two passes, whose parts are joined.
 struct Kv8SharedArgs {
     Kv8AttendArgs prefix, own;
+    bool many;  // rows of the prefix: kv8_prefix_kernel takes them
 };
 
 // Attention over prompts as their products give them, tokens of all sequences in a row.
@@ -114,8 +119,10 @@ bool kv8_dim_supported(int dim);
 void kv8_attend_plan(Kv8AttendArgs &a, int64_t max_len, int cus);
 int64_t kv8_attend_partial_bytes(const Kv8AttendArgs &a);
 hipError_t launch_kv8_attend(const Kv8AttendArgs &a, int type, hipStream_t s);
+bool kv8_prefix_plan(Kv8AttendArgs &a, int type, int cus);
+hipError_t launch_kv8_prefix(const Kv8AttendArgs &a, int type, hipStream_t s);
 hipError_t launch_prompt_attend(const PromptArgs &a, int type, hipStream_t s);
-void kv8_shared_plan(Kv8SharedArgs &a, int cus);
+void kv8_shared_plan(Kv8SharedArgs &a, int type, int cus);
 int64_t kv8_shared_partial_bytes(const Kv8SharedArgs &a);
 hipError_t launch_kv8_attend_shared(Kv8SharedArgs &a, int type, hipStream_t s);
 

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "attend_device.h"
 #include "mx_device.h"
 #include "mx_lds.h"
 
@@ -11,26 +12,7 @@ namespace qwg {
 
 namespace {
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-
-// Two fp32 values rounded to a 16-bit type (nearest, ties to even) in one word.
-template <int TYPE>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    if constexpr (TYPE == kF16) return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
-    else return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
-}
-
-// 32 x 32 outputs of 16 products each from two operands of eight 16-bit values a lane.
-template <int TYPE>
-__device__ __forceinline__ f32x16 mfma16(u32x4 a, u32x4 b, f32x16 c) {
-    if constexpr (TYPE == kF16)
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-}
 
 // Four positions of one channel each from a [position][channel] tile of 16-bit values: of
 // sixteen lanes, lane i gives the address of four channels of position i / 4 and takes channel i.
@@ -38,23 +20,6 @@ __device__ __forceinline__ u32x2 read_turned(const uint8_t *p) {
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                                          (__attribute__((address_space(3))) s16x4 *)p));
 }
-
-// One instruction; a NaN stays one.
-__device__ __forceinline__ float maximum3(float a, float b, float c) {
-    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
-}
-
-__device__ __forceinline__ float max_halves(float v) {
-    const auto a = __builtin_amdgcn_permlane32_swap(f2u(v), f2u(v), false, false);
-    return __builtin_elementwise_maximum(u2f(a[0]), u2f(a[1]));
-}
-
-__device__ __forceinline__ float sum_halves(float v) {
-    const auto a = __builtin_amdgcn_permlane32_swap(f2u(v), f2u(v), false, false);
-    return u2f(a[0]) + u2f(a[1]);
-}
-
-constexpr int kSlack = 8;  // a maximum may grow by this many powers of two before sums shrink
 
 // Positions of a block of keys and values in LDS.
 constexpr int block_of(int type, int d) { return type == kF32 && d > 128 ? 32 : 64; }
@@ -172,10 +137,9 @@ __global__ __launch_bounds__(W * 64, 2) void prompt_kernel(PromptArgs a) {
         }
     }
 
-    // Granule f of a tile in LDS holds granule (f % G) ^ key of row f / G: the granules that
-    // sixteen lanes read of K at once, and thirty-two of V, lie in all of the 256 bytes that LDS gives
-    // (of rows of 16 granules a multiple, of 8, and of 12).
-    auto k_key = [](int row) { return G % 16 == 0 ? row & 15 : G % 8 == 0 ? row >> 1 & 7 : row >> 2 & 3; };
+    // granule f of a tile in LDS holds granule (f % G) ^ key of row f / G; what thirty-two lanes
+    // read of V at once, 32 bytes of each of four rows twice, lies in 256 bytes too
+    auto k_key = [](int row) { return row_key<G>(row); };
     auto v_key = [](int row) {
         return TYPE == kF32 ? 0 : G % 16 == 0 ? (row & 3) * 4 : G % 8 == 0 ? (row & 3) * 2 : 0;
     };
@@ -288,7 +252,7 @@ __global__ __launch_bounds__(W * 64, 2) void prompt_kernel(PromptArgs a) {
                         for (int e = 0; e < 4; ++e)
                             s[r][u] = __builtin_amdgcn_mfma_f32_32x32x2f32(u2f(k[e]), u2f(q[r][c][e]), s[r][u], 0, 0, 0);
                     } else {
-                        s[r][u] = mfma16<TYPE>(k, q[r][c], s[r][u]);
+                        s[r][u] = mfma32<TYPE == kF16>(k, q[r][c], s[r][u]);
                     }
                 }
             }
@@ -350,7 +314,7 @@ __global__ __launch_bounds__(W * 64, 2) void prompt_kernel(PromptArgs a) {
                 for (int j = 0; j < U * 2; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        p[r][j][e] = pack2<TYPE>(s[r][j / 2][(j & 1) * 8 + e * 2], s[r][j / 2][(j & 1) * 8 + e * 2 + 1]);
+                        p[r][j][e] = pack2<TYPE == kF16>(s[r][j / 2][(j & 1) * 8 + e * 2], s[r][j / 2][(j & 1) * 8 + e * 2 + 1]);
             }
         }
         if constexpr (TYPE == kF32) {
@@ -374,7 +338,7 @@ __global__ __launch_bounds__(W * 64, 2) void prompt_kernel(PromptArgs a) {
                     const u32x2 x = read_turned(v), y = read_turned(v + 8 * G * 16);
 #pragma unroll
                     for (int r = 0; r < R; ++r)
-                        out[r][t] = mfma16<TYPE>(u32x4{x[0], x[1], y[0], y[1]}, p[r][j], out[r][t]);
+                        out[r][t] = mfma32<TYPE == kF16>(u32x4{x[0], x[1], y[0], y[1]}, p[r][j], out[r][t]);
                 }
         }
     }

@@ -44,19 +44,21 @@ def prompt(q, k, v, starts, scale, window=0):
 
 
 def shared(q, cache, prefix, prefix_len, table, lens, scale):
-    """q [seqs, q_len, heads, dim] -> as softmax_rows."""
+    """q [seqs, q_len, heads, dim] -> as softmax_rows, and the largest |v|."""
     seqs, q_len, heads, dim = q.shape
     out, weight, size = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape[:3] + (1,))
     kp, vp = cache.rows(prefix[None], 0, prefix_len)
     group = heads // kp.shape[0]
+    v_top = np.abs(vp).max(initial=0)
     for s in range(seqs):
         ko, vo = cache.rows(table, s, lens[s])
         k, v = np.concatenate([kp, ko], 1), np.concatenate([vp, vo], 1)
+        v_top = np.fmax(v_top, np.abs(vo).max(initial=0))
         n = prefix_len + lens[s]
         seen = np.arange(n) <= (n - q_len + np.arange(q_len))[:, None]
         for h in range(heads):
             out[s, :, h], weight[s, :, h], size[s, :, h, 0] = softmax_rows(q[s, :, h], k[h // group], v[h // group], seen, scale)
-    return out, weight, size
+    return out, weight, size, v_top
 
 
 def codes_of(x, slack, exponent):

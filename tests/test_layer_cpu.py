@@ -56,9 +56,9 @@ def test_shared_refuses(change, status):
     L, desc = qwg.lib(), Kv8Desc(**CACHE)
     args = {**SHARED, **change}
     assert L.qwg_kv8_attend_shared(ctypes.byref(desc), *args.values()) == status
-    size = L.qwg_kv8_attend_shared_workspace(ctypes.byref(desc), *(args[x] for x in ("prefix_width", "width", "n_seqs", "q_len", "n_heads")))
-    shape = set(change) & {"prefix_width", "width", "n_seqs", "q_len", "n_heads"}
-    assert size == -SHAPE if shape else size > 0 and size % 16 == 0
+    size = L.qwg_kv8_attend_shared_workspace(ctypes.byref(desc), *(args[x] for x in ("type", "prefix_width", "width", "n_seqs", "q_len", "n_heads")))
+    shape = set(change) & {"type", "prefix_width", "width", "n_seqs", "q_len", "n_heads"}
+    assert size == -status if shape else size > 0 and size % 16 == 0
 
 
 def test_binding_refuses_what_is_not_on_a_device():

@@ -1,7 +1,10 @@
 """Attention behind a shared prefix against plain 64-bit implementations, and the calls of a layer in a row.
 
-The bound is that of attention over the cache (test_kv8_gpu), with the rounding of a probability of the 16-bit types
-to fp16 or better: 2^-11 of it, and 2^-24 of the largest where it is below 2^-14."""
+The bound is that of attention over the cache (test_kv8_gpu), with a probability of the 16-bit types rounded to fp16: 2^-11
+of it; and where it is below 2^-14 (times its page's scale, against the largest such product of the row) 2^-25 of that
+product, each of at most 448 codes: a page's largest is over 224, so n 2^-24 of the largest |v| covers them. Over many
+outputs the two roundings add up as independent errors of at most half a step, evenly spread: a third of their
+squares."""
 import numpy as np
 import pytest
 import torch
@@ -17,7 +20,7 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 
 
-def assert_shared(out, want, weight, size, t, n, v_top):
+def assert_shared(out, want, weight, size, v_top, t, n):
     dim = want.shape[-1]
     got = out.cpu().double().numpy().reshape(want.shape)
     p = 0 if t is torch.float32 else 2.0 ** -11
@@ -25,6 +28,9 @@ def assert_shared(out, want, weight, size, t, n, v_top):
     tol = tol + torch.finfo(t).eps / 2 * np.abs(want) + (2.0 ** -25 if t is torch.float16 else 0)
     tol = tol + (0 if t is torch.float32 else 2.0 ** -24 * n * v_top)
     bad = ~(np.abs(got - want) <= tol)
+    if t is not torch.float32 and want.size > 20000:
+        half = torch.finfo(t).eps / 2
+        assert np.linalg.norm(got - want) <= ((half ** 2 + 2.0 ** -22) / 3) ** 0.5 * np.linalg.norm(want)
     assert not bad.any(), f"{bad.sum()} of {bad.size} off, first at {np.argwhere(bad)[0]}: {got[bad][0]} for {want[bad][0]}"
 
 
@@ -63,7 +69,7 @@ def test_shared_matches(t, dim, page, kv, group, q_len, prefix):
     out = attend(q, c, pre, prefix, table, lens)
     assert out.is_contiguous() and out.shape == q.shape
     want = layer_ref.shared(qd, c, pre, prefix, table, lens, dim ** -0.5)
-    assert_shared(out, *want, t, prefix + max(LENS), 20)
+    assert_shared(out, *want, t, prefix + max(LENS))
     assert torch.equal(out, attend(q, c, pre, prefix, table, lens))
 
 
@@ -78,7 +84,7 @@ def test_shared_by_many_sequences(t, dim, page, kv, group, seqs, prefix):
     q, qd = typed(rng.standard_normal((seqs, kv * group, dim)), t)
     out = attend(q, c, pre, prefix, table, lens)
     want = layer_ref.shared(qd[:, None], c, pre, prefix, table, lens, dim ** -0.5)
-    assert_shared(out, *want, t, prefix + 700, 10)
+    assert_shared(out, *want, t, prefix + 700)
 
 
 @pytest.mark.parametrize("t", TYPES)
@@ -90,9 +96,8 @@ def test_shared_is_attention_over_the_whole(t):
     out = attend(q, c, pre, 640, table, lens, scale=0.05)
     full = np.concatenate([np.repeat(pre[None, :10], 4, 0), table], 1)
     whole = qwg.kv8_attend(q, *pages(c), dev(full), dev(lens + 640), scale=0.05)
-    want = ref.attend(qd, c, full, lens + 640, 0.05)
-    assert_shared(out, *want, t, 740, 20)
-    assert_attend(whole, *want, t, 128)
+    assert_attend(whole, *ref.attend(qd, c, full, lens + 640, 0.05), t, 128)
+    assert_shared(out, *layer_ref.shared(qd, c, pre, 640, table, lens, 0.05), t, 740)
 
 
 @pytest.mark.parametrize("t", TYPES)
@@ -103,7 +108,7 @@ def test_shared_prefixes_of_no_and_of_bad_length(t):
     for n in (0, 1, 2, 40):
         out = attend(q, c, pre, n, table, lens)
         want = layer_ref.shared(qd, c, pre, n, table, lens, 0.125)
-        assert_shared(out, *want, t, 100, 20)
+        assert_shared(out, *want, t, 100)
         if n == 0:
             assert (out[1] == 0).all() and (out[3, 0] == 0).all()  # rows that see nothing
     for n in (-1, 16 * len(pre) + 1):
@@ -111,7 +116,7 @@ def test_shared_prefixes_of_no_and_of_bad_length(t):
     out = attend(q, c, pre, 40, table, [20, -1, 16 * table.shape[1] + 1, 2])
     assert torch.isnan(out[1:3]).all()
     keep = [0, 3]
-    assert_shared(out[keep], *(w[keep] for w in layer_ref.shared(qd, c, pre, 40, table, lens, 0.125)), t, 100, 20)
+    assert_shared(out[keep], *(w if np.ndim(w) == 0 else w[keep] for w in layer_ref.shared(qd, c, pre, 40, table, lens, 0.125)), t, 100)
 
 
 @pytest.mark.parametrize("t", TYPES)
@@ -127,7 +132,7 @@ def test_shared_bad_pages_and_nan_reach_the_rows_that_see_them(t, seqs):
     out = attend(q, c, pre, 100, bad, lens)
     assert torch.isnan(out[1]).all()
     keep = [s for s in range(seqs) if s != 1]
-    assert_shared(out[keep], *(w[keep] for w in want), t, 110, 20)
+    assert_shared(out[keep], *(w if np.ndim(w) == 0 else w[keep] for w in want), t, 110)
     broken = pre.copy()
     broken[2] = -1
     assert torch.isnan(attend(q, c, broken, 100, table, lens)).all()
@@ -142,7 +147,7 @@ def test_shared_bad_pages_and_nan_reach_the_rows_that_see_them(t, seqs):
     c.v[p, 0, 7, slot] = 0x30
     c.v[p, 0, :, slot + 1:], c.k[p, 0, slot + 1:] = 0x7F, 0x7F
     out = attend(q, c, pre, 100, table, lens)
-    assert_shared(out, *layer_ref.shared(qd, c, pre, 100, table, lens, 0.125), t, 110, 20)
+    assert_shared(out, *layer_ref.shared(qd, c, pre, 100, table, lens, 0.125), t, 110)
     # a NaN in one query
     q[0, 1, 1, 9] = float("nan")
     out = attend(q, c, pre, 100, table, lens).cpu()
@@ -159,10 +164,10 @@ def test_shared_pages_of_unlike_scales(t, seqs):
     at = 35  # (its page has the middle scale)
     q, qd = typed(np.repeat(ref.E4M3[c.k[pre[at // 16], 0, at % 16]][None, None] / 8, seqs, 0).repeat(2, 1), t)
     out = attend(q, c, pre, 256, table, lens, scale=0.05)
-    assert_shared(out, *layer_ref.shared(qd[:, None], c, pre, 256, table, lens, 0.05), t, 264, 0)
+    assert_shared(out, *layer_ref.shared(qd[:, None], c, pre, 256, table, lens, 0.05), t, 264)
     for scale in (1.0, 4.0):  # sharper
         out = attend(q, c, pre, 256, table, lens, scale=scale)
-        want, weight, size = layer_ref.shared(qd[:, None], c, pre, 256, table, lens, scale)
+        want, weight, size, _ = layer_ref.shared(qd[:, None], c, pre, 256, table, lens, scale)
         got = out.cpu().double().numpy().reshape(want.shape)
         tol = (np.expm1(4 * 42 * 2.0 ** -24 * size) + 2.0 ** -11 + 2.0 ** -15) * weight + torch.finfo(t).eps / 2 * np.abs(want) + 2.0 ** -25
         assert (np.abs(got - want) <= tol).all()
@@ -231,7 +236,7 @@ def test_a_prompt_and_answers_to_it(t):
         out = qwg.kv8_attend_shared(turned, *cache, dev(prefix), held, dev(table), lens)
         plain.k, plain.ks, plain.v, plain.vs = (y.cpu().numpy() for y in cache)
         rd = turned.cpu().double().numpy()[:, None]
-        assert_shared(out, *layer_ref.shared(rd, plain, prefix, n, table, [step + 1] * seqs, dim ** -0.5), t, n + step, 20)
+        assert_shared(out, *layer_ref.shared(rd, plain, prefix, n, table, [step + 1] * seqs, dim ** -0.5), t, n + step)
 
 
 def test_shared_refusals():
