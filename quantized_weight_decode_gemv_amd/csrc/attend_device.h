@@ -43,6 +43,28 @@ __device__ __forceinline__ float sum_halves(float v) {
     return u2f(a[0]) + u2f(a[1]);
 }
 
+// N products whose first operands come from LDS, `ahead` of them on the way: `read(i)` is the i-th
+// operand (READS LDS instructions), `use(i, operand)` its EACH products. The order is laid down: left to
+// itself the compiler reads each operand just before its product and waits for LDS every time.
+template <int N, int READS, int EACH, typename Read, typename Use>
+__device__ __forceinline__ void products(Read read, Use use) {
+    constexpr int A = N < 4 ? N : 4;
+    u32x4 ring[A];
+#pragma unroll
+    for (int i = 0; i < A; ++i) ring[i] = read(i);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        use(i, ring[i % A]);
+        if (i + A < N) ring[i % A] = read(i + A);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x100, A * READS, 0);  // LDS reads
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, EACH, 0);  // matrix products
+        if (i + A < N) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+    }
+}
+
 constexpr int kSlack = 8;  // a maximum may grow by this many powers of two before sums shrink
 
 // Where a row of a tile in LDS holds its 16-byte granule c: c ^ key, so that the granules that

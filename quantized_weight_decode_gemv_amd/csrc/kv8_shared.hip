@@ -1,9 +1,11 @@
 // Attention behind a shared prefix of the 8-bit cache: the prefix's pass over the rows of all
 // sequences at once. The sequences' own positions, and the meeting of both: kv8.hip.
 #include <algorithm>
+#include <type_traits>
 
 #include "attend_device.h"
 #include "kv8_device.h"
+#include "mx_lds.h"
 
 namespace qwg {
 
@@ -23,23 +25,37 @@ __device__ __forceinline__ u32x2 widened(uint32_t w) {
 // Parts of a query and of a probability: fp32 ones are three bf16s, which hold every bit.
 constexpr int parts_of(int type) { return type == kF32 ? 3 : 1; }
 
-// What a page's positions share: its number (-1: none of the pool), its scale of the scores
-// (log2 e and the call's scale in it), the exponent of its values and what that leaves out.
+// What a page's positions share: its scale of the scores (log2 e and the call's scale in it; NaN
+// where it is no page of the pool), log2 v as the products take it in and its inverse, what of v
+// that leaves out.
 struct Page {
-    int id;
-    float scale, power, rest;
+    float scale, power, inverse, rest;
 };
 
 // Exponents of values that a split's products take in: at most so far below the largest.
 constexpr int kPowers = 64;
-constexpr int kPrefixPages = kMaxPages * (int)sizeof(Page);
+// (beside a Page, where its head's keys and values begin in the pool: byte, or code, number)
+constexpr int kPrefixPages = kMaxPages * (int)(sizeof(Page) + sizeof(int64_t));
 
-// LDS: two blocks of keys and of values in 16 bits, the split's pages, the exponents' range, a flag.
-constexpr size_t shared_lds(int d) { return 4 * (size_t)kBlk * d * 2 + kPrefixPages + 16; }
+// LDS of a workgroup of W wavefronts: blocks of keys and values in 16 bits (two where they fit, and
+// then one is made while the other is used), blocks on their way from memory, pages, the
+// exponents' range, a flag. Four wavefronts of up to 128 channels leave room for a second workgroup.
+template <int D, int W>
+struct PrefixLds {
+    static constexpr int kWide = 2 * kBlk * D * 2;
+    static constexpr int kChunks = (4 * D + W * 64 - 1) / (W * 64);  // 16 bytes of K a thread, and of V
+    static constexpr int kRaw = 2 * kChunks * W * 1024;
+    static constexpr int kRest = (kPrefixPages + 31) & ~15;
+    static constexpr int kBudget = (W == 4 && D <= 128 ? 80 : 160) * 1024 - kRest;
+    static constexpr int kWides = 2 * kWide + 2 * kRaw <= kBudget ? 2 : 1;
+    static constexpr int kAhead = (kBudget - kWides * kWide) / kRaw < 4 ? (kBudget - kWides * kWide) / kRaw : 4;
+    static constexpr int kBytes = kWides * kWide + kAhead * kRaw + kRest;
+    static_assert(kAhead >= 2, "blocks on their way");
+};
 
 // One workgroup: one split of the prefix, one key/value head, W x 32 rows; a row is a (token of
 // any sequence, head of the group) pair. 64 positions of keys and values at a time are made 16 bits
-// wide by the workgroup together (in registers on the way from memory, a block ahead) and
+// wide by the workgroup together and
 // lie in LDS for all wavefronts: each would spend as long on the conversion alone as on the
 // products. The values' transposed rows go in the order in which the second product's lanes take
 // positions: of sixteen, 0-3 and 8-11, then 4-7 and 12-15.
@@ -61,7 +77,8 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
     constexpr int S = D / 16;                // steps of the first product
     constexpr int DT = D / 32;               // channel tiles
     constexpr int kTile = kBlk * D * 2;      // bytes of a block's keys (or values)
-    constexpr int N = (4 * D + W * 64 - 1) / (W * 64);  // 16-byte chunks of a block that a thread fetches
+    typedef PrefixLds<D, W> L;
+    constexpr int N = L::kChunks;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int n = lane & 31, g = lane >> 5;
@@ -78,37 +95,53 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
     if (begin >= end) return;
 
     extern __shared__ __align__(16) uint8_t lds[];
-    Page *const pages = (Page *)(lds + 4 * kTile);
-    int *const range = (int *)(lds + 4 * kTile + kPrefixPages);  // largest, smallest exponent
+    uint8_t *const raw = lds + L::kWides * L::kWide;
+    Page *const pages = (Page *)(raw + L::kAhead * L::kRaw);
+    int64_t *const places = (int64_t *)(pages + kMaxPages);
+    int *const range = (int *)(places + kMaxPages);  // largest, smallest exponent
     int *const dirty = range + 2;
     if (threadIdx.x == 0) range[0] = 0, range[1] = 255, *dirty = 0;
-    __syncthreads();
     const float to_log2 = fabsf(a.scale) * 1.4426950408889634f;
     const int first_page = begin >> shift;
     for (int i = threadIdx.x; i << shift < a.chunk + kBlk; i += W * 64) {
         const int pos = (first_page + i) << shift;
-        Page e = {0, 0, 0, 127};  // past the end: any page does, its codes are masked
-        if (pos < end) {
-            const int id = a.table[first_page + i];
-            if (id < 0 || id >= c.n_pages) {
-                e.id = -1;
-            } else {
-                const int64_t p = (int64_t)id * c.n_kv + head;
-                const int v = c.v_scales[p];
-                e.id = id, e.scale = e8m0(c.k_scales[p]) * to_log2, e.rest = v;
-                if (v != 255) atomicMax(&range[0], v), atomicMin(&range[1], v);
-            }
-            if (e.id < 0 || e.rest == 255) e.scale = __builtin_nanf("");
-        }
-        pages[i] = e;
+        int id = pos < end ? a.table[first_page + i] : 0;  // past the end: any page does, its codes are masked
+        const bool none = id < 0 || id >= c.n_pages;
+        if (none) id = 0;
+        places[i] = ((int64_t)id * c.n_kv + head) * ((int64_t)D << shift);
+        pages[i].scale = none ? __builtin_nanf("") : 0.0f;
     }
     __syncthreads();
-    const int largest = range[0], least = max(largest - kPowers, 0);
-    const bool far = range[1] < least;
+
+    // Blocks come by LDS DMA: chunk f of the keys is sixteen channels of position f / (D/16), of the
+    // values sixteen positions (all in one page) of channel f / 4. A thread makes wide what
+    // its own lane fetched.
+    auto fetch = [&](int b0, int slot) {
+        const uint32_t to = L::kWides * L::kWide + slot * L::kRaw + wave * 1024;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            // (every wavefront fetches as much: the waits count)
+            const int f = min(i * W * 64 + (int)threadIdx.x, 4 * D - 1);
+            const int kpos = b0 + f / (D / 16), vpos = b0 + f % 4 * 16;
+            const int64_t k0 = places[(kpos >> shift) - first_page], v0 = places[(vpos >> shift) - first_page];
+            dma16(c.k + k0 + ((kpos & (c.page - 1)) * D + f % (D / 16) * 16), to + i * W * 1024);
+            dma16(c.v + v0 + ((f / 4 << shift) + (vpos & (c.page - 1))), to + (N + i) * W * 1024);
+        }
+    };
+    // A block behind the last is fetched like the others, from the last one's place.
+    const int final_block = begin + (end - 1 - begin) / kBlk * kBlk;
+#pragma unroll
+    for (int i = 0; i < L::kAhead; ++i) fetch(min(begin + i * kBlk, final_block), i);
+
     for (int i = threadIdx.x; i << shift < a.chunk + kBlk; i += W * 64) {
-        const int v = (int)pages[i].rest;
-        pages[i].power = max(v, least) - largest;
-        pages[i].rest = v < least ? __builtin_amdgcn_exp2f(v - least) : 1.0f;
+        int v = 127;
+        if ((first_page + i) << shift < end && pages[i].scale == 0) {
+            const int64_t p = places[i] / ((int64_t)D << shift);
+            v = c.v_scales[p];
+            pages[i].scale = v == 255 ? __builtin_nanf("") : e8m0(c.k_scales[p]) * to_log2;
+            if (v != 255) atomicMax(&range[0], v), atomicMin(&range[1], v);
+        }
+        pages[i].rest = v;
     }
 
     // the row, its queries' parts, the last position that it sees
@@ -120,23 +153,27 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
         const T *p = (const T *)a.q + token * a.q_stride + (int64_t)(head * group + (row0 + n) % group) * D;
         const bool vec = ((uintptr_t)a.q | (uintptr_t)a.q_stride * sizeof(T)) % 16 == 0;
         const float sign = a.scale < 0 ? -1.0f : 1.0f;  // (the maximum is taken before the scale)
+        auto load = [&](auto vec) {
+            float v[S][8];
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            float v[8];
-            vec ? load8<T, true>(p + s * 16 + g * 8, v) : load8<T, false>(p + s * 16 + g * 8, v);
+            for (int s = 0; s < S; ++s) load8<T, vec.value>(p + s * 16 + g * 8, v[s]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float v0 = v[2 * e] * sign, v1 = v[2 * e + 1] * sign;
-                if constexpr (TYPE == kF32) {
-                    uint32_t h0, m0, l0, h1, m1, l1;
-                    split3(v0, h0, m0, l0);
-                    split3(v1, h1, m1, l1);
-                    q[s][0][e] = h0 | h1 << 16, q[s][1][e] = m0 | m1 << 16, q[s][2][e] = l0 | l1 << 16;
-                } else {
-                    q[s][0][e] = pack2<KH>(v0, v1);
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v0 = v[s][2 * e] * sign, v1 = v[s][2 * e + 1] * sign;
+                    if constexpr (TYPE == kF32) {
+                        uint32_t h0, m0, l0, h1, m1, l1;
+                        split3(v0, h0, m0, l0);
+                        split3(v1, h1, m1, l1);
+                        q[s][0][e] = h0 | h1 << 16, q[s][1][e] = m0 | m1 << 16, q[s][2][e] = l0 | l1 << 16;
+                    } else {
+                        q[s][0][e] = pack2<KH>(v0, v1);
+                    }
                 }
-            }
-        }
+        };
+        if (vec) load(std::true_type{});
+        else load(std::false_type{});
     }
     const int own = a.tails[token / a.tail_q_len] - a.tail_q_len + token % a.tail_q_len;
     const int last = len - 1 + min(own + 1, 0);
@@ -151,24 +188,18 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
         by_all = __builtin_amdgcn_readfirstlane(by_all);
     }
     __syncthreads();
+    const int largest = range[0], least = max(largest - kPowers, 0);
+    const bool far = range[1] < least;
+    for (int i = threadIdx.x; i << shift < a.chunk + kBlk; i += W * 64) {
+        const int v = (int)pages[i].rest;
+        pages[i].power = max(v, least) - largest;
+        pages[i].inverse = __builtin_amdgcn_exp2f(largest - max(v, least));
+        pages[i].rest = v < least ? __builtin_amdgcn_exp2f(v - least) : 1.0f;
+    }
 
-    // A block ahead in registers: chunk f of the keys is sixteen channels of position f / (D/16), of the
-    // values sixteen positions (all in one page) of channel f / 4.
-    u32x4 kr[N], vr[N];
-    auto fetch = [&](int b0) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int f = i * W * 64 + threadIdx.x;
-            if (4 * D % (W * 64) != 0 && f >= 4 * D) break;
-            const int kpos = b0 + f / (D / 16), vpos = b0 + f % 4 * 16;
-            const int64_t kid = max((int)pages[(kpos >> shift) - first_page].id, 0);
-            const int64_t vid = max((int)pages[(vpos >> shift) - first_page].id, 0);
-            kr[i] = *(const u32x4 *)(c.k + (((kid * c.n_kv + head) << shift) + (kpos & (c.page - 1))) * D + f % (D / 16) * 16);
-            vr[i] = *(const u32x4 *)(c.v + (((vid * c.n_kv + head) * D + f / 4) << shift) + (vpos & (c.page - 1)));
-        }
-    };
-    auto put = [&](int b0, int buf) {
-        uint8_t *const k_lds = lds + buf * 2 * kTile, *const v_lds = k_lds + kTile;
+    auto put = [&](int b0, int slot, int buf) {
+        uint8_t *const k_lds = lds + buf * L::kWide, *const v_lds = k_lds + kTile;
+        const uint8_t *const from = raw + slot * L::kRaw + threadIdx.x * 16;
         const bool whole = b0 + kBlk <= by_all;
         bool found = false;
 #pragma unroll
@@ -176,7 +207,7 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
             const int f = i * W * 64 + threadIdx.x;
             if (4 * D % (W * 64) != 0 && f >= 4 * D) break;
             const int r = f / (D / 16), gr = f % (D / 16) * 2, ch = f / 4, piece = f % 4;
-            u32x4 k = kr[i], v = vr[i];
+            u32x4 k = *(const u32x4 *)(from + i * W * 1024), v = *(const u32x4 *)(from + (N + i) * W * 1024);
             if (!whole) {
                 // codes past the end are whatever the pool held; a NaN that some rows do not see
                 // is left to the end
@@ -210,29 +241,51 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) v_at[j] = (n * 8 + ((j * 2 + g) ^ row_key<8>(n))) * 16;
 
-    fetch(begin);
-    put(begin, 0);
-    if (begin + kBlk < end) fetch(begin + kBlk);
-    int buf = 0;
-    for (int b0 = begin; b0 < end; b0 += kBlk, buf ^= 1) {
-        __syncthreads();  // the block is in LDS, and nobody reads the other buffer any more
-        if (b0 + kBlk < end) put(b0 + kBlk, buf ^ 1);
-        if (b0 + 2 * kBlk < end) fetch(b0 + 2 * kBlk);
-        if (row0 >= rows) continue;
-        const uint8_t *const k_lds = lds + buf * 2 * kTile, *const v_lds = k_lds + kTile;
+    // the oldest of the blocks under way has arrived when 2 N (kAhead - 1) younger DMAs may be left
+    auto make = [&](int b0, int slot, int buf) {
+        wait_vmcnt<2 * N * (L::kAhead - 1)>();
+        put(b0, slot, buf);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // it has been read: its place is free
+        fetch(min(b0 + L::kAhead * kBlk, final_block), slot);
+    };
+    if (L::kWides == 2) {
+        __syncthreads();  // (the pages' powers)
+        make(begin, 0, 0);
+    }
+    // Of eight wavefronts, two to a SIMD, one makes its part of the next block before its products
+    // and one after them, so that they want the matrix cores and the vector units in turn.
+    const bool early = true;
+    int buf = 0, slot = L::kWides == 2 ? 1 : 0;
+    for (int b0 = begin; b0 < end; b0 += kBlk, slot = slot + 1 == L::kAhead ? 0 : slot + 1) {
+        __syncthreads();  // the block is made (of two), and nobody reads the one before any more
+        const uint8_t *const k_lds = lds + buf * L::kWide, *const v_lds = k_lds + kTile;
+        const bool more = L::kWides == 2 && b0 + kBlk < end;
+        if (L::kWides == 2) {
+            buf ^= 1;
+            if (more && early) make(b0 + kBlk, slot, buf);
+        } else {
+            make(b0, slot, 0);
+            __syncthreads();
+        }
+        if (row0 >= rows) {
+            if (more && !early) make(b0 + kBlk, slot, buf);
+            continue;
+        }
         f32x16 s[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[u][i] = 0;
-            const uint8_t *const row = k_lds + (u * 32 + n) * G * 16;
+        {
+            const uint8_t *const row = k_lds + n * G * 16;
             const int key = row_key<G>(n);
+            // both halves' operands of a step in turn: two chains of sums
+            products<2 * S, 1, PARTS>(
+                [&](int i) { return *(const u32x4 *)(row + i % 2 * 32 * G * 16 + ((i / 2 * 2 + g) ^ key) * 16); },
+                [&](int i, u32x4 k) {
 #pragma unroll
-            for (int x = 0; x < S; ++x) {
-                const u32x4 k = *(const u32x4 *)(row + ((x * 2 + g) ^ key) * 16);
-#pragma unroll
-                for (int p = PARTS - 1; p >= 0; --p) s[u] = mfma32<KH>(k, q[x][p], s[u]);
-            }
+                    for (int p = PARTS - 1; p >= 0; --p) s[i % 2] = mfma32<KH>(k, q[i / 2][p], s[i % 2]);
+                });
         }
         const bool whole = b0 + kBlk <= by_all;
         const int hi = last - b0 - g * 4;
@@ -244,17 +297,17 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
                 for (int i = 0; i < 16; ++i)
                     if (!seen(u, i)) s[u][i] = -__builtin_inff();
         }
-        // sixteen positions at a time, which lie in one page: this lane's eight of them
-        float scale[4], power[4], rest[4], m = -__builtin_inff();
+        // sixteen positions at a time lie in one page: this lane's eight of them
+        Page page[4];
+        float m = -__builtin_inff();
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const Page p = pages[((b0 + j * 16) >> shift) - first_page];
-            scale[j] = p.scale, power[j] = p.power, rest[j] = p.rest;
+            page[j] = pages[((b0 + j * 16) >> shift) - first_page];
             const f32x16 &x = s[j / 2];
             const int i = (j & 1) * 8;
             const float t = maximum3(maximum3(maximum3(x[i], x[i + 1], x[i + 2]), x[i + 3], x[i + 4]),
                                      maximum3(x[i + 5], x[i + 6], x[i + 7]), x[i]);
-            const float y = t == -__builtin_inff() ? t : __builtin_fmaf(t, scale[j], power[j]);
+            const float y = t == -__builtin_inff() ? t : __builtin_fmaf(t, page[j].scale, page[j].power);
             m = maximum3(m, y, y);
         }
         m = max_halves(m);
@@ -268,44 +321,50 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
         }
         const float base = top == -__builtin_inff() ? 0.0f : top;
 #pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float x = __builtin_fmaf(s[i / 16][i % 16], page[i / 8].scale, page[i / 8].power - base);
+            s[i / 16][i % 16] = __builtin_amdgcn_exp2f(x);
+        }
+        if (!whole) {  // (-infinity times a scale of zero, or of NaN, is none)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (!seen(i / 16, i % 16)) s[i / 16][i % 16] = 0;
+        }
+#pragma unroll
         for (int j = 0; j < 4; ++j) {
-            f32x16 &x = s[j / 2];
-            const int i0 = (j & 1) * 8;
-            const float less = power[j] - base;
+            const f32x16 &x = s[j / 2];
+            const int i = (j & 1) * 8;
+            const float part = ((x[i] + x[i + 1]) + (x[i + 2] + x[i + 3])) + ((x[i + 4] + x[i + 5]) + (x[i + 6] + x[i + 7]));
+            sum = __builtin_fmaf(part, page[j].inverse, sum);
+        }
+        if (far) {
 #pragma unroll
-            for (int i = i0; i < i0 + 8; ++i) x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], scale[j], less));
-            if (!whole) {  // (-infinity times a scale of zero, or of NaN, is none)
+            for (int i = 0; i < 32; ++i) s[i / 16][i % 16] *= page[i / 8].rest;
+        }
+        u32x4 w[4][PARTS];
 #pragma unroll
-                for (int i = i0; i < i0 + 8; ++i)
-                    if (!seen(j / 2, i)) x[i] = 0;
-            }
-            const float part = ((x[i0] + x[i0 + 1]) + (x[i0 + 2] + x[i0 + 3])) + ((x[i0 + 4] + x[i0 + 5]) + (x[i0 + 6] + x[i0 + 7]));
-            sum = __builtin_fmaf(part, __builtin_amdgcn_exp2f(-power[j]), sum);
-            if (far) {
-#pragma unroll
-                for (int i = i0; i < i0 + 8; ++i) x[i] *= rest[j];
-            }
-            u32x4 w[PARTS];
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float p0 = x[i0 + e * 2], p1 = x[i0 + e * 2 + 1];
+                const float p0 = s[j / 2][(j & 1) * 8 + e * 2], p1 = s[j / 2][(j & 1) * 8 + e * 2 + 1];
                 if constexpr (TYPE == kF32) {
-                    w[0][e] = upper_halves(p0, p1);
-                    const float r0 = p0 - u2f(w[0][e] << 16), r1 = p1 - u2f(w[0][e] & 0xffff0000u);
-                    w[1][e] = upper_halves(r0, r1);
-                    w[2][e] = upper_halves(r0 - u2f(f2u(r0) & 0xffff0000u), r1 - u2f(f2u(r1) & 0xffff0000u));
+                    w[j][0][e] = upper_halves(p0, p1);
+                    const float r0 = p0 - u2f(w[j][0][e] << 16), r1 = p1 - u2f(w[j][0][e] & 0xffff0000u);
+                    w[j][1][e] = upper_halves(r0, r1);
+                    w[j][2][e] = upper_halves(r0 - u2f(f2u(r0) & 0xffff0000u), r1 - u2f(f2u(r1) & 0xffff0000u));
                 } else {
-                    w[0][e] = pack2<VH>(p0, p1);
+                    w[j][0][e] = pack2<VH>(p0, p1);
                 }
             }
+        products<4 * DT, 1, PARTS>(
+            [&](int i) { return *(const u32x4 *)(v_lds + v_at[i / DT] + i % DT * 32 * 8 * 16); },
+            [&](int i, u32x4 v) {
 #pragma unroll
-            for (int t = 0; t < DT; ++t) {
-                const u32x4 v = *(const u32x4 *)(v_lds + v_at[j] + t * 32 * 8 * 16);
-#pragma unroll
-                for (int p = PARTS - 1; p >= 0; --p) out[t] = mfma32<VH>(v, w[p], out[t]);
-            }
-        }
+                for (int p = PARTS - 1; p >= 0; --p) out[i % DT] = mfma32<VH>(v, w[i / DT][p], out[i % DT]);
+            });
+        if (more && !early) make(b0 + kBlk, slot, buf);
     }
+    wait_vmcnt<0>();  // (no DMA outlives its workgroup's LDS)
     __syncthreads();
     const bool mend = *dirty != 0;
     const float total = sum_halves(sum);
@@ -322,10 +381,10 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
             f32x4 o = f32x4{out[t][i], out[t][i + 1], out[t][i + 2], out[t][i + 3]} * unit;
             if (mend) {  // the NaNs of positions that some rows do not see
                 for (int pos = max(begin, by_all & -kBlk); pos <= min(last, end - 1); ++pos) {
-                    const int64_t row = ((int64_t)max(pages[(pos >> shift) - first_page].id, 0) * c.n_kv + head) * D + d;
+                    const uint8_t *codes = c.v + places[(pos >> shift) - first_page] + (pos & (c.page - 1));
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if ((c.v[((row + e) << shift) + (pos & (c.page - 1))] & 127) == 127) o[e] = __builtin_nanf("");
+                        if ((codes[(int64_t)(d + e) << shift] & 127) == 127) o[e] = __builtin_nanf("");
                 }
             }
             *(f32x4 *)(part + out_row * D + d) = o;
@@ -334,15 +393,14 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
 
 template <int TYPE, int D, int W>
 hipError_t prefix(const Kv8AttendArgs &a, hipStream_t s) {
-    static_assert(shared_lds(D) <= 160 * 1024, "LDS");
     const int64_t rows = (int64_t)a.q_len * (a.n_heads / a.cache.n_kv), tiles = (rows + W * 32 - 1) / (W * 32);
     kv8_prefix_kernel<TYPE, D, W>
-        <<<(unsigned)(tiles * a.max_splits * a.cache.n_kv), W * 64, shared_lds(D), s>>>(a);
+        <<<(unsigned)(tiles * a.max_splits * a.cache.n_kv), W * 64, PrefixLds<D, W>::kBytes, s>>>(a);
     return hipGetLastError();
 }
 
 // Whether eight wavefronts' registers (256 each) hold the queries' parts and the sums.
-constexpr bool eight_fit(int type, int d) { return d * (parts_of(type) + 2) <= 640 && d < 256; }
+constexpr bool eight_fit(int type, int d) { return d * (parts_of(type) + 2) <= 512; }
 
 template <int TYPE, int D>
 hipError_t prefix_rows(const Kv8AttendArgs &a, hipStream_t s) {

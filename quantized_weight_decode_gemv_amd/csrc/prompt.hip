@@ -238,24 +238,25 @@ __global__ __launch_bounds__(W * 64, 2) void prompt_kernel(PromptArgs a) {
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[r][u][i] = 0;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint8_t *const row = k_lds + (u * 32 + n) * G * 16;
+        {
+            const uint8_t *const row = k_lds + n * G * 16;
             const int key = k_key(n);
+            // the tiles' operands of a step in turn: a chain of sums each
+            products<U * G / 2, 1, R * (TYPE == kF32 ? 4 : 1)>(
+                [&](int i) { return *(const u32x4 *)(row + i % U * 32 * G * 16 + ((i / U * 2 + g) ^ key) * 16); },
+                [&](int i, u32x4 k) {
 #pragma unroll
-            for (int c = 0; c < G / 2; ++c) {
-                const u32x4 k = *(const u32x4 *)(row + ((c * 2 + g) ^ key) * 16);
+                    for (int r = 0; r < R; ++r) {
+                        f32x16 &x = s[r][i % U];
+                        if constexpr (TYPE == kF32) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    if constexpr (TYPE == kF32) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            s[r][u] = __builtin_amdgcn_mfma_f32_32x32x2f32(u2f(k[e]), u2f(q[r][c][e]), s[r][u], 0, 0, 0);
-                    } else {
-                        s[r][u] = mfma32<TYPE == kF16>(k, q[r][c], s[r][u]);
+                            for (int e = 0; e < 4; ++e)
+                                x = __builtin_amdgcn_mfma_f32_32x32x2f32(u2f(k[e]), u2f(q[r][i / U][e]), x, 0, 0, 0);
+                        } else {
+                            x = mfma32<TYPE == kF16>(k, q[r][i / U], x);
+                        }
                     }
-                }
-            }
+                });
         }
         u32x4 p[R][TYPE == kF32 ? 1 : U * 2];
         const bool clear = whole(b0, w_lo, w_hi);
@@ -330,16 +331,17 @@ __global__ __launch_bounds__(W * 64, 2) void prompt_kernel(PromptArgs a) {
                             out[r][t] = __builtin_amdgcn_mfma_f32_32x32x2f32(row[t * 32 + n], s[r][u][i], out[r][t], 0, 0, 0);
                 }
         } else {
-#pragma unroll
-            for (int j = 0; j < U * 2; ++j)
-#pragma unroll
-                for (int t = 0; t < DT; ++t) {
-                    const uint8_t *v = v_lds + v_at[t] + j * 16 * G * 16;
+            products<U * 2 * DT, 2, R>(
+                [&](int i) {
+                    const uint8_t *v = v_lds + v_at[i % DT] + i / DT * 16 * G * 16;
                     const u32x2 x = read_turned(v), y = read_turned(v + 8 * G * 16);
+                    return u32x4{x[0], x[1], y[0], y[1]};
+                },
+                [&](int i, u32x4 v) {
 #pragma unroll
                     for (int r = 0; r < R; ++r)
-                        out[r][t] = mfma32<TYPE == kF16>(u32x4{x[0], x[1], y[0], y[1]}, p[r][j], out[r][t]);
-                }
+                        out[r][i % DT] = mfma32<TYPE == kF16>(v, p[r][i / DT], out[r][i % DT]);
+                });
         }
     }
 
