@@ -110,7 +110,8 @@ __global__ __launch_bounds__(W * 64, 2) void prompt_kernel(PromptArgs a) {
 
     // queries: the B operand's lane takes row n, eight channels (four of fp32) per half
     const bool flip = a.scale < 0;  // the maximum is taken before the scale
-    const float to_log2 = fabsf(a.scale) * 1.4426950408889634f;
+    // (never zero: -infinity, of what is masked, has to stay what it is)
+    const float to_log2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 0x1p-126f);
     u32x4 q[R][G / 2];
     int token[R];
 #pragma unroll
@@ -145,39 +146,41 @@ __global__ __launch_bounds__(W * 64, 2) void prompt_kernel(PromptArgs a) {
     };
     const T *const kp = (const T *)a.k + first * a.k_stride + (int64_t)head * D;
     const T *const vp = (const T *)a.v + first * a.v_stride + (int64_t)head * D;
-    // a wavefront's DMAs of a block: byte offsets from the block's first key and value
+    // A wavefront's DMAs of a block. Where they lie whole 16 rows apart, and so their granules' keys
+    // are the same, one offset serves all of them.
     constexpr int N = (B * G / 64 + W - 1) / W;
-    uint32_t k_off[N], v_off[N];
-    auto offsets = [&](int last) {  // last: the block's last position, or the sequence's
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int f = (i * W + wave) * 64 + lane, row = f / G, c = f - row * G;
-            const uint32_t pos = min(row, last);  // past the end: masked
-            k_off[i] = (pos * (uint32_t)a.k_stride + (c ^ k_key(row)) * E) * sizeof(T);
-            v_off[i] = (pos * (uint32_t)a.v_stride + (c ^ v_key(row)) * E) * sizeof(T);
-        }
+    constexpr bool kEven = W * 64 % G == 0 && W * 64 / G % 16 == 0;
+    auto offset = [&](int i, bool of_v, int last) {  // last: the block's last position, or the sequence's
+        const int f = (i * W + wave) * 64 + lane, row = f / G, c = f - row * G;
+        const uint32_t pos = min(row, last);  // past the end: masked
+        return (pos * (uint32_t)(of_v ? a.v_stride : a.k_stride) + (c ^ (of_v ? v_key(row) : k_key(row))) * E) * (uint32_t)sizeof(T);
     };
-    offsets(B - 1);
-    auto issue = [&](int b0, int buf) {
-        const uint32_t to = buf * 2 * kTile + wave * 1024;
-        const T *const k0 = kp + b0 * a.k_stride, *const v0 = vp + b0 * a.v_stride;
-        if (b0 + B > len) offsets(len - 1 - b0);
+    uint32_t k_off[kEven ? 1 : N], v_off[kEven ? 1 : N];
+#pragma unroll
+    for (int i = 0; i < (kEven ? 1 : N); ++i) k_off[i] = offset(i, false, B), v_off[i] = offset(i, true, B);
+    auto fetch = [&](bool of_v, int b0, uint32_t to) {
+        const int64_t stride = of_v ? a.v_stride : a.k_stride;
+        const T *const p0 = (of_v ? vp : kp) + b0 * stride;
+        to += wave * 1024;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             if (B * G / 64 % W != 0 && i * W + wave >= B * G / 64) break;
+            const bool whole = b0 + B <= len;
+            const T *const p = kEven && whole ? p0 + i * (W * 64 / G) * stride : p0;
+            const uint32_t off = whole ? (of_v ? v_off : k_off)[kEven ? 0 : i] : offset(i, of_v, len - 1 - b0);
             if (a.vec) {
-                dma16(k0, k_off[i], to + i * W * 1024);
-                dma16(v0, v_off[i], to + kTile + i * W * 1024);
+                dma16(p, off, to + i * W * 1024);
             } else {
-                T x[E], y[E];
+                T x[E];
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    x[e] = k0[k_off[i] / sizeof(T) + e], y[e] = v0[v_off[i] / sizeof(T) + e];
+                for (int e = 0; e < E; ++e) x[e] = p[off / sizeof(T) + e];
                 __builtin_memcpy(lds + to + i * W * 1024 + lane * 16, x, 16);
-                __builtin_memcpy(lds + to + kTile + i * W * 1024 + lane * 16, y, 16);
             }
         }
     };
+    // a block of keys, or of values, into the first or second of its two places
+    auto issue_k = [&](int b0, int buf) { fetch(false, b0, buf * 2 * kTile); };
+    auto issue_v = [&](int b0, int buf) { fetch(true, b0, buf * 2 * kTile + kTile); };
 
     float top[R], sum[R];  // maximum times to_log2, sum of this half lane's probabilities
     f32x16 out[R][DT];
@@ -194,121 +197,132 @@ __global__ __launch_bounds__(W * 64, 2) void prompt_kernel(PromptArgs a) {
     // whether every one of the tokens from lo to hi sees the whole block
     auto whole = [&](int b0, int lo, int hi) { return b0 + B - 1 <= lo && (window == 0 || b0 > hi - window); };
 
-    // what a lane reads of V first: four channels of the position of its quarter
-    int v_at[DT];
-#pragma unroll
-    for (int t = 0; t < DT; ++t) {
-        const int row = g * 4 + (n >> 2 & 3), granule = t * 4 + (n >> 4) * 2 + (n >> 1 & 1);
-        v_at[t] = (row * G + (granule ^ v_key(row))) * 16 + (n & 1) * 8;
-    }
+    // Where a lane reads a tile: of K granule g of row n, of V (the first) four channels of the position
+    // of its quarter. The granules of other steps and channel tiles lie an exclusive or away.
+    const int v_row = g * 4 + (n >> 2 & 3);
+    const int k_at = (n * G + (g ^ k_key(n))) * 16;
+    const int v_at = (v_row * G + (((n >> 4) * 2 + (n >> 1 & 1)) ^ v_key(v_row))) * 16 + (n & 1) * 8;
+    auto key = [&](const uint8_t *k_lds, int i) {  // the i-th operand of the first product: tile i % U, step i / U
+        const int c = i / U * 2;
+        const int at = G % 16 == 0 && c < 16 ? k_at ^ c * 16 : (n * G + ((c + g) ^ k_key(n))) * 16;
+        return *(const u32x4 *)(k_lds + at + i % U * 32 * G * 16);
+    };
+    auto value = [&](const uint8_t *v_lds, int i) {  // of the second: step i / DT, channel tile i % DT
+        const int c = i % DT * 4;
+        const int at = G % 16 == 0 && c < 16 ? v_at ^ c * 16
+                                             : (v_row * G + ((c + (n >> 4) * 2 + (n >> 1 & 1)) ^ v_key(v_row))) * 16 + (n & 1) * 8;
+        const uint8_t *v = v_lds + at + i / DT * 16 * G * 16;
+        const u32x2 x = read_turned(v), y = read_turned(v + 8 * G * 16);
+        return u32x4{x[0], x[1], y[0], y[1]};
+    };
 
-    issue(low, 0);
-    int buf = 0;
-    for (int b0 = low; b0 <= t_hi; b0 += B, buf ^= 1) {
-        wait_vmcnt<0>();
-        __syncthreads();
-        if (b0 + B <= t_hi) issue(b0 + B, buf ^ 1);
-        uint8_t *const k_lds = lds + buf * 2 * kTile, *const v_lds = k_lds + kTile;
-        if (!whole(b0, t_lo, t_hi)) {
-            bool found = false;
-            for (int f = threadIdx.x; f < B * G; f += W * 64) {
-                u32x4 w = *(u32x4 *)(v_lds + f * 16);
-                bool here = false;
+    // infinities and NaNs of a block of values that some row does not see all of: to zero
+    auto clean = [&](uint8_t *v_lds) {
+        bool found = false;
+        for (int f = threadIdx.x; f < B * G; f += W * 64) {
+            u32x4 w = *(u32x4 *)(v_lds + f * 16);
+            bool here = false;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    constexpr uint32_t x = TYPE == kF32 ? 0x7f800000u : TYPE == kF16 ? 0x7c00u : 0x7f80u;
-                    if constexpr (TYPE == kF32) {
-                        if ((w[e] & x) == x) w[e] = 0, here = true;
-                    } else {
-                        if ((w[e] & x) == x) w[e] &= 0xffff0000u, here = true;
-                        if ((w[e] >> 16 & x) == x) w[e] &= 0xffffu, here = true;
-                    }
+            for (int e = 0; e < 4; ++e) {
+                constexpr uint32_t x = TYPE == kF32 ? 0x7f800000u : TYPE == kF16 ? 0x7c00u : 0x7f80u;
+                if constexpr (TYPE == kF32) {
+                    if ((w[e] & x) == x) w[e] = 0, here = true;
+                } else {
+                    if ((w[e] & x) == x) w[e] &= 0xffff0000u, here = true;
+                    if ((w[e] >> 16 & x) == x) w[e] &= 0xffffu, here = true;
                 }
-                if (here) *(u32x4 *)(v_lds + f * 16) = w, found = true;
             }
-            if (found) *dirty = 1;
-            __syncthreads();
+            if (here) *(u32x4 *)(v_lds + f * 16) = w, found = true;
         }
-        if (idle || b0 > w_hi || (window > 0 && b0 + B - 1 <= w_lo - window)) continue;
-
-        f32x16 s[R][U];
+        if (found) *dirty = 1;
+        __syncthreads();
+    };
+    auto scores = [&](f32x16 (&s)[R][U], const uint8_t *k_lds) {
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[r][u][i] = 0;
-        {
-            const uint8_t *const row = k_lds + n * G * 16;
-            const int key = k_key(n);
-            // the tiles' operands of a step in turn: a chain of sums each
-            products<U * G / 2, 1, R * (TYPE == kF32 ? 4 : 1)>(
-                [&](int i) { return *(const u32x4 *)(row + i % U * 32 * G * 16 + ((i / U * 2 + g) ^ key) * 16); },
-                [&](int i, u32x4 k) {
+        // the tiles' operands of a step in turn: a chain of sums each
+        products<U * G / 2, 1, R * (TYPE == kF32 ? 4 : 1)>(
+            [&](int i) { return key(k_lds, i); },
+            [&](int i, u32x4 k) {
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        f32x16 &x = s[r][i % U];
-                        if constexpr (TYPE == kF32) {
+                for (int r = 0; r < R; ++r) {
+                    f32x16 &x = s[r][i % U];
+                    if constexpr (TYPE == kF32) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                x = __builtin_amdgcn_mfma_f32_32x32x2f32(u2f(k[e]), u2f(q[r][i / U][e]), x, 0, 0, 0);
-                        } else {
-                            x = mfma32<TYPE == kF16>(k, q[r][i / U], x);
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            x = __builtin_amdgcn_mfma_f32_32x32x2f32(u2f(k[e]), u2f(q[r][i / U][e]), x, 0, 0, 0);
+                    } else {
+                        x = mfma32<TYPE == kF16>(k, q[r][i / U], x);
                     }
-                });
+                }
+            });
+    };
+    // what a row does not see becomes -infinity
+    auto mask = [&](int r, f32x16 (&s)[U], int b0) {
+        // the positions that the lane's row sees, from the lane's first of the block
+        const int hi = token[r] - b0 - g * 4, lo = window > 0 ? hi - window : -1;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int pos = u * 32 + (i >> 2) * 8 + (i & 3);
+                if (pos > hi || pos <= lo) s[u][i] = -__builtin_inff();
+            }
+    };
+    float base[R];  // what the exponents are taken from: the maximum, or zero before there is one
+    // takes a block's largest scores in: where one is far above the maximum so far, what was summed shrinks
+    auto raise = [&](int r, float largest) {
+        const float t = max_halves(largest);
+        const float scaled = t == -__builtin_inff() ? t : t * to_log2;
+        if (__any(scaled > top[r] + kSlack)) {  // (every number is more than -infinity)
+            const float now = fmaxf(top[r], scaled);
+            const float alpha = now == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(top[r] - now);
+            top[r] = now;
+            sum[r] *= alpha;
+#pragma unroll
+            for (int t = 0; t < DT; ++t) out[r][t] *= alpha;
         }
+        base[r] = top[r] == -__builtin_inff() ? 0.0f : top[r];
+    };
+    auto largest = [&](const f32x16 (&s)[U]) {
+        float m[2] = {-__builtin_inff(), -__builtin_inff()};
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) m[i >> 1 & 1] = maximum3(m[i >> 1 & 1], s[u][i], s[u][i + 1]);
+        return maximum3(m[0], m[1], m[1]);
+    };
+    auto weight = [&](float s, int r) { return __builtin_amdgcn_exp2f(__builtin_fmaf(s, to_log2, -base[r])); };
+
+    f32x16 s[R][U];
+    issue_k(low, 0);
+    issue_v(low, 0);
+    int buf = 0;
+    for (int b0 = low; b0 <= t_hi; b0 += B, buf ^= 1) {
+        wait_vmcnt<0>();
+        __syncthreads();
+        if (b0 + B <= t_hi) issue_k(b0 + B, buf ^ 1), issue_v(b0 + B, buf ^ 1);
+        uint8_t *const k_lds = lds + buf * 2 * kTile, *const v_lds = k_lds + kTile;
+        if (!whole(b0, t_lo, t_hi)) clean(v_lds);
+        if (idle || b0 > w_hi || (window > 0 && b0 + B - 1 <= w_lo - window)) continue;
+        scores(s, k_lds);
         u32x4 p[R][TYPE == kF32 ? 1 : U * 2];
-        const bool clear = whole(b0, w_lo, w_hi);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            // the positions that the lane's row sees, from the lane's first of the block
-            const int hi = token[r] - b0 - g * 4, lo = window > 0 ? hi - window : -1;
-            auto seen = [&](int u, int i) {
-                const int pos = u * 32 + (i >> 2) * 8 + (i & 3);
-                return pos <= hi && pos > lo;
-            };
-            if (!clear) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (!seen(u, i)) s[r][u][i] = -__builtin_inff();
-            }
-            float m[2] = {-__builtin_inff(), -__builtin_inff()};
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < 16; i += 2)
-                    m[i >> 1 & 1] = maximum3(m[i >> 1 & 1], s[r][u][i], s[r][u][i + 1]);
-            const float t = max_halves(maximum3(m[0], m[1], m[1]));
-            const float scaled = t == -__builtin_inff() ? t : t * to_log2;
-            if (__any(scaled > top[r] + kSlack)) {  // (every number is more than -infinity)
-                const float now = fmaxf(top[r], scaled);
-                const float alpha = now == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(top[r] - now);
-                top[r] = now;
-                sum[r] *= alpha;
-#pragma unroll
-                for (int t = 0; t < DT; ++t) out[r][t] *= alpha;
-            }
-            const float base = top[r] == -__builtin_inff() ? 0.0f : top[r];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    s[r][u][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][u][i], to_log2, -base));
-            if (!clear) {  // (-infinity times a scale of zero is none)
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (!seen(u, i)) s[r][u][i] = 0;
-            }
+            if (!whole(b0, w_lo, w_hi)) mask(r, s[r], b0);
+            raise(r, largest(s[r]));
             float part[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) part[i & 3] += s[r][u][i];
+                for (int i = 0; i < 16; ++i) {
+                    s[r][u][i] = weight(s[r][u][i], r);
+                    part[i & 3] += s[r][u][i];
+                }
             sum[r] += (part[0] + part[1]) + (part[2] + part[3]);
             if constexpr (TYPE != kF32) {
 #pragma unroll
@@ -331,17 +345,12 @@ __global__ __launch_bounds__(W * 64, 2) void prompt_kernel(PromptArgs a) {
                             out[r][t] = __builtin_amdgcn_mfma_f32_32x32x2f32(row[t * 32 + n], s[r][u][i], out[r][t], 0, 0, 0);
                 }
         } else {
-            products<U * 2 * DT, 2, R>(
-                [&](int i) {
-                    const uint8_t *v = v_lds + v_at[i % DT] + i / DT * 16 * G * 16;
-                    const u32x2 x = read_turned(v), y = read_turned(v + 8 * G * 16);
-                    return u32x4{x[0], x[1], y[0], y[1]};
-                },
-                [&](int i, u32x4 v) {
+            products<U * 2 * DT, 2, R>([&](int i) { return value(v_lds, i); },
+                                       [&](int i, u32x4 v) {
 #pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        out[r][i % DT] = mfma32<TYPE == kF16>(v, p[r][i / DT], out[r][i % DT]);
-                });
+                                           for (int r = 0; r < R; ++r)
+                                               out[r][i % DT] = mfma32<TYPE == kF16>(v, p[r][i / DT], out[r][i % DT]);
+                                       });
         }
     }
 
