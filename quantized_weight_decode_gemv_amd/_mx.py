@@ -7,6 +7,7 @@ that does not is refused with a QwgError."""
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -373,16 +374,18 @@ def prompt_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     sequence, if known; it shapes the launch only. Returns a contiguous tensor of q's shape and type;
     rows of tokens that belong to no sequence are left as they were (in a new tensor: undefined)."""
     _on_device(q, "q")
-    _on_device(k, "k", q.device)
-    _on_device(v, "v", q.device)
-    kind = _type(q.dtype, "q")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    device, dtype = q.device, q.dtype
+    _on_device(k, "k", device)
+    _on_device(v, "v", device)
+    kind = _type(dtype, "q")
+    if k.dtype != dtype or v.dtype != dtype:
         raise ValueError("q, k and v must be of one type")
-    if q.dim() not in (3, 4) or k.dim() != q.dim() or v.shape != k.shape or q.shape[:-2] != k.shape[:-2]:
+    shape, of_k = q.shape, k.shape
+    if len(shape) not in (3, 4) or v.shape != of_k or shape[:-2] != of_k[:-2] or len(of_k) != len(shape):
         raise ValueError("q must be [n_tokens, n_heads, head_dim] and k and v [n_tokens, n_kv_heads, head_dim], "
                          "or [n_seqs, tokens, ...] alike")
-    heads, dim = q.shape[-2:]
-    kv = k.shape[-2]
+    heads, dim = shape[-2:]
+    kv = of_k[-2]
     if dim not in KV8_HEAD_DIMS or kv < 1 or heads < 1 or heads % kv:
         raise ValueError(f"head_dim must be one of {KV8_HEAD_DIMS} and n_heads a multiple of n_kv_heads")
     n, q_stride = _tokens(q, "q", heads, dim)
@@ -390,16 +393,16 @@ def prompt_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if n < 1:
         raise ValueError("a call needs at least one token")
     if starts is None:
-        n_seqs = 1 if q.dim() == 3 else q.shape[0]
+        n_seqs = 1 if len(shape) == 3 else shape[0]
     else:
-        _plain(starts, "starts", _I32, q.device)
+        _plain(starts, "starts", _I32, device)
         if starts.dim() != 1 or starts.shape[0] < 2:
             raise ValueError("starts must be [n_seqs + 1]")
         n_seqs = starts.shape[0] - 1
     if window < 0 or (max_len is not None and max_len < 0):
         raise ValueError("window and max_len must not be negative")
-    out = _out(out, q.shape, q)
-    _run("qwg_prompt_attend", q.device, out.data_ptr(), q.data_ptr(), q_stride, k.data_ptr(),
+    out = _out(out, shape, q)
+    _run("qwg_prompt_attend", device, out.data_ptr(), q.data_ptr(), q_stride, k.data_ptr(),
          k_stride, v.data_ptr(), v_stride, kind, n, None if starts is None else starts.data_ptr(),
          n_seqs, max_len or 0, heads, kv, dim, dim ** -0.5 if scale is None else scale, window)
     return out
@@ -448,6 +451,16 @@ def kv8_attend(q: torch.Tensor, k_pages: torch.Tensor, k_scales: torch.Tensor,
     return out
 
 
+@functools.lru_cache(maxsize=256)
+def _shared_workspace(kind, n_pages, n_kv_heads, head_dim, page_tokens, *sizes) -> int:
+    """Its bytes, by the call's sizes alone (asking the library takes 1.5 us of a call's 14)."""
+    desc = Kv8Desc(1 << 12, 1 << 12, 1 << 12, 1 << 12, n_pages, n_kv_heads, head_dim, page_tokens)
+    size = lib().qwg_kv8_attend_shared_workspace(ctypes.byref(desc), kind, *sizes)
+    if size < 0:
+        _check(-size, "qwg_kv8_attend_shared_workspace")
+    return size
+
+
 def kv8_attend_shared(q: torch.Tensor, k_pages: torch.Tensor, k_scales: torch.Tensor,
                       v_pages: torch.Tensor, v_scales: torch.Tensor, prefix: torch.Tensor,
                       prefix_len: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -468,7 +481,8 @@ def kv8_attend_shared(q: torch.Tensor, k_pages: torch.Tensor, k_scales: torch.Te
     n_seqs, width = _sequences(table, lens, q.device)
     _plain(prefix, "prefix", _I32, q.device)
     _plain(prefix_len, "prefix_len", _I32, q.device)
-    if prefix.dim() != 1 or prefix.numel() < 1 or prefix_len.numel() != 1:
+    pages = prefix.numel()
+    if prefix.dim() != 1 or pages < 1 or prefix_len.numel() != 1:
         raise ValueError("prefix must be [pages] and prefix_len [1]")
     heads, dim = q.shape[-2:] if q.dim() in (3, 4) else (0, 0)
     if dim != cache.head_dim or heads < 1 or heads % cache.n_kv_heads or q.shape[0] != n_seqs:
@@ -480,13 +494,12 @@ def kv8_attend_shared(q: torch.Tensor, k_pages: torch.Tensor, k_scales: torch.Te
         raise ValueError("q_len * n_heads must be in 1..65535")
     out = _out(out, q.shape, q)
     ref = ctypes.byref(cache)
-    size = lib().qwg_kv8_attend_shared_workspace(ref, kind, prefix.numel(), width, n_seqs, q_len, heads)
-    if size < 0:
-        _check(-size, "qwg_kv8_attend_shared_workspace")
+    size = _shared_workspace(kind, cache.n_pages, cache.n_kv_heads, dim, cache.page_tokens, pages,
+                             width, n_seqs, q_len, heads)
     # of this call's stream (or of the graph that captures it): no two calls share one
     space = table.new_empty(size // 4)
     _run("qwg_kv8_attend_shared", q.device, ref, out.data_ptr(), q.data_ptr(), kind, stride,
-         prefix.data_ptr(), prefix.numel(), prefix_len.data_ptr(), table.data_ptr(), width,
+         prefix.data_ptr(), pages, prefix_len.data_ptr(), table.data_ptr(), width,
          lens.data_ptr(), n_seqs, q_len, heads, dim ** -0.5 if scale is None else scale,
          space.data_ptr(), size)
     return out

@@ -252,25 +252,18 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
         __syncthreads();  // (the pages' powers)
         make(begin, 0, 0);
     }
-    // Of eight wavefronts, two to a SIMD, one makes its part of the next block before its products
-    // and one after them, so that they want the matrix cores and the vector units in turn.
-    const bool early = true;
     int buf = 0, slot = L::kWides == 2 ? 1 : 0;
     for (int b0 = begin; b0 < end; b0 += kBlk, slot = slot + 1 == L::kAhead ? 0 : slot + 1) {
         __syncthreads();  // the block is made (of two), and nobody reads the one before any more
         const uint8_t *const k_lds = lds + buf * L::kWide, *const v_lds = k_lds + kTile;
-        const bool more = L::kWides == 2 && b0 + kBlk < end;
         if (L::kWides == 2) {
             buf ^= 1;
-            if (more && early) make(b0 + kBlk, slot, buf);
+            if (b0 + kBlk < end) make(b0 + kBlk, slot, buf);
         } else {
             make(b0, slot, 0);
             __syncthreads();
         }
-        if (row0 >= rows) {
-            if (more && !early) make(b0 + kBlk, slot, buf);
-            continue;
-        }
+        if (row0 >= rows) continue;
         f32x16 s[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -362,7 +355,6 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
 #pragma unroll
                 for (int p = PARTS - 1; p >= 0; --p) out[i % DT] = mfma32<VH>(v, w[i / DT][p], out[i % DT]);
             });
-        if (more && !early) make(b0 + kBlk, slot, buf);
     }
     wait_vmcnt<0>();  // (no DMA outlives its workgroup's LDS)
     __syncthreads();
