@@ -80,7 +80,7 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int64_t at, int t
 // Non-finite values in V where some row of the tile does not see them are set to zero in
 // LDS (0 times infinity is NaN) and added at the end for the rows that do see them.
 template <int TYPE, int D, int W, int R>
-__global__ __launch_bounds__(W * 64, 2) void prompt_kernel(PromptArgs a) {
+__global__ __launch_bounds__(W * 64, (TYPE == kF32 ? D >= 192 : D == 256) ? 1 : 2) void prompt_kernel(PromptArgs a) {
     typedef typename Elem<TYPE>::T T;
     constexpr int B = block_of(TYPE, D);
     constexpr int U = B / 32;                       // score tiles of a block
