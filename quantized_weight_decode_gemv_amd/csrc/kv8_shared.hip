@@ -22,9 +22,6 @@ __device__ __forceinline__ u32x2 widened(uint32_t w) {
                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true))};
 }
 
-// Parts of a query and of a probability: fp32 ones are three bf16s, which hold every bit.
-constexpr int parts_of(int type) { return type == kF32 ? 3 : 1; }
-
 // What a page's positions share: its scale of the scores (log2 e and the call's scale in it; NaN
 // where it is no page of the pool), log2 v as the products take it in and its inverse, what of v
 // that leaves out.
@@ -37,20 +34,21 @@ constexpr int kPowers = 64;
 // (beside a Page, where its head's keys and values begin in the pool: byte, or code, number)
 constexpr int kPrefixPages = kMaxPages * (int)(sizeof(Page) + sizeof(int64_t));
 
-// LDS of a workgroup of W wavefronts: blocks of keys and values in 16 bits (two where they fit, and
-// then one is made while the other is used), blocks on their way from memory, pages, the
-// exponents' range, a flag. Four wavefronts of up to 128 channels leave room for a second workgroup.
-template <int D, int W>
+// Eight wavefronts, a compute unit's registers: rows that share the conversion of what they see. (In
+// fours, two workgroups to a compute unit, 64 sequences behind 32,000 positions, 8 heads of 128,
+// took 58 us for 52.)
+constexpr int kPrefixWaves = 8, kPrefixRows = kPrefixWaves * 32;
+
+// LDS of a workgroup: two blocks of keys and values in 16 bits, of which one is made while the other is
+// used, blocks on their way from memory, the split's pages, the exponents' range, a flag.
+template <int D>
 struct PrefixLds {
     static constexpr int kWide = 2 * kBlk * D * 2;
-    static constexpr int kChunks = (4 * D + W * 64 - 1) / (W * 64);  // 16 bytes of K a thread, and of V
-    static constexpr int kRaw = 2 * kChunks * W * 1024;
-    static constexpr int kRest = (kPrefixPages + 31) & ~15;
-    static constexpr int kBudget = (W == 4 && D <= 128 ? 80 : 160) * 1024 - kRest;
-    static constexpr int kWides = 2 * kWide + 2 * kRaw <= kBudget ? 2 : 1;
-    static constexpr int kAhead = (kBudget - kWides * kWide) / kRaw < 4 ? (kBudget - kWides * kWide) / kRaw : 4;
-    static constexpr int kBytes = kWides * kWide + kAhead * kRaw + kRest;
-    static_assert(kAhead >= 2, "blocks on their way");
+    static constexpr int kChunks = (4 * D + kPrefixWaves * 64 - 1) / (kPrefixWaves * 64);  // 16 bytes of K a thread, and of V
+    static constexpr int kRaw = 2 * kChunks * kPrefixWaves * 1024;
+    static constexpr int kAhead = 4;
+    static constexpr int kBytes = 2 * kWide + kAhead * kRaw + ((kPrefixPages + 31) & ~15);
+    static_assert(kBytes <= 160 * 1024, "LDS");
 };
 
 // One workgroup: one split of the prefix, one key/value head, W x 32 rows; a row is a (token of
@@ -67,17 +65,17 @@ struct PrefixLds {
 // the pages' scales, what it loses by its rounding to fp16 (2^-11 of itself, 2^-25 of the largest) is
 // small against the row's sum, and no product overflows. The softmax's total is the sum of P / v, in fp32.
 // Where a page's v is below 2^-64 of the split's largest, P takes that in the exponent and the
-// rest after the total. fp32: queries and P as three bf16 parts, which lose nothing.
-template <int TYPE, int D, int W>
-__global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
+// rest after the total.
+template <int TYPE, int D>
+__global__ __launch_bounds__(kPrefixWaves * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
     typedef typename Elem<TYPE>::T T;
-    constexpr int PARTS = parts_of(TYPE);
-    constexpr bool KH = TYPE == kF16, VH = TYPE != kF32;  // keys, values and P in fp16, or bf16
+    constexpr int W = kPrefixWaves;
+    constexpr bool KH = TYPE == kF16;        // keys in the queries' type; values and P in fp16
     constexpr int G = D / 8;                 // granules of a row of keys
     constexpr int S = D / 16;                // steps of the first product
     constexpr int DT = D / 32;               // channel tiles
     constexpr int kTile = kBlk * D * 2;      // bytes of a block's keys (or values)
-    typedef PrefixLds<D, W> L;
+    typedef PrefixLds<D> L;
     constexpr int N = L::kChunks;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -95,7 +93,7 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
     if (begin >= end) return;
 
     extern __shared__ __align__(16) uint8_t lds[];
-    uint8_t *const raw = lds + L::kWides * L::kWide;
+    uint8_t *const raw = lds + 2 * L::kWide;
     Page *const pages = (Page *)(raw + L::kAhead * L::kRaw);
     int64_t *const places = (int64_t *)(pages + kMaxPages);
     int *const range = (int *)(places + kMaxPages);  // largest, smallest exponent
@@ -117,7 +115,7 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
     // values sixteen positions (all in one page) of channel f / 4. A thread makes wide what
     // its own lane fetched.
     auto fetch = [&](int b0, int slot) {
-        const uint32_t to = L::kWides * L::kWide + slot * L::kRaw + wave * 1024;
+        const uint32_t to = 2 * L::kWide + slot * L::kRaw + wave * 1024;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             // (every wavefront fetches as much: the waits count)
@@ -148,7 +146,7 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
     const bool live = row0 + n < rows;
     const int token = live ? (row0 + n) / group : 0;
     const int64_t out_row = (int64_t)token * a.n_heads + head * group + (row0 + n) % group;
-    u32x4 q[S][PARTS];
+    u32x4 q[S];
     {
         const T *p = (const T *)a.q + token * a.q_stride + (int64_t)(head * group + (row0 + n) % group) * D;
         const bool vec = ((uintptr_t)a.q | (uintptr_t)a.q_stride * sizeof(T)) % 16 == 0;
@@ -162,14 +160,7 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float v0 = v[s][2 * e] * sign, v1 = v[s][2 * e + 1] * sign;
-                    if constexpr (TYPE == kF32) {
-                        uint32_t h0, m0, l0, h1, m1, l1;
-                        split3(v0, h0, m0, l0);
-                        split3(v1, h1, m1, l1);
-                        q[s][0][e] = h0 | h1 << 16, q[s][1][e] = m0 | m1 << 16, q[s][2][e] = l0 | l1 << 16;
-                    } else {
-                        q[s][0][e] = pack2<KH>(v0, v1);
-                    }
+                    q[s][e] = pack2<KH>(v0, v1);
                 }
         };
         if (vec) load(std::true_type{});
@@ -221,7 +212,7 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
                 }
             }
             const u32x2 k0 = widened<KH>(k[0]), k1 = widened<KH>(k[1]), k2 = widened<KH>(k[2]), k3 = widened<KH>(k[3]);
-            const u32x2 v0 = widened<VH>(v[0]), v1 = widened<VH>(v[1]), v2 = widened<VH>(v[2]), v3 = widened<VH>(v[3]);
+            const u32x2 v0 = widened<true>(v[0]), v1 = widened<true>(v[1]), v2 = widened<true>(v[2]), v3 = widened<true>(v[3]);
             const int kk = row_key<G>(r), vk = row_key<8>(ch);
             *(u32x4 *)(k_lds + (r * G + (gr ^ kk)) * 16) = u32x4{k0[0], k0[1], k1[0], k1[1]};
             *(u32x4 *)(k_lds + (r * G + ((gr + 1) ^ kk)) * 16) = u32x4{k2[0], k2[1], k3[0], k3[1]};
@@ -248,21 +239,14 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // it has been read: its place is free
         fetch(min(b0 + L::kAhead * kBlk, final_block), slot);
     };
-    if (L::kWides == 2) {
-        __syncthreads();  // (the pages' powers)
-        make(begin, 0, 0);
-    }
-    int buf = 0, slot = L::kWides == 2 ? 1 : 0;
+    __syncthreads();  // (the pages' powers)
+    make(begin, 0, 0);
+    int buf = 0, slot = 1;
     for (int b0 = begin; b0 < end; b0 += kBlk, slot = slot + 1 == L::kAhead ? 0 : slot + 1) {
-        __syncthreads();  // the block is made (of two), and nobody reads the one before any more
+        __syncthreads();  // the block is made, and nobody reads the one before any more
         const uint8_t *const k_lds = lds + buf * L::kWide, *const v_lds = k_lds + kTile;
-        if (L::kWides == 2) {
-            buf ^= 1;
-            if (b0 + kBlk < end) make(b0 + kBlk, slot, buf);
-        } else {
-            make(b0, slot, 0);
-            __syncthreads();
-        }
+        buf ^= 1;
+        if (b0 + kBlk < end) make(b0 + kBlk, slot, buf);
         if (row0 >= rows) continue;
         f32x16 s[2];
 #pragma unroll
@@ -273,12 +257,9 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
             const uint8_t *const row = k_lds + n * G * 16;
             const int key = row_key<G>(n);
             // both halves' operands of a step in turn: two chains of sums
-            products<2 * S, 1, PARTS>(
+            products<2 * S, 1, 1>(
                 [&](int i) { return *(const u32x4 *)(row + i % 2 * 32 * G * 16 + ((i / 2 * 2 + g) ^ key) * 16); },
-                [&](int i, u32x4 k) {
-#pragma unroll
-                    for (int p = PARTS - 1; p >= 0; --p) s[i % 2] = mfma32<KH>(k, q[i / 2][p], s[i % 2]);
-                });
+                [&](int i, u32x4 k) { s[i % 2] = mfma32<KH>(k, q[i / 2], s[i % 2]); });
         }
         const bool whole = b0 + kBlk <= by_all;
         const int hi = last - b0 - g * 4;
@@ -334,27 +315,11 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) s[i / 16][i % 16] *= page[i / 8].rest;
         }
-        u32x4 w[4][PARTS];
+        u32x4 w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float p0 = s[j / 2][(j & 1) * 8 + e * 2], p1 = s[j / 2][(j & 1) * 8 + e * 2 + 1];
-                if constexpr (TYPE == kF32) {
-                    w[j][0][e] = upper_halves(p0, p1);
-                    const float r0 = p0 - u2f(w[j][0][e] << 16), r1 = p1 - u2f(w[j][0][e] & 0xffff0000u);
-                    w[j][1][e] = upper_halves(r0, r1);
-                    w[j][2][e] = upper_halves(r0 - u2f(f2u(r0) & 0xffff0000u), r1 - u2f(f2u(r1) & 0xffff0000u));
-                } else {
-                    w[j][0][e] = pack2<VH>(p0, p1);
-                }
-            }
-        products<4 * DT, 1, PARTS>(
-            [&](int i) { return *(const u32x4 *)(v_lds + v_at[i / DT] + i % DT * 32 * 8 * 16); },
-            [&](int i, u32x4 v) {
-#pragma unroll
-                for (int p = PARTS - 1; p >= 0; --p) out[i % DT] = mfma32<VH>(v, w[i / DT][p], out[i % DT]);
-            });
+        for (int i = 0; i < 16; ++i) w[i / 4][i % 4] = pack2<true>(s[i / 8][i % 8 * 2], s[i / 8][i % 8 * 2 + 1]);
+        products<4 * DT, 1, 1>([&](int i) { return *(const u32x4 *)(v_lds + v_at[i / DT] + i % DT * 32 * 8 * 16); },
+                               [&](int i, u32x4 v) { out[i % DT] = mfma32<true>(v, w[i / DT], out[i % DT]); });
     }
     wait_vmcnt<0>();  // (no DMA outlives its workgroup's LDS)
     __syncthreads();
@@ -383,36 +348,32 @@ __global__ __launch_bounds__(W * 64) void kv8_prefix_kernel(Kv8AttendArgs a) {
         }
 }
 
-template <int TYPE, int D, int W>
-hipError_t prefix(const Kv8AttendArgs &a, hipStream_t s) {
-    const int64_t rows = (int64_t)a.q_len * (a.n_heads / a.cache.n_kv), tiles = (rows + W * 32 - 1) / (W * 32);
-    kv8_prefix_kernel<TYPE, D, W>
-        <<<(unsigned)(tiles * a.max_splits * a.cache.n_kv), W * 64, PrefixLds<D, W>::kBytes, s>>>(a);
-    return hipGetLastError();
-}
-
-// Whether eight wavefronts' registers (256 each) hold the queries' parts and the sums.
-constexpr bool eight_fit(int type, int d) { return d * (parts_of(type) + 2) <= 512; }
-
 template <int TYPE, int D>
-hipError_t prefix_rows(const Kv8AttendArgs &a, hipStream_t s) {
-    if constexpr (eight_fit(TYPE, D)) {
-        if (a.row_tiles == 8) return prefix<TYPE, D, 8>(a, s);
-    }
-    return prefix<TYPE, D, 4>(a, s);
+hipError_t prefix(const Kv8AttendArgs &a, hipStream_t s) {
+    const int64_t rows = (int64_t)a.q_len * (a.n_heads / a.cache.n_kv), tiles = (rows + kPrefixRows - 1) / kPrefixRows;
+    kv8_prefix_kernel<TYPE, D><<<(unsigned)(tiles * a.max_splits * a.cache.n_kv), kPrefixWaves * 64,
+                                 PrefixLds<D>::kBytes, s>>>(a);
+    return hipGetLastError();
 }
 
 }  // namespace
 
-// Whether the prefix's pass takes kv8_prefix_kernel, and its splits.
+// Whether the prefix's pass takes kv8_prefix_kernel, and its splits. It does where rows and
+// positions are many, in 16 bits and up to 128 channels, and fill
+// three quarters of its tiles: a workgroup's start and end, and a split's sums
+// on their way through memory, have to be small beside its blocks. Elsewhere attention's own kernel is
+// faster, whose wavefronts share a split's positions and not its rows (4 key/value heads, prefix's
+// and own pass together, us, this and that: 1000 rows of 64 behind 4000 positions 27.6 and 29.7, 256
+// behind 4000 21.9 and 18.4; 256 rows of 128 behind 20,000 42 and 40, with 8 heads behind 32,000 71
+// and 99; 256 rows of 256 behind 20,000 83 and 73; fp32, 1000 rows of 64 behind 4000 35 and 34, of
+// 128 73 and 52).
 bool kv8_prefix_plan(Kv8AttendArgs &a, int type, int cus) {
-    const int64_t rows = (int64_t)a.q_len * (a.n_heads / a.cache.n_kv);
-    if (rows <= 32 || a.cache.dim * parts_of(type) > 384) return false;
-    a.row_tiles = rows > 128 && eight_fit(type, a.cache.dim) ? 8 : 4;  // wavefronts of 32 rows
-    const int64_t groups = a.cache.n_kv * ((rows + a.row_tiles * 32 - 1) / (a.row_tiles * 32));
-    const int64_t slots = a.row_tiles == 8 ? cus : 2 * cus;
-    const int64_t cap = a.width * a.cache.page;
-    int64_t chunk = (cap * groups + slots - 1) / slots;
+    const int64_t rows = (int64_t)a.q_len * (a.n_heads / a.cache.n_kv), cap = a.width * a.cache.page;
+    const int64_t tiles = (rows + kPrefixRows - 1) / kPrefixRows;
+    if (type == kF32 || a.cache.dim > 128 || rows * a.cache.n_kv * cap < 15 << 20 || rows * 4 < tiles * kPrefixRows * 3)
+        return false;
+    // a workgroup to each compute unit
+    int64_t chunk = (cap * a.cache.n_kv * tiles + cus - 1) / cus;
     chunk = std::min<int64_t>(std::max<int64_t>((chunk + kBlk - 1) / kBlk * kBlk, 256), kMaxChunk);
     a.chunk = (int)chunk;
     a.max_splits = (int)((cap + chunk - 1) / chunk);
@@ -420,22 +381,12 @@ bool kv8_prefix_plan(Kv8AttendArgs &a, int type, int cus) {
 }
 
 hipError_t launch_kv8_prefix(const Kv8AttendArgs &a, int type, hipStream_t s) {
-    switch (a.cache.dim * 4 + type) {
-        case 64 * 4 + kF32: return prefix_rows<kF32, 64>(a, s);
-        case 64 * 4 + kF16: return prefix_rows<kF16, 64>(a, s);
-        case 64 * 4 + kBF16: return prefix_rows<kBF16, 64>(a, s);
-        case 96 * 4 + kF32: return prefix_rows<kF32, 96>(a, s);
-        case 96 * 4 + kF16: return prefix_rows<kF16, 96>(a, s);
-        case 96 * 4 + kBF16: return prefix_rows<kBF16, 96>(a, s);
-        case 128 * 4 + kF32: return prefix_rows<kF32, 128>(a, s);
-        case 128 * 4 + kF16: return prefix_rows<kF16, 128>(a, s);
-        case 128 * 4 + kBF16: return prefix_rows<kBF16, 128>(a, s);
-        case 192 * 4 + kF16: return prefix_rows<kF16, 192>(a, s);
-        case 192 * 4 + kBF16: return prefix_rows<kBF16, 192>(a, s);
-        case 256 * 4 + kF16: return prefix_rows<kF16, 256>(a, s);
-        case 256 * 4 + kBF16: return prefix_rows<kBF16, 256>(a, s);
+    const bool half = type == kF16;
+    switch (a.cache.dim) {
+        case 64: return half ? prefix<kF16, 64>(a, s) : prefix<kBF16, 64>(a, s);
+        case 96: return half ? prefix<kF16, 96>(a, s) : prefix<kBF16, 96>(a, s);
+        default: return half ? prefix<kF16, 128>(a, s) : prefix<kBF16, 128>(a, s);
     }
-    return hipErrorInvalidValue;  // (kv8_prefix_plan refuses the others)
 }
 
 }  // namespace qwg

@@ -22,7 +22,7 @@ __device__ __forceinline__ u32x2 read_turned(const uint8_t *p) {
 }
 
 // Positions of a block of keys and values in LDS.
-constexpr int block_of(int type, int d) { return type == kF32 && d > 128 ? 32 : 64; }
+constexpr int block_of(int type, int d) { return type == kF32 && d > 64 ? 32 : 64; }
 
 // The first token of a sequence, its length and which of its tiles the workgroup takes:
 // false past the last tile. Every wavefront looks for itself.

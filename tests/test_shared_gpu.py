@@ -55,6 +55,13 @@ def attend(q, c, prefix, prefix_len, table, lens, **more):
     return qwg.kv8_attend_shared(q, *pages(c), dev(prefix), dev(np.array([prefix_len], np.int32)), dev(table), dev(np.asarray(lens, np.int32)), **more)
 
 
+def wide(prefix, q, c):
+    """The table, with entries that are no pages behind the prefix's, as wide as it takes for many rows to be
+    taken on large tiles (15 * 2^20 rows and positions): the launch goes by what a table may hold."""
+    rows = q.numel() // q.shape[-1]
+    return np.concatenate([prefix, np.full(-(-(15 << 20) // (rows * c.page)), -9, np.int32)])
+
+
 LENS = [0, 1, 2, 15, 16, 17, 64, 130, 3]
 
 
@@ -73,18 +80,33 @@ def test_shared_matches(t, dim, page, kv, group, q_len, prefix):
     assert torch.equal(out, attend(q, c, pre, prefix, table, lens))
 
 
+# (rows per key/value head fill three quarters and more of tiles of 256, or not)
 @pytest.mark.parametrize("t", TYPES)
-@pytest.mark.parametrize("dim,page,kv,group,seqs,prefix", [(64, 16, 1, 8, 40, 5000), (128, 64, 2, 4, 70, 3000), (128, 128, 1, 1, 300, 1500),
-                                                           (96, 32, 1, 3, 50, 2100), (192, 16, 1, 16, 20, 900), (256, 64, 2, 2, 65, 1025)])
-def test_shared_by_many_sequences(t, dim, page, kv, group, seqs, prefix):
+@pytest.mark.parametrize("dim,page,kv,group,seqs,q_len,prefix", [
+    (64, 16, 1, 8, 30, 1, 5000), (128, 64, 2, 4, 60, 1, 3000), (128, 128, 1, 1, 250, 1, 1501), (96, 32, 1, 3, 70, 1, 2100),
+    (64, 64, 1, 16, 31, 1, 700), (96, 16, 2, 2, 50, 2, 300), (128, 32, 1, 3, 33, 5, 64), (64, 128, 1, 5, 40, 1, 999),
+    (192, 16, 1, 16, 20, 1, 900), (256, 64, 2, 2, 65, 1, 1025)])
+def test_shared_by_many_sequences(t, dim, page, kv, group, seqs, q_len, prefix):
     rng = np.random.default_rng(seqs)
-    lens = rng.integers(1, 40, seqs)
+    lens = rng.integers(0, 40, seqs)
     lens[seqs // 2] = 700
     c, pre, table, lens = filled(rng, prefix, lens, kv, dim, page, spread=0.3)
-    q, qd = typed(rng.standard_normal((seqs, kv * group, dim)), t)
-    out = attend(q, c, pre, prefix, table, lens)
-    want = layer_ref.shared(qd[:, None], c, pre, prefix, table, lens, dim ** -0.5)
-    assert_shared(out, *want, t, prefix + 700)
+    q, qd = typed(rng.standard_normal((seqs, q_len, kv * group, dim)), t)
+    want = layer_ref.shared(qd, c, pre, prefix, table, lens, dim ** -0.5)
+    for width in (pre, wide(pre, q, c)):
+        out = attend(q, c, width, prefix, table, lens)
+        assert_shared(out, *want, t, prefix + 700)
+        assert torch.equal(out, attend(q, c, width, prefix, table, lens))
+
+
+@pytest.mark.parametrize("t", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("scale", [0.0, -0.1])
+def test_shared_scales_on_large_tiles(t, scale):
+    rng = np.random.default_rng(31)
+    c, pre, table, lens = filled(rng, 500, [9] * 30, 1, 64, 16, spread=0.3)
+    q, qd = typed(rng.standard_normal((30, 1, 8, 64)), t)
+    out = attend(q, c, wide(pre, q, c), 500, table, lens, scale=scale)
+    assert_shared(out, *layer_ref.shared(qd, c, pre, 500, table, lens, scale), t, 509)
 
 
 @pytest.mark.parametrize("t", TYPES)
@@ -101,81 +123,99 @@ def test_shared_is_attention_over_the_whole(t):
 
 
 @pytest.mark.parametrize("t", TYPES)
-def test_shared_prefixes_of_no_and_of_bad_length(t):
+@pytest.mark.parametrize("times", [1, 10])
+def test_shared_prefixes_of_no_and_of_bad_length(t, times):
     rng = np.random.default_rng(4)
-    c, pre, table, lens = filled(rng, 40, [20, 0, 33, 2], 1, 64, 16)
-    q, qd = typed(rng.standard_normal((4, 3, 2, 64)), t)
+    c, pre, table, lens = filled(rng, 40, [20, 0, 33, 2] * times, 1, 64, 16)
+    q, qd = typed(rng.standard_normal((4 * times, 3, 2, 64)), t)  # (240 rows are taken on a large tile)
+    widths = [pre, wide(pre, q, c)]
     for n in (0, 1, 2, 40):
-        out = attend(q, c, pre, n, table, lens)
         want = layer_ref.shared(qd, c, pre, n, table, lens, 0.125)
-        assert_shared(out, *want, t, 100)
-        if n == 0:
-            assert (out[1] == 0).all() and (out[3, 0] == 0).all()  # rows that see nothing
-    for n in (-1, 16 * len(pre) + 1):
-        assert torch.isnan(attend(q, c, pre, n, table, lens)).all()
-    out = attend(q, c, pre, 40, table, [20, -1, 16 * table.shape[1] + 1, 2])
-    assert torch.isnan(out[1:3]).all()
-    keep = [0, 3]
-    assert_shared(out[keep], *(w if np.ndim(w) == 0 else w[keep] for w in layer_ref.shared(qd, c, pre, 40, table, lens, 0.125)), t, 100)
+        for width in widths:
+            out = attend(q, c, width, n, table, lens)
+            assert_shared(out, *want, t, 100)
+            if n == 0:
+                assert (out[1] == 0).all() and (out[3, 0] == 0).all()  # rows that see nothing
+    for width in widths:
+        for n in (-1, 16 * len(width) + 1):
+            assert torch.isnan(attend(q, c, width, n, table, lens)).all()
+        bad = lens.copy()
+        bad[1:3] = [-1, 16 * table.shape[1] + 1]
+        out = attend(q, c, width, 40, table, bad)
+        assert torch.isnan(out[1:3]).all()
+        keep = [0] + list(range(3, 4 * times))
+        want = layer_ref.shared(qd, c, pre, 40, table, lens, 0.125)
+        assert_shared(out[keep], *(w if np.ndim(w) == 0 else w[keep] for w in want), t, 100)
 
 
 @pytest.mark.parametrize("t", TYPES)
-@pytest.mark.parametrize("seqs", [3, 40])
-def test_shared_bad_pages_and_nan_reach_the_rows_that_see_them(t, seqs):
+@pytest.mark.parametrize("seqs,tiled", [(3, False), (60, False), (60, True)])
+def test_shared_bad_pages_and_nan_reach_the_rows_that_see_them(t, seqs, tiled):
     rng = np.random.default_rng(5)
-    lens = [10] * seqs
-    c, pre, table, lens = filled(rng, 100, lens, 1, 64, 16)
+    c, pre, table, lens = filled(rng, 100, [10] * seqs, 1, 64, 16)
     q, qd = typed(rng.standard_normal((seqs, 2, 2, 64)), t)
+
+    def call(q=q, pre=pre, table=table):
+        return attend(q, c, wide(pre, q, c) if tiled else pre, 100, table, lens)
+
     want = layer_ref.shared(qd, c, pre, 100, table, lens, 0.125)
     bad = table.copy()
     bad[1, 0] = 1 << 20  # one sequence's own page
-    out = attend(q, c, pre, 100, bad, lens)
+    out = call(table=bad)
     assert torch.isnan(out[1]).all()
     keep = [s for s in range(seqs) if s != 1]
     assert_shared(out[keep], *(w if np.ndim(w) == 0 else w[keep] for w in want), t, 110)
     broken = pre.copy()
     broken[2] = -1
-    assert torch.isnan(attend(q, c, broken, 100, table, lens)).all()
+    assert torch.isnan(call(pre=broken)).all()
     # a NaN in the last position of the prefix: the rows of a sequence whose first query stands before it do not see it
     p, slot = pre[99 // 16], 99 % 16
     c.v[p, 0, 7, slot] = 0x7F
     lens[2] = 0  # two queries, none of them own: the first is at position 98, the second at 99
-    out = attend(q, c, pre, 100, table, lens).cpu()
-    nan = torch.isnan(out)
+    nan = torch.isnan(call().cpu())
     assert not nan[2, 0].any() and nan[..., 7].sum() == nan.sum() == 2 * (2 * seqs - 1)
     # NaN codes behind the prefix's end, in the same page, are nobody's
     c.v[p, 0, 7, slot] = 0x30
     c.v[p, 0, :, slot + 1:], c.k[p, 0, slot + 1:] = 0x7F, 0x7F
-    out = attend(q, c, pre, 100, table, lens)
-    assert_shared(out, *layer_ref.shared(qd, c, pre, 100, table, lens, 0.125), t, 110)
+    assert_shared(call(), *layer_ref.shared(qd, c, pre, 100, table, lens, 0.125), t, 110)
     # a NaN in one query
     q[0, 1, 1, 9] = float("nan")
-    out = attend(q, c, pre, 100, table, lens).cpu()
+    out = call().cpu()
     assert torch.isnan(out[0, 1, 1]).all() and torch.isnan(out).sum() == 64
+    # scales that are none
+    q[0, 1, 1, 9] = 0
+    for scales in (c.ks, c.vs):
+        kept, scales[pre[1], 0] = scales[pre[1], 0], 255
+        assert torch.isnan(call()).all()
+        scales[pre[1], 0] = kept
+    assert not torch.isnan(call()).any()
 
 
 @pytest.mark.parametrize("t", TYPES)
-@pytest.mark.parametrize("seqs", [2, 40])
-def test_shared_pages_of_unlike_scales(t, seqs):
+@pytest.mark.parametrize("step", [12, 40])
+@pytest.mark.parametrize("seqs", [2, 100])
+def test_shared_pages_of_unlike_scales(t, step, seqs):
     # pages of V whose scales lie far apart, and a softmax that picks the small ones
     rng = np.random.default_rng(6)
     c, pre, table, lens = filled(rng, 256, [8] * seqs, 1, 64, 16, spread=0)
-    c.vs[pre[:16], 0] = 120 + 12 * (np.arange(16) % 3) - 12  # 2^-19, 2^-7, 2^5 times a code
+    c.vs[pre[:16], 0] = 120 + step * (np.arange(16) % 3 - 1)  # 2^-7 times a code, and far below and above
     at = 35  # (its page has the middle scale)
     q, qd = typed(np.repeat(ref.E4M3[c.k[pre[at // 16], 0, at % 16]][None, None] / 8, seqs, 0).repeat(2, 1), t)
-    out = attend(q, c, pre, 256, table, lens, scale=0.05)
-    assert_shared(out, *layer_ref.shared(qd[:, None], c, pre, 256, table, lens, 0.05), t, 264)
-    for scale in (1.0, 4.0):  # sharper
-        out = attend(q, c, pre, 256, table, lens, scale=scale)
+    for scale in (0.05, 1.0, 4.0, 16.0):  # sharper and sharper
         want, weight, size, _ = layer_ref.shared(qd[:, None], c, pre, 256, table, lens, scale)
-        got = out.cpu().double().numpy().reshape(want.shape)
-        tol = (np.expm1(4 * 42 * 2.0 ** -24 * size) + 2.0 ** -11 + 2.0 ** -15) * weight + torch.finfo(t).eps / 2 * np.abs(want) + 2.0 ** -25
-        assert (np.abs(got - want) <= tol).all()
+        # the weights' errors, those of fp16's smallest against the largest product of a row, and the type's own
+        tol = (np.expm1(4 * 42 * 2.0 ** -24 * size) + 2.0 ** -11 + 2.0 ** -15) * weight + 2.0 ** -24 * 264 * weight.max(-1, keepdims=True)
+        tol = tol + torch.finfo(t).eps / 2 * np.abs(want) + (2.0 ** -25 if t is torch.float16 else 0)
+        for width in (pre, wide(pre, q, c)):
+            got = attend(q, c, width, 256, table, lens, scale=scale).cpu().double().numpy().reshape(want.shape)
+            big = np.abs(want) >= torch.finfo(t).max  # (an fp16 result of the largest scale is infinite)
+            assert (np.abs(got - want)[~big] <= tol[~big]).all() and np.isinf(got[big]).all()
 
 
 def test_shared_graphs_and_streams_do_not_share_a_workspace():
     rng = np.random.default_rng(11)
     c, pre, table, lens = filled(rng, 5000, [300, 1200], 2, 64, 16, spread=0.3)
+    pre = np.concatenate([pre, np.full(100, -7, np.int32)])
     args = *pages(c), dev(pre), dev(np.array([5000], np.int32)), dev(table), dev(lens)
     qs = [typed(rng.standard_normal((2, 8, 64)), torch.bfloat16)[0] for _ in range(3)]
     want = [qwg.kv8_attend_shared(q, *args).clone() for q in qs]
