@@ -670,8 +670,8 @@ int qwg_kv8_attend(const qwg_kv8 *cache, void *out, const void *q, int type, int
  * (a, b) of channels (j, j + rotary_dim/2), or (2j, 2j + 1) where interleaved is not 0,
  * becomes (a cos - b sin, b cos + a sin) of position * freqs[j] radians, freqs [rotary_dim/2]
  * fp32 in device memory; channels past rotary_dim stay. rotary_dim is a multiple of 16
- * up to head_dim. The angle is computed in 64 bits and exact to 2^-52 of itself; q and k
- * are rotated in fp32 and rounded once to `type`, keys on the way to their page
+ * up to head_dim. The angle is computed in 64 bits, to 2^-51 of itself, its sine and cosine to
+ * 2^-45; q and k are rotated in fp32 and rounded once to `type`, keys on the way to their page
  * in 64 bits and rounded once to fp32. q [n_tokens][n_heads][head_dim] -> q_out,
  * tokens q_stride and q_out_stride elements apart; q_out may be q itself with the same
  * stride. k_out: the rotated keys as `type` too, or NULL. Neither may overlap k or v, nor k_out q
@@ -689,10 +689,12 @@ int qwg_kv8_attend(const qwg_kv8 *cache, void *out, const void *q, int type, int
  * n_seqs each); a sequence may be empty, and rows of tokens that belong to none are left as
  * they were. n_tokens * n_heads <= 2^28, n_seqs * n_kv_heads <= 2^22, k_stride and v_stride
  * <= 2^23. Products, sums and softmax are
- * fp32; a probability is rounded to `type` before it meets v. What masked positions and
+ * fp32; a probability is rounded to `type` before it meets v. out may be q itself (q_stride n_heads *
+ * head_dim) and may otherwise share no memory with q, k or v (QWG_ERR_OVERLAP). What masked positions and
  * neighbouring sequences hold (NaN and infinities too) has no effect; a row whose visible
  * scores are all -infinity, or one of them +infinity or NaN, is NaN. max_len is the longest
- * sequence, if known, or 0: it shapes the launch only. No workspace.
+ * sequence, if known, or 0: a hint that no result depends on (the present launch needs none). No
+ * workspace.
  *
  * qwg_kv8_attend_shared: qwg_kv8_attend (without a window) for sequences that begin with
  * the same positions, which are read once for all of them. prefix [prefix_width] holds the
@@ -701,8 +703,10 @@ int qwg_kv8_attend(const qwg_kv8 *cache, void *out, const void *q, int type, int
  * positions behind the prefix (the queries' own among them), the first of which lies in slot
  * 0 of its table's first page. Token t of sequence s is at position prefix_len + lens[s] -
  * q_len + t of the whole and sees it up to there. Every row is NaN where prefix_len is
- * negative or past the prefix's pages; otherwise as qwg_kv8_attend. n_seqs * q_len * n_heads <=
- * 2^20. The parts meet in `workspace` (device, 16-byte aligned,
+ * negative or past the prefix's pages; otherwise as qwg_kv8_attend, out and q as qwg_prompt_attend's.
+ * Products, sums and softmax are fp32. The 16-bit types' probabilities are off by 2^-17 of themselves
+ * at most before they meet v; where rows and the prefix's positions are many, those over the prefix by
+ * 2^-11 and 2^-25 of the row's largest weight v. n_seqs * q_len * n_heads <= 2^20. The parts meet in `workspace` (device, 16-byte aligned,
  * qwg_kv8_attend_shared_workspace bytes for the same arguments, never 0), which is the
  * caller's: calls that may overlap in time need one each.
  */

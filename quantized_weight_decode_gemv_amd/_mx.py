@@ -324,7 +324,7 @@ def kv8_append_rotary(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, freqs: 
     a fused q|k|v result may be given). Token i of sequence s is at position lens[s] + i
     (behind prefix_len others). freqs:
     fp32 [rotary_dim / 2] (rotary_dim a multiple of 16, head_dim at most), radians per position;
-    the angle is exact for every position. Channels (j, j + rotary_dim / 2), or with `interleaved`
+    the angle is computed in 64 bits. Channels (j, j + rotary_dim / 2), or with `interleaved`
     (2j, 2j + 1), turn by position * freqs[j]; those past rotary_dim stay. out: where the queries go
     (q itself may be given), else a new tensor. k_out: a tensor of k's shape that gets the rotated
     keys too (for prompt_attend); it must not overlap q, k or v. prefix_len int32 [1]: positions of a
@@ -355,8 +355,8 @@ def kv8_append_rotary(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, freqs: 
     _run("qwg_kv8_append_rotary", k.device, ctypes.byref(cache), out.data_ptr(), out_stride,
          None if k_out is None else k_out.data_ptr(), k_out_stride, q.data_ptr(), q_stride,
          k.data_ptr(), k_stride, v.data_ptr(), v_stride, kind, heads, freqs.data_ptr(), rotary,
-         int(interleaved), None if prefix_len is None else prefix_len.data_ptr(), n, None if starts is None else starts.data_ptr(), table.data_ptr(), width,
-         lens.data_ptr(), n_seqs, most)
+         int(interleaved), None if prefix_len is None else prefix_len.data_ptr(), n,
+         None if starts is None else starts.data_ptr(), table.data_ptr(), width, lens.data_ptr(), n_seqs, most)
     return out
 
 
@@ -371,8 +371,9 @@ def prompt_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     [n_seqs + 1]: sequence s holds tokens starts[s] .. starts[s+1]-1; without it three-dimensional
     tensors hold one sequence, four-dimensional ones n_seqs. A token sees its sequence up to itself,
     the last `window` positions (0: all). scale defaults to head_dim ** -0.5. max_len: the longest
-    sequence, if known; it shapes the launch only. Returns a contiguous tensor of q's shape and type;
-    rows of tokens that belong to no sequence are left as they were (in a new tensor: undefined)."""
+    sequence, if known: a hint that no result depends on. out: where the result goes (a contiguous q
+    itself may be given, else nothing that shares its memory or k's or v's), else a new tensor. Returns
+    a contiguous tensor of q's shape and type; rows of tokens that belong to no sequence are left as they were (in a new tensor: undefined)."""
     _on_device(q, "q")
     device, dtype = q.device, q.dtype
     _on_device(k, "k", device)
@@ -473,7 +474,7 @@ def kv8_attend_shared(q: torch.Tensor, k_pages: torch.Tensor, k_scales: torch.Te
     positions that they hold (any number: the last page need not be full). table int32 [n_seqs, pages]
     and lens int32 [n_seqs]: each sequence's own pages and positions, the first right behind the
     prefix, the queries' own among them (kv8_append and kv8_append_rotary fill them; the latter's
-    takes prefix_len too). scale defaults to head_dim ** -0.5. Returns a
+    takes prefix_len too). scale defaults to head_dim ** -0.5. out: as prompt_attend's. Returns a
     contiguous tensor of q's shape and type."""
     _on_device(q, "q")
     kind = _type(q.dtype, "q")

@@ -90,6 +90,12 @@ bool may_share(const Rows &a, const Rows &b) {
     return ahead < a.width * a.size || pitch - ahead < b.width * b.size;
 }
 
+// Whether `out` may not be written while `x` is read: x is all of out's rows (in_place: each is read by
+// the one workgroup that writes it, before), or shares none of their memory.
+bool clashes(const Rows &out, const Rows &x, bool in_place) {
+    return may_share(out, x) && !(in_place && out.p == x.p && (out.rows == 1 || out.stride == x.stride));
+}
+
 // Rows of qwg_kv8_attend_shared: the prefix's tiles of 16 then fit the y of a grid.
 constexpr int64_t kMaxSharedRows = 1 << 20;
 
@@ -218,14 +224,13 @@ int qwg_kv8_append_rotary(const qwg_kv8 *cache, void *q_out, int64_t q_out_strid
         !aligned(k_out, size) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(starts, 4) ||
         !aligned(freqs, 4) || !aligned(prefix_len, 4))
         return QWG_ERR_ALIGN;
-    // workgroups read and write in no order: q alone may be turned in place
+    // workgroups read and write in no order
     const Rows rk = {k, n_tokens, width, k_stride, size}, rv = {v, n_tokens, width, v_stride, size};
     const Rows rq = {q, n_tokens, q_width, q_stride, size};
     const Rows oq = {q_out, n_tokens, q_width, q_out_stride, size};
     const Rows ok = {k_out, n_tokens, width, k_out_stride, size};
-    const bool in_place = q_out == q && (n_tokens == 1 || q_out_stride == q_stride);
-    if (may_share(oq, rk) || may_share(oq, rv) || (!in_place && may_share(oq, rq)) ||
-        (k_out && (may_share(ok, rk) || may_share(ok, rv) || may_share(ok, rq) || may_share(ok, oq))))
+    if (clashes(oq, rk, false) || clashes(oq, rv, false) || clashes(oq, rq, true) ||
+        (k_out && (clashes(ok, rk, false) || clashes(ok, rv, false) || clashes(ok, rq, false) || clashes(ok, oq, false))))
         return QWG_ERR_OVERLAP;
     Kv8RotaryArgs a = {};
     static_cast<Kv8AppendArgs &>(a) = {cache_of(cache), k, v, k_stride, v_stride, n_tokens, starts,
@@ -303,6 +308,9 @@ int qwg_kv8_attend_shared(const qwg_kv8 *cache, void *out, const void *q, int ty
         !aligned(prefix_len, 4) || !aligned(table, 4) || !aligned(lens, 4) ||
         !aligned(workspace, 16))
         return QWG_ERR_ALIGN;
+    const int64_t n = n_seqs * q_len, q_width = (int64_t)n_heads * cache->head_dim;
+    const uintptr_t size = size_of(type);
+    if (clashes({out, n, q_width, q_width, size}, {q, n, q_width, q_stride, size}, true)) return QWG_ERR_OVERLAP;
     Kv8SharedArgs a = shared_of(cache, type, prefix_width, table_width, n_seqs, q_len, n_heads);
     if (kv8_shared_partial_bytes(a) > workspace_bytes) return QWG_ERR_SHAPE;
     for (Kv8AttendArgs *p : {&a.prefix, &a.own}) p->q = q, p->out = out, p->q_stride = q_stride, p->scale = scale;
@@ -332,6 +340,10 @@ int qwg_prompt_attend(void *out, const void *q, int64_t q_stride, const void *k,
     if (!aligned(q, size) || !aligned(k, size) || !aligned(v, size) || !aligned(out, size) ||
         !aligned(starts, 4))
         return QWG_ERR_ALIGN;
+    const Rows ro = {out, n_tokens, q_width, q_width, size};
+    if (clashes(ro, {k, n_tokens, width, k_stride, size}, false) || clashes(ro, {v, n_tokens, width, v_stride, size}, false) ||
+        clashes(ro, {q, n_tokens, q_width, q_stride, size}, true))
+        return QWG_ERR_OVERLAP;
     PromptArgs a = {q, k, v, out, q_stride, k_stride, v_stride, starts, n_tokens, n_seqs, window,
                     n_heads, n_kv_heads, head_dim, scale, false};
     if (n_tokens == 1) a.q_stride = q_width, a.k_stride = a.v_stride = width;

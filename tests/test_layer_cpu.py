@@ -14,7 +14,7 @@ ROTARY = dict(q_out=16 * P, q_out_stride=512, k_out=None, k_out_stride=0, q=2 * 
               starts=None, table=P, width=3, lens=P, n_seqs=2, max_new=2, stream=None)
 PROMPT = dict(out=16 * P, q=2 * P, q_stride=512, k=3 * P, k_stride=128, v=4 * P, v_stride=128, type=0, n_tokens=4, starts=None,
               n_seqs=2, max_len=0, n_heads=8, n_kv=2, dim=64, scale=0.1, window=0, stream=None)
-SHARED = dict(out=P, q=P, type=0, q_stride=512, prefix=P, prefix_width=3, prefix_len=P, table=P, width=2, lens=P, n_seqs=2,
+SHARED = dict(out=16 * P, q=2 * P, type=0, q_stride=512, prefix=P, prefix_width=3, prefix_len=P, table=P, width=2, lens=P, n_seqs=2,
               q_len=1, n_heads=8, scale=0.1, workspace=P, bytes=1 << 40, stream=None)
 
 
@@ -42,7 +42,9 @@ def test_rotary_refuses(change, status):
     ({"n_kv": 2048, "n_heads": 2048}, SHAPE), ({"n_heads": 0}, SHAPE), ({"n_seqs": 0}, SHAPE), ({"n_seqs": 3}, SHAPE), ({"n_tokens": 0}, SHAPE),
     ({"n_tokens": 1 << 28, "starts": P}, SHAPE), ({"n_seqs": 1 << 22, "starts": P}, SHAPE), ({"n_tokens": 1 << 62, "starts": P}, SHAPE),
     ({"n_seqs": 1 << 62, "starts": P}, SHAPE), ({"max_len": -1}, SHAPE), ({"window": -1}, SHAPE), ({"q_stride": 511}, SHAPE), ({"k_stride": 127}, SHAPE),
-    ({"v_stride": -128}, SHAPE), ({"q": 2 * P + 2}, ALIGN), ({"out": 16 * P + 2}, ALIGN), ({"starts": P + 2}, ALIGN), ({"v": 4 * P + 1, "type": 2}, ALIGN)])
+    ({"v_stride": -128}, SHAPE), ({"q": 2 * P + 2}, ALIGN), ({"out": 16 * P + 2}, ALIGN), ({"starts": P + 2}, ALIGN), ({"v": 4 * P + 1, "type": 2}, ALIGN),
+    ({"out": 3 * P}, OVERLAP), ({"out": 4 * P}, OVERLAP), ({"out": 3 * P - 4096}, OVERLAP), ({"out": 2 * P + 4}, OVERLAP),
+    ({"out": 2 * P, "q_stride": 768}, OVERLAP), ({"out": 4 * P + 1024}, OVERLAP)])
 def test_prompt_refuses(change, status):
     assert qwg.lib().qwg_prompt_attend(*{**PROMPT, **change}.values()) == status
 
@@ -51,7 +53,8 @@ def test_prompt_refuses(change, status):
     *[({x: None}, NULL) for x in ("out", "q", "prefix", "prefix_len", "table", "lens", "workspace")], ({"type": 7}, TYPE),
     ({"q_stride": 511}, SHAPE), ({"prefix_width": 0}, SHAPE), ({"prefix_width": 1 << 27}, SHAPE), ({"width": 0}, SHAPE), ({"n_seqs": 0}, SHAPE),
     ({"n_seqs": 65536}, SHAPE), ({"n_seqs": 65535, "n_heads": 18}, SHAPE), ({"q_len": 0}, SHAPE), ({"n_heads": 7}, SHAPE), ({"bytes": 15}, SHAPE),
-    ({"workspace": P + 8}, ALIGN), ({"prefix_len": P + 2}, ALIGN), ({"prefix": P + 1}, ALIGN), ({"out": P + 2}, ALIGN)])
+    ({"workspace": P + 8}, ALIGN), ({"prefix_len": P + 2}, ALIGN), ({"prefix": P + 1}, ALIGN), ({"out": P + 2}, ALIGN),
+    ({"out": 2 * P + 4}, OVERLAP), ({"out": 2 * P + 4092}, OVERLAP), ({"out": 2 * P, "q_stride": 600}, OVERLAP)])
 def test_shared_refuses(change, status):
     L, desc = qwg.lib(), Kv8Desc(**CACHE)
     args = {**SHARED, **change}

@@ -179,13 +179,27 @@ def test_prompt_on_other_streams_and_in_graphs(t):
 
 
 def test_prompt_starts_that_are_none():
-    # starts out of order or out of range: no more than the tokens there are is read, and no row is written twice
+    # starts out of order or out of range: no more than the tokens there are is read or written
     rng = np.random.default_rng(12)
     (q, k, v), (qd, kd, vd) = fused(rng, 100, 2, 1, 64, torch.float32)
     out = torch.full(q.shape, 7.0, device=DEV)
     qwg.prompt_attend(q, k, v, starts=dev(np.array([-5, 40, 40, 30, 1000], np.int32)), out=out)
     want = layer_ref.prompt(qd, kd, vd, [0, 40], 0.125)
     assert_prompt(out[:30], *(w[:30] for w in want), torch.float32, 40, np.abs(vd).max())
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("dim", [64, 192])
+def test_prompt_in_place(t, dim):
+    rng = np.random.default_rng(dim)
+    q, k, v = (typed(rng.standard_normal((300, heads, dim)), t)[0] for heads in (6, 2, 2))
+    want = qwg.prompt_attend(q, k, v, window=100)
+    assert qwg.prompt_attend(q, k, v, window=100, out=q) is q and torch.equal(q, want)
+    rows = torch.zeros(301, 2, dim, dtype=t, device=DEV)
+    for bad in (lambda: qwg.prompt_attend(rows[:300], k, v, out=rows[1:]), lambda: qwg.prompt_attend(k, rows[1:], v, out=rows[:300]),
+                lambda: qwg.prompt_attend(k, k, rows[:300], out=rows[:300])):
+        with pytest.raises(qwg.QwgError):
+            bad()
 
 
 def test_prompt_refusals():

@@ -279,6 +279,21 @@ def test_a_prompt_and_answers_to_it(t):
         assert_shared(out, *layer_ref.shared(rd, plain, prefix, n, table, [step + 1] * seqs, dim ** -0.5), t, n + step)
 
 
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("own,tiled", [(30, False), (30, True), (6000, False)])
+def test_shared_in_place(t, own, tiled):
+    rng = np.random.default_rng(own)
+    c, pre, table, lens = filled(rng, 400, [own] * 32, 1, 64, 128)
+    q = typed(rng.standard_normal((32, 2, 4, 64)), t)[0]
+    pre = wide(pre, q, c) if tiled else pre
+    want = attend(q, c, pre, 400, table, lens)
+    args = *pages(c), dev(pre), dev(np.array([400], np.int32)), dev(table), dev(lens)
+    assert qwg.kv8_attend_shared(q, *args, out=q) is q and torch.equal(q, want)
+    rows = torch.zeros(33, 2, 4, 64, dtype=t, device=DEV)
+    with pytest.raises(qwg.QwgError):
+        qwg.kv8_attend_shared(rows[:32], *args, out=rows[1:])
+
+
 def test_shared_refusals():
     cache = qwg.kv8_pages(4, 2, 64, 16, device=DEV)
     table, lens = torch.zeros(2, 2, dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
