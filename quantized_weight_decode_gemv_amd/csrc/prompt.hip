@@ -108,36 +108,6 @@ __global__ __launch_bounds__(W * 64, (TYPE == kF32 ? D >= 192 : D == 256) ? 1 : 
     int *const dirty = (int *)(lds + 4 * kTile);
     if (threadIdx.x == 0) *dirty = 0;
 
-    // queries: the B operand's lane takes row n, eight channels (four of fp32) per half
-    const bool flip = a.scale < 0;  // the maximum is taken before the scale
-    // (never zero: -infinity, of what is masked, has to stay what it is)
-    const float to_log2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 0x1p-126f);
-    u32x4 q[R][G / 2];
-    int token[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int64_t row = wrow0 + r * 32 + n;
-        token[r] = row < rows ? (int)(row / group) : -1;
-        const T *p = (const T *)a.q + (first + max(token[r], 0)) * a.q_stride +
-                     (int64_t)(head * group + (int)(row % group)) * D;
-#pragma unroll
-        for (int s = 0; s < G / 2; ++s) {
-            u32x4 w = {0, 0, 0, 0};
-            if (token[r] >= 0) {
-                if (a.vec) {
-                    w = *(const u32x4 *)(p + (s * 2 + g) * E);
-                } else {
-                    T v[E];
-#pragma unroll
-                    for (int e = 0; e < E; ++e) v[e] = p[(s * 2 + g) * E + e];
-                    __builtin_memcpy(&w, v, 16);
-                }
-            }
-            const uint32_t sign = flip ? (sizeof(T) == 4 ? 0x80000000u : 0x80008000u) : 0u;
-            q[r][s] = w ^ sign;
-        }
-    }
-
     // granule f of a tile in LDS holds granule (f % G) ^ key of row f / G; what thirty-two lanes
     // read of V at once, 32 bytes of each of four rows twice, lies in 256 bytes too
     auto k_key = [](int row) { return row_key<G>(row); };
@@ -182,6 +152,40 @@ __global__ __launch_bounds__(W * 64, (TYPE == kF32 ? D >= 192 : D == 256) ? 1 : 
     auto issue_k = [&](int b0, int buf) { fetch(false, b0, buf * 2 * kTile); };
     auto issue_v = [&](int b0, int buf) { fetch(true, b0, buf * 2 * kTile + kTile); };
 
+    const int low = window > 0 ? max(0, t_lo - window + 1) / B * B : 0;
+    issue_k(low, 0);  // (ahead of the queries: one trip to memory for both)
+    issue_v(low, 0);
+
+    // queries: the B operand's lane takes row n, eight channels (four of fp32) per half
+    const bool flip = a.scale < 0;  // the maximum is taken before the scale
+    // (never zero: -infinity, of what is masked, has to stay what it is)
+    const float to_log2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 0x1p-126f);
+    u32x4 q[R][G / 2];
+    int token[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int64_t row = wrow0 + r * 32 + n;
+        token[r] = row < rows ? (int)(row / group) : -1;
+        const T *p = (const T *)a.q + (first + max(token[r], 0)) * a.q_stride +
+                     (int64_t)(head * group + (int)(row % group)) * D;
+#pragma unroll
+        for (int s = 0; s < G / 2; ++s) {
+            u32x4 w = {0, 0, 0, 0};
+            if (token[r] >= 0) {
+                if (a.vec) {
+                    w = *(const u32x4 *)(p + (s * 2 + g) * E);
+                } else {
+                    T v[E];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[e] = p[(s * 2 + g) * E + e];
+                    __builtin_memcpy(&w, v, 16);
+                }
+            }
+            const uint32_t sign = flip ? (sizeof(T) == 4 ? 0x80000000u : 0x80008000u) : 0u;
+            q[r][s] = w ^ sign;
+        }
+    }
+
     float top[R], sum[R];  // maximum times to_log2, sum of this half lane's probabilities
     f32x16 out[R][DT];
 #pragma unroll
@@ -193,7 +197,6 @@ __global__ __launch_bounds__(W * 64, (TYPE == kF32 ? D >= 192 : D == 256) ? 1 : 
 #pragma unroll
             for (int i = 0; i < 16; ++i) out[r][t][i] = 0;
     }
-    const int low = window > 0 ? max(0, t_lo - window + 1) / B * B : 0;
     // whether every one of the tokens from lo to hi sees the whole block
     auto whole = [&](int b0, int lo, int hi) { return b0 + B - 1 <= lo && (window == 0 || b0 > hi - window); };
 
@@ -299,8 +302,6 @@ __global__ __launch_bounds__(W * 64, (TYPE == kF32 ? D >= 192 : D == 256) ? 1 : 
     auto weight = [&](float s, int r) { return __builtin_amdgcn_exp2f(__builtin_fmaf(s, to_log2, -base[r])); };
 
     f32x16 s[R][U];
-    issue_k(low, 0);
-    issue_v(low, 0);
     int buf = 0;
     for (int b0 = low; b0 <= t_hi; b0 += B, buf ^= 1) {
         wait_vmcnt<0>();
@@ -362,6 +363,7 @@ __global__ __launch_bounds__(W * 64, (TYPE == kF32 ? D >= 192 : D == 256) ? 1 : 
         if (token[r] < 0) continue;
         const int64_t row = wrow0 + r * 32 + n;
         const float inv = 1.0f / total;
+        uint32_t even[2] = {0, 0};
         T *dst = (T *)a.out + ((first + token[r]) * a.n_heads + head * group + (int)(row % group)) * D;
 #pragma unroll
         for (int t = 0; t < DT; ++t)
@@ -384,8 +386,21 @@ __global__ __launch_bounds__(W * 64, (TYPE == kF32 ? D >= 192 : D == 256) ? 1 : 
                         }
                     }
                 }
-                typedef T t4 __attribute__((ext_vector_type(4), aligned(sizeof(T))));
-                *(t4 *)(dst + d) = t4{(T)o[0], (T)o[1], (T)o[2], (T)o[3]};
+                if constexpr (TYPE == kF32) {
+                    typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+                    *(f4 *)(dst + d) = f4{o[0], o[1], o[2], o[3]};
+                } else {
+                    // of two runs of four channels the half lanes take one's eight each: 16 bytes a store
+                    const uint32_t w0 = pack2<TYPE == kF16>(o[0], o[1]), w1 = pack2<TYPE == kF16>(o[2], o[3]);
+                    if (i % 8 == 0) {
+                        even[0] = w0, even[1] = w1;
+                    } else {
+                        const auto x = __builtin_amdgcn_permlane32_swap(even[0], w0, false, false);
+                        const auto y = __builtin_amdgcn_permlane32_swap(even[1], w1, false, false);
+                        typedef uint32_t u4 __attribute__((ext_vector_type(4), aligned(2)));
+                        *(u4 *)(dst + t * 32 + (i - 4) * 2 + g * 8) = u4{x[0], y[0], x[1], y[1]};
+                    }
+                }
             }
     }
 }
