@@ -21,28 +21,34 @@ __device__ __forceinline__ u32x2 read_turned(const uint8_t *p) {
                                          (__attribute__((address_space(3))) s16x4 *)p));
 }
 
-// Positions of a block of keys and values in LDS.
+// Positions of a block of keys and values in LDS. In fp32 two blocks of 64 leave room for one
+// workgroup a compute unit from 96 channels on (4 prompts of 2000 tokens, 16 heads, us with 32 and 64
+// positions: of 64 channels 280 and 220, of 96 302 and 318, of 128 397 and 406; of more, 64 do not fit).
 constexpr int block_of(int type, int d) { return type == kF32 && d > 64 ? 32 : 64; }
 
 // The first token of a sequence, its length and which of its tiles the workgroup takes:
-// false past the last tile. Every wavefront looks for itself.
+// false past the last tile. Every wavefront looks for itself. Equal lengths need no search; of
+// others a lane takes eight sequences at once (where both were searched one to a lane, 32 heads of 128,
+// bf16: 640 prompts of 32 tokens took 169 us, now 112, 300 of up to 60 68 and 63, 21 of up to 900 87 and 89).
 __device__ __forceinline__ bool find_tile(const PromptArgs &a, int64_t at, int tile_rows, int group,
                                           int64_t &first, int &len, int &tile) {
+    if (!a.starts) {
+        const int64_t each = a.n_tokens / a.n_seqs, tiles = (each * group + tile_rows - 1) / tile_rows;
+        const int64_t s = at / tiles;
+        first = s * each, len = (int)each;
+        tile = (int)(tiles - 1 - (at - s * tiles));  // the tiles that see the most come first
+        return s < a.n_seqs;
+    }
     const int lane = threadIdx.x & 63;
-    for (int64_t s0 = 0; s0 < a.n_seqs; s0 += 64) {
-        const int64_t s = s0 + lane;
-        int64_t begin = 0, end = 0;
-        if (s < a.n_seqs) {
-            if (a.starts) {
-                begin = min(max((int64_t)a.starts[s], (int64_t)0), a.n_tokens);
-                end = min(max((int64_t)a.starts[s + 1], begin), a.n_tokens);
-            } else {
-                const int64_t each = a.n_tokens / a.n_seqs;
-                begin = s * each, end = begin + each;
-            }
-        }
-        const int tiles = (int)(((end - begin) * group + tile_rows - 1) / tile_rows);
-        int upto = tiles;
+    constexpr int S = 8;
+    auto tiles_of = [&](int n) { return (int)((uint32_t)(n * group + tile_rows - 1) / (uint32_t)tile_rows); };  // (2^28 rows at most)
+    for (int64_t s0 = 0; s0 < a.n_seqs; s0 += 64 * S) {
+        int edge[S + 1], upto = 0;
+#pragma unroll
+        for (int j = 0; j <= S; ++j)
+            edge[j] = min(max(a.starts[min(s0 + lane * S + j, a.n_seqs)], 0), (int)a.n_tokens);
+#pragma unroll
+        for (int j = 0; j < S; ++j) upto += tiles_of(max(edge[j + 1] - edge[j], 0));
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
             const int v = __shfl_up(upto, o);
@@ -51,12 +57,16 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int64_t at, int t
         const uint64_t past = __ballot(at < upto);
         if (past) {
             const int l = __builtin_ctzll(past);
-            auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
-            first = ((int64_t)of((int)(begin >> 32)) << 32) | (uint32_t)of((int)begin);
-            len = of((int)(end - begin));
-            // the tiles that see the most come first
-            tile = of(upto) - 1 - (int)at;
-            return true;
+            int left = (int)at - (l ? __builtin_amdgcn_readlane(upto, l - 1) : 0);
+#pragma unroll
+            for (int j = 0; j < S; ++j) {
+                first = __builtin_amdgcn_readlane(edge[j], l);
+                len = max(__builtin_amdgcn_readlane(edge[j + 1], l) - (int)first, 0);
+                const int tiles = tiles_of(len);
+                tile = tiles - 1 - left;
+                if (tile >= 0) return true;
+                left -= tiles;
+            }
         }
         at -= __builtin_amdgcn_readlane(upto, 63);
     }
@@ -79,6 +89,16 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int64_t at, int t
 //
 // Non-finite values in V where some row of the tile does not see them are set to zero in
 // LDS (0 times infinity is NaN) and added at the end for the rows that do see them.
+//
+// Bound by the matrix cores and the exponentials between them where prompts are long, at the clock that the
+// card's power leaves: one of 12,000 tokens, 32 heads of 128, bf16: 1170-1230 us, 0.96-1.0 PFLOP/s of
+// what the rows see (a large library product: 1.13); 3 of up to 2500 in fp32, a window of 1000: 395 us.
+// Short ones by a tile's start and end, 10 us of which memory is the larger part (a block costs 1.9
+// more): 21 of up to 900 take 89 us. One of 77 tokens takes 7.7: the launch and two trips to memory.
+// Of 256 channels, and in fp32 of 192, one wavefront to a SIMD: with two the sums spill (4 x 2000, 16
+// heads of 256: bf16 316 us for 137, fp32 1815 for 816). Eight wavefronts, 64 rows to a wavefront, scores of
+// the next block ahead of this one's exponentials, results by way of LDS (21 x 900: 95 us for 87)
+// and non-temporal ones (111 for 106, wall) were no faster.
 template <int TYPE, int D, int W, int R>
 __global__ __launch_bounds__(W * 64, (TYPE == kF32 ? D >= 192 : D == 256) ? 1 : 2) void prompt_kernel(PromptArgs a) {
     typedef typename Elem<TYPE>::T T;
@@ -96,6 +116,10 @@ __global__ __launch_bounds__(W * 64, (TYPE == kF32 ? D >= 192 : D == 256) ? 1 : 
     int64_t first;
     int len, tile;
     if (!find_tile(a, blockIdx.x / a.n_kv, W * R * 32, group, first, len, tile)) return;
+    // (as scalars: left to itself the compiler keeps some of what follows from them in vector registers, and
+    // 5 prompts of up to 4000 take 503 us for 483)
+    first = __builtin_amdgcn_readfirstlane((int)first);
+    len = __builtin_amdgcn_readfirstlane(len), tile = __builtin_amdgcn_readfirstlane(tile);
     const int64_t rows = (int64_t)len * group;
     const int64_t row0 = (int64_t)tile * (W * R * 32), wrow0 = row0 + wave * R * 32;
     // tokens of the workgroup's rows and of the wavefront's

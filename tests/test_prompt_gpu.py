@@ -188,6 +188,29 @@ def test_prompt_starts_that_are_none():
     assert_prompt(out[:30], *(w[:30] for w in want), torch.float32, 40, np.abs(vd).max())
 
 
+@pytest.mark.parametrize("long", [0, 7, 8, 511, 512, 1023, 1301])
+def test_prompt_among_many_sequences(long):
+    # short and empty ones, one of several tiles, the last ones empty
+    rng = np.random.default_rng(long)
+    lens = rng.integers(0, 3, 1400)
+    lens[1310:], lens[long] = 0, 150
+    starts = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    n = int(starts[-1])
+    (q, k, v), (qd, kd, vd) = fused(rng, n, 2, 1, 64, torch.float16)
+    out = qwg.prompt_attend(q, k, v, starts=dev(starts))
+    assert_prompt(out, *layer_ref.prompt(qd, kd, vd, starts, 0.125), torch.float16, 150, np.abs(vd).max())
+
+
+@pytest.mark.parametrize("seqs,each", [(700, 1), (70, 65), (3, 130), (1, 33)])
+def test_prompt_of_equal_lengths(seqs, each):
+    rng = np.random.default_rng(seqs)
+    (q, k, v), (qd, kd, vd) = fused(rng, seqs * each, 6, 2, 64, torch.bfloat16)
+    parts = (x.unflatten(0, (seqs, each)) for x in (q, k, v))
+    out = qwg.prompt_attend(*parts)
+    want = layer_ref.prompt(qd, kd, vd, np.arange(seqs + 1) * each, 0.125)
+    assert_prompt(out.flatten(0, 1), *want, torch.bfloat16, each, np.abs(vd).max())
+
+
 @pytest.mark.parametrize("t", TYPES)
 @pytest.mark.parametrize("dim", [64, 192])
 def test_prompt_in_place(t, dim):
