@@ -96,9 +96,9 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int64_t at, int t
 // Short ones by a tile's start and end, 10 us of which memory is the larger part (a block costs 1.9
 // more): 21 of up to 900 take 89 us. One of 77 tokens takes 7.7: the launch and two trips to memory.
 // Of 256 channels, and in fp32 of 192, one wavefront to a SIMD: with two the sums spill (4 x 2000, 16
-// heads of 256: bf16 316 us for 137, fp32 1815 for 816). Eight wavefronts, 64 rows to a wavefront, scores of
-// the next block ahead of this one's exponentials, results by way of LDS (21 x 900: 95 us for 87)
-// and non-temporal ones (111 for 106, wall) were no faster.
+// heads of 256: bf16 316 us for 137, fp32 1815 for 816). The scores of the
+// next block ahead of this one's exponentials, wavefronts set out of step, results by way of LDS
+// (21 x 900: 95 us for 87) and non-temporal ones (in a loop of calls 111 for 105) were no faster.
 template <int TYPE, int D, int W, int R>
 __global__ __launch_bounds__(W * 64, (TYPE == kF32 ? D >= 192 : D == 256) ? 1 : 2) void prompt_kernel(PromptArgs a) {
     typedef typename Elem<TYPE>::T T;
