@@ -489,19 +489,25 @@ __global__ __launch_bounds__(W * 64) void kv8_attend_kernel(Kv8AttendArgs a) {
         const int64_t rows_all = all * a.n_seqs, each = partial_floats(rows_all, D);
         auto of_all = [&](int row) { return (row_base + row / group) * a.n_heads + head * group + row % group; };
         {
-            constexpr int L = W * 64 / (R * 16);  // lanes that take one row's parts in turn
+            // lanes that take one row's parts in turn: a power of two, for the exchanges below
+            // (three wavefronts and two row tiles leave a third of the lanes without a row)
+            constexpr int share = W * 64 / (R * 16), L = 1 << (31 - __builtin_clz(share));
+            static_assert(L >= W && L <= 64, "a lane per wavefront, in one wavefront");
             const int lr = threadIdx.x / L, l = threadIdx.x % L, row = row0 + lr;
-            const float *ml = a.prefix_partial + rows_all * D + (row < rows ? of_all(row) : 0) * 2;
-            float m = l < W ? sm[(l * R * 16 + lr) * 2] : -__builtin_inff();
-            for (int s = l; s < parts; s += L) m = fmaxf(m, ml[s * each]);
+            const bool mine = lr < R * 16;
+            const bool here = mine && l < W;  // takes a wavefront's own sums
+            const int n_mine = mine ? parts : 0, own = here ? (l * R * 16 + lr) * 2 : 0;
+            const float *ml = a.prefix_partial + rows_all * D + (mine && row < rows ? of_all(row) : 0) * 2;
+            float m = here ? sm[own] : -__builtin_inff();
+            for (int s = l; s < n_mine; s += L) m = fmaxf(m, ml[s * each]);
 #pragma unroll
             for (int o = 1; o < L; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
             m = m == -__builtin_inff() ? 0.0f : m;
-            float t = l < W ? __builtin_amdgcn_exp2f(sm[(l * R * 16 + lr) * 2] - m) * sm[(l * R * 16 + lr) * 2 + 1] : 0.0f;
-            for (int s = l; s < parts; s += L) t += __builtin_amdgcn_exp2f(ml[s * each] - m) * ml[s * each + 1];
+            float t = here ? __builtin_amdgcn_exp2f(sm[own] - m) * sm[own + 1] : 0.0f;
+            for (int s = l; s < n_mine; s += L) t += __builtin_amdgcn_exp2f(ml[s * each] - m) * ml[s * each + 1];
 #pragma unroll
             for (int o = 1; o < L; o <<= 1) t += __shfl_xor(t, o);
-            if (l == 0) meet[lr * 2] = m, meet[lr * 2 + 1] = t;
+            if (mine && l == 0) meet[lr * 2] = m, meet[lr * 2 + 1] = t;
         }
         __syncthreads();
         for (int i = threadIdx.x; i < R * 16 * (D / 4); i += W * 64) {
