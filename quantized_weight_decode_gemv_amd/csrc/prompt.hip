@@ -182,8 +182,9 @@ __global__ __launch_bounds__(W * 64, (TYPE == kF32 ? D >= 192 : D == 256) ? 1 : 
 
     // queries: the B operand's lane takes row n, eight channels (four of fp32) per half
     const bool flip = a.scale < 0;  // the maximum is taken before the scale
-    // (never zero: -infinity, of what is masked, has to stay what it is; a NaN stays one)
-    const float to_log2 = __builtin_elementwise_maximum(fabsf(a.scale) * 1.4426950408889634f, 0x1p-126f);
+    // (never zero: -infinity, of what is masked, has to stay what it is; the smallest number moves no
+    // score by more than 2^-21; a NaN stays one)
+    const float to_log2 = __builtin_elementwise_maximum(fabsf(a.scale) * 1.4426950408889634f, 0x1p-149f);
     u32x4 q[R][G / 2];
     int token[R];
 #pragma unroll
