@@ -330,7 +330,7 @@ int qwg_prompt_attend(void *out, const void *q, int64_t q_stride, const void *k,
         n_heads > 65535 || n_heads % n_kv_heads)
         return QWG_ERR_SHAPE;
     const int64_t width = (int64_t)n_kv_heads * head_dim, q_width = (int64_t)n_heads * head_dim;
-    if (n_seqs < 1 || n_seqs * n_kv_heads > kMaxPromptPairs || n_seqs > kMaxPromptPairs ||
+    if (n_seqs < 1 || n_seqs > kMaxPromptPairs || n_seqs * n_kv_heads > kMaxPromptPairs ||
         n_tokens < 1 || n_tokens > kMaxPromptRows || n_tokens * n_heads > kMaxPromptRows ||
         max_len < 0 || window < 0 || (!starts && n_tokens % n_seqs) ||
         (n_tokens > 1 && (q_stride < q_width || k_stride < width || v_stride < width ||
