@@ -692,7 +692,7 @@ int qwg_kv8_attend(const qwg_kv8 *cache, void *out, const void *q, int type, int
  * fp32; a probability is rounded to `type` before it meets v. out may be q itself (q_stride n_heads *
  * head_dim) and may otherwise share no memory with q, k or v (QWG_ERR_OVERLAP). What masked positions and
  * neighbouring sequences hold (NaN and infinities too) has no effect; a row whose visible
- * scores are all -infinity, or one of them +infinity or NaN, is NaN. max_len is the longest
+ * scores are all -infinity, or one of them +infinity or NaN, is NaN, and under a scale that is NaN all are. max_len is the longest
  * sequence, if known, or 0: a hint that no result depends on (the present launch needs none). No
  * workspace.
  *
@@ -705,8 +705,10 @@ int qwg_kv8_attend(const qwg_kv8 *cache, void *out, const void *q, int type, int
  * q_len + t of the whole and sees it up to there. Every row is NaN where prefix_len is
  * negative or past the prefix's pages; otherwise as qwg_kv8_attend, out and q as qwg_prompt_attend's.
  * Products, sums and softmax are fp32. The 16-bit types' probabilities are off by 2^-17 of themselves
- * at most before they meet v; where rows and the prefix's positions are many, those over the prefix by
- * 2^-11 and 2^-25 of the row's largest weight v. n_seqs * q_len * n_heads <= 2^20. The parts meet in `workspace` (device, 16-byte aligned,
+ * at most before they meet v; up to 128 channels, where the rows and the positions that prefix_width pages
+ * may hold are many (15 * 2^20 rows times positions and more), those over the prefix by 2^-11 and 2^-25 of
+ * the row's largest weight v. Launch and workspace go by prefix_width and table_width: a prefix and a table
+ * cut to what they hold are the faster ones. n_seqs * q_len * n_heads <= 2^20. The parts meet in `workspace` (device, 16-byte aligned,
  * qwg_kv8_attend_shared_workspace bytes for the same arguments, never 0), which is the
  * caller's: calls that may overlap in time need one each.
  */

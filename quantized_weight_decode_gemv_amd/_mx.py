@@ -371,7 +371,7 @@ def prompt_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     [n_seqs + 1]: sequence s holds tokens starts[s] .. starts[s+1]-1; without it three-dimensional
     tensors hold one sequence, four-dimensional ones n_seqs. A token sees its sequence up to itself,
     the last `window` positions (0: all). scale defaults to head_dim ** -0.5. max_len: the longest
-    sequence, if known: a hint that no result depends on. out: where the result goes (a contiguous q
+    sequence, if known: a hint that no result depends on, and that the present launch needs none of. out: where the result goes (a contiguous q
     itself may be given, else nothing that shares its memory or k's or v's), else a new tensor. Returns
     a contiguous tensor of q's shape and type; rows of tokens that belong to no sequence are left as they were (in a new tensor: undefined)."""
     _on_device(q, "q")
@@ -474,8 +474,9 @@ def kv8_attend_shared(q: torch.Tensor, k_pages: torch.Tensor, k_scales: torch.Te
     positions that they hold (any number: the last page need not be full). table int32 [n_seqs, pages]
     and lens int32 [n_seqs]: each sequence's own pages and positions, the first right behind the
     prefix, the queries' own among them (kv8_append and kv8_append_rotary fill them; the latter's
-    takes prefix_len too). scale defaults to head_dim ** -0.5. out: as prompt_attend's. Returns a
-    contiguous tensor of q's shape and type."""
+    takes prefix_len too). scale defaults to head_dim ** -0.5. out: as prompt_attend's. A prefix and a
+    table cut to what they hold are faster than ones that are much wider, and take a smaller workspace.
+    Returns a contiguous tensor of q's shape and type."""
     _on_device(q, "q")
     kind = _type(q.dtype, "q")
     cache = _cache(k_pages, k_scales, v_pages, v_scales, q.device)

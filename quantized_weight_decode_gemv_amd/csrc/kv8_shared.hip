@@ -362,14 +362,19 @@ hipError_t prefix(const Kv8AttendArgs &a, hipStream_t s) {
 }  // namespace
 
 // Whether the prefix's pass takes kv8_prefix_kernel, and its splits. It does in 16 bits, up to 128
-// channels, where rows and positions are many and fill three quarters of its tiles: a workgroup's
+// channels, where rows and the positions that the prefix's pages may hold are many: a workgroup's
 // start and end, and a split's sums on their way through memory, have to be small beside its blocks.
-// Elsewhere attention's own kernel is faster, whose wavefronts share a split's positions and not its
-// rows (4 key/value heads, prefix's
-// and own pass together, us, this and that: 1000 rows of 64 behind 4000 positions 27.6 and 29.7, 256
-// behind 4000 21.9 and 18.4; 256 rows of 128 behind 20,000 42 and 40, with 8 heads behind 32,000 71
-// and 99; 256 rows of 256 behind 20,000 83 and 73; fp32, 1000 rows of 64 behind 4000 35 and 34, of
-// 128 73 and 52).
+// Elsewhere attention's own kernel, whose wavefronts share a split's positions and not its rows, takes
+// less (prefix's and own pass together, us, this and that: 256 rows of 256 channels, 4 key/value heads
+// behind 20,000 positions, 83 and 73; fp32, 1000 rows of 64 behind 4000 35 and 34, of 128 73 and 52).
+// Where the kernels cross (rows x heads x positions in 2^20, the switch being at 15): 256 rows, 8 heads
+// of 128 behind 6000 (12) 34.0 and 31.7, behind 10,000 (20) 40.0 and 39.4, behind 16,000 (31) 46 and 51;
+// 1000 rows of these behind 1500 (12) 53 and 51, 1920 (15) 51.7 and 54.2, 3000 (23) 56 and 63; of 4 heads
+// of 64 behind 2000 (8) 24.6 and 24.6, 3900 (15) 27.4 and 30.9; 256 rows, 2 heads of 128 behind 30,000
+// (15) 43.5 and 41.0: within 13% of the better one.
+// The rows also have to fill three quarters of the tiles, which keeps the kernel from rows that it
+// would be faster for: 260 to 380 rows, 8 heads of 128 behind 32,000 85-88 and 123-126, 520 143 and 203,
+// 128 49 and 54; 320 rows, 4 heads of 64 behind 16,000 34 and 41, 264 34.0 and 34.7.
 bool kv8_prefix_plan(Kv8AttendArgs &a, int type, int cus) {
     const int64_t rows = (int64_t)a.q_len * (a.n_heads / a.cache.n_kv), cap = a.width * a.cache.page;
     const int64_t tiles = (rows + kPrefixRows - 1) / kPrefixRows;

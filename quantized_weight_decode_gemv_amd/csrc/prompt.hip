@@ -92,11 +92,14 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int64_t at, int t
 //
 // Bound by the matrix cores and the exponentials between them where prompts are long, at the clock that the
 // card's power leaves: one of 12,000 tokens, 32 heads of 128, bf16: 1170-1230 us, 0.96-1.0 PFLOP/s of
-// what the rows see (a large library product: 1.13); 3 of up to 2500 in fp32, a window of 1000: 395 us.
+// what the rows see (a large library product: 1.13); the matrix cores are busy for half of the cycles.
+// 3 of up to 2500 in fp32, a window of 1000: 376-400 us, the matrix cores busy for 80% of the compute units'
+// cycles, 6% of them with positions that no row sees.
 // Short ones by a tile's start and end, 10 us of which memory is the larger part (a block costs 1.9
 // more): 21 of up to 900 take 89 us. One of 77 tokens takes 7.7: the launch and two trips to memory.
 // Of 256 channels, and in fp32 of 192, one wavefront to a SIMD: with two the sums spill (4 x 2000, 16
-// heads of 256: bf16 316 us for 137, fp32 1815 for 816). The scores of the
+// heads of 256: bf16 316 us for 137, fp32 1815 for 816). Of 192 in 16 bits two spill as well, 20 bytes a
+// lane (4 x 2000, 16 heads: bf16 160 us, 155 with one; one of 6000, 32 heads: 543 and 535). The scores of the
 // next block ahead of this one's exponentials, wavefronts set out of step, results by way of LDS
 // (21 x 900: 95 us for 87) and non-temporal ones (in a loop of calls 111 for 105) were no faster.
 template <int TYPE, int D, int W, int R>
